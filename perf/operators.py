@@ -68,7 +68,8 @@ def draw(rng):
         return {"op": op, "tokens": _log(rng, 1, 4096), "q_heads": heads[0], "kv_heads": heads[1],
                 "head_dim": heads[2], "rotary": rng.choice([heads[2], heads[2] // 2]), "page": page}
     if op == "norm":
-        return {"op": op, "tokens": _log(rng, 1, 2048), "width": 128 * _log(rng, 4, 64),
+        width = 128 * _log(rng, 4, 64)
+        return {"op": op, "tokens": _log(rng, 1, min(2048, 7000000 // width)), "width": width,
                 "post": rng.random() < 0.5, "gate": rng.choice(["none", "channel", "token"]),
                 "residual": rng.choice(["float16", "float32"]), "quantize": rng.random() < 0.5}
     if rng.random() < 0.7:  # decode and checks of a few proposed tokens
