@@ -56,9 +56,11 @@ typedef enum {
     MIXLLM_ERR_UNSUPPORTED = 2, /* group != 128, K % 128 != 0, no sm_100a  */
     MIXLLM_ERR_CUDA = 3,        /* a CUDA runtime call failed              */
     MIXLLM_ERR_TIMEOUT = 4,     /* a device-side wait gave up              */
-    MIXLLM_ERR_BOUNDS = 5       /* checked build: a kernel's range check of
-                                   a tensor- or shared-memory access failed
-                                   (the access was skipped)                */
+    MIXLLM_ERR_BOUNDS = 5       /* a KV-cache kernel met a page, slot,
+                                   position or length out of range; checked
+                                   build: a range check of a tensor- or
+                                   shared-memory access failed (in each case
+                                   the access was skipped)                 */
 } mixllm_status;
 
 #define MIXLLM_GROUP 128
@@ -464,10 +466,190 @@ MIXLLM_API mixllm_status mixllm_select_top_t(const float *S, int64_t n, int64_t 
                                              size_t workspace_bytes, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Between the linears of a decoder layer: the residual norms and the attention
+ * over a paged KV cache held in 4 bits.  They produce and consume what the
+ * linears do: fp16 activations, and int8 codes with a scale per 128.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * X = fp16(A_q * s_a), the activations as the GEMM sees them (the inverse of
+ * mixllm_quantize_act up to its rounding).
+ *   A_q    device, int8 [M, K] row-major, 8-byte aligned, read only
+ *   s_a    device, fp32 [M, K/128], read only
+ *   X_f16  device, fp16 [M, K], 16-byte aligned, written
+ * M = 0 is a no-op.  Asynchronous on `stream`.
+ */
+MIXLLM_API mixllm_status mixllm_dequantize_act(const int8_t *A_q, const float *s_a, int64_t M, int64_t K,
+                                               int32_t group, void *X_f16, void *stream);
+
+/*
+ * The norms around a block, one kernel.  Per token (all sums in fp32):
+ *   u  = x                                     (w_post NULL)
+ *      = x * rsqrt(mean(x^2) + eps) * w_post   (the norm after the block)
+ *   r' = r + scale * gate * u                  (rounded to r's type; gate NULL: 1)
+ *   y  = r' * rsqrt(mean(r'^2) + eps) * w      (rounded to fp16; from the rounded r')
+ * and, when A_q is given, the codes and scales of y, bit for bit those of
+ * mixllm_quantize_act(y).  With x NULL the residual is left alone: r' = r.
+ *   r        device, fp16 (r_is_f32 = 0) or fp32 [M, K], rows r_stride elements apart
+ *   x_f16    device, fp16 [M, K], rows x_stride apart, or NULL
+ *   w_post   device, fp16 [K], or NULL
+ *   gate     device, fp16 [M, K], rows gate_stride apart (0: one row for every token), or NULL
+ *   r_out    device, r's type [M, K], rows r_out_stride apart; NULL: r' is not kept.  May be r.
+ *   w_f16    device, fp16 [K]
+ *   y_f16    device, fp16 [M, K] contiguous, or NULL.  May be x when x is contiguous.
+ *   A_q, s_a device, int8 [M, K] and fp32 [M, K/128] contiguous, or both NULL;
+ *            y or A_q must be given
+ * Outputs overlap no input except as said.  Every buffer 16-byte aligned (A_q
+ * 8, s_a 4), row strides multiples of 16 bytes.  K a multiple of 128 up to
+ * 32768; M = 0 is a no-op.  Asynchronous on `stream`.
+ */
+MIXLLM_API mixllm_status mixllm_residual_norm(const void *r, int64_t r_stride, int32_t r_is_f32, const void *x_f16,
+                                              int64_t x_stride, const void *w_post_f16, const void *gate_f16,
+                                              int64_t gate_stride, float scale, void *r_out, int64_t r_out_stride,
+                                              const void *w_f16, float eps, int64_t M, int64_t K, void *y_f16,
+                                              int8_t *A_q, float *s_a, void *stream);
+
+/*
+ * The paged 4-bit KV cache.  Two buffers of `pages` pages of page_size tokens
+ * (16, 32, 64, 128 or 256), H = kv_heads, D = head_dim (64 or 128):
+ *   codes  uint8  [pages, 2, H, page_size, D/2]  keys then values; byte i of a
+ *          row holds the code of channel 2i (low nibble) and 2i + 1 (high)
+ *   meta   uint32 [pages, 2, H, page_size]       low half: the row's fp16 scale
+ *          s; bits 16..19: its zero point z
+ * both 16-byte aligned; a row's values are s * (code - z).  A row (one token,
+ * head, key or value) is quantized like the weights' 4-bit set:
+ *   lo = min(0, min x), hi = max(0, max x), s = fp16((hi - lo) / 15),
+ *   z = clamp(rne(-lo/s), 0, 15), code = clamp(rne(x/s) + z, 0, 15);
+ *   s = 0 gives z = code = 0.
+ * A row with a NaN or an infinity is stored with s = NaN and z = code = 0.
+ * A token's place is its slot: page * page_size + row.
+ *
+ * What the host cannot see is checked on the device: a page, slot, position or
+ * length outside its range is skipped (the tokens of a bad page count as not
+ * seen, a bad slot or position writes nothing, a request with bad lengths
+ * gets no output) and recorded: mixllm_sync_status() then returns
+ * MIXLLM_ERR_BOUNDS.
+ */
+
+/*
+ * Pages and slots for one step's new tokens.  Request b holds ctx_lens[b]
+ * cached tokens in the first ceil(ctx/page_size) entries of its row of
+ * block_table and gets new_lens[b] more.  Each page it lacks is popped from the
+ * stack free_pages[0 .. *free_count) and entered in its row; requests take
+ * theirs in order, each its first page first, from the top of the stack.
+ *   seq_lens  int32 [requests]      ctx + new; may be ctx_lens
+ *   cu_new    int32 [requests + 1]  exclusive sum of new_lens, and the total
+ *   slots     int64 [n_slots], positions int32 [n_slots]
+ *             slot and position (ctx .. ctx + new - 1) of every new token,
+ *             requests one after the other; -1 behind the last one
+ *   free_left int32 [1]  pages left on the stack; may be free_count
+ *   status    int32 [1]  0, or the sum of: 1 too few free pages (or
+ *             *free_count beyond n_free), 2 a request would need more than
+ *             table_width pages, 4 more than n_slots new tokens, 8 a negative
+ *             length.  Then nothing is assigned: the table stays, seq_lens =
+ *             ctx_lens, cu_new = 0, slots and positions = -1, free_left =
+ *             *free_count.
+ * All device buffers; rows of block_table int32 [requests, table_width] are
+ * table_stride apart.  At most 16384 requests; their number may be 0.
+ * Asynchronous on `stream`.
+ */
+MIXLLM_API mixllm_status mixllm_kv4_assign(const int32_t *ctx_lens, const int32_t *new_lens, int64_t requests,
+                                           int32_t *block_table, int64_t table_stride, int64_t table_width,
+                                           const int32_t *free_pages, int64_t n_free, const int32_t *free_count,
+                                           int32_t page_size, int32_t *seq_lens, int32_t *cu_new, int64_t *slots,
+                                           int32_t *positions, int64_t n_slots, int32_t *free_left, int32_t *status,
+                                           void *stream);
+
+/*
+ * Writes the keys and values of n_slots tokens into their slots and, on the
+ * way, rotates keys and queries (one kernel).
+ *   slots     device int64 [n_slots], distinct; a negative one skips the token
+ *             (its q_out row too)
+ *   k, v      device fp16, token t's heads contiguous at t * stride
+ *             ([n_slots, kv_heads, head_dim]; e.g. slices of one qkv output)
+ *   q, q_out  device fp16 [n_slots, q_heads, head_dim] likewise; q_heads = 0:
+ *             none (both NULL).  q_out may be q.
+ *   rope      device fp32 [max_pos, rotary]: row p holds the rotary/2 cosines
+ *             and then the rotary/2 sines of position p; with
+ *   positions device int32 [n_slots], channels i and i + rotary/2 of every
+ *             query and key head become
+ *               x_i cos_i - x_j sin_i,  x_j cos_i + x_i sin_i  (j = i + rotary/2)
+ *             in fp32 (each product and sum rounded) and are rounded to fp16.
+ *             rotary = 0: no rotation (both NULL); else a multiple of 16 up to
+ *             head_dim.
+ * k, v, q, q_out, rope 16-byte aligned, strides (in elements) multiples of 8.
+ * n_slots = 0 is a no-op.  Asynchronous on `stream`.
+ */
+MIXLLM_API mixllm_status mixllm_kv4_append(uint8_t *codes, uint32_t *meta, int64_t pages, int32_t kv_heads,
+                                           int32_t head_dim, int32_t page_size, const int64_t *slots,
+                                           int64_t n_slots, const void *k_f16, int64_t k_stride, const void *v_f16,
+                                           int64_t v_stride, const void *q_f16, int64_t q_stride, int32_t q_heads,
+                                           void *q_out_f16, int64_t q_out_stride, const int32_t *positions,
+                                           const float *rope, int64_t max_pos, int32_t rotary, void *stream);
+
+/*
+ * The cached keys and values of n_slots slots as fp16 [n_slots, kv_heads,
+ * head_dim] each, contiguous and 16-byte aligned: s * (code - z) rounded once,
+ * within +-65504.  A negative slot leaves its rows as they were.
+ * Asynchronous on `stream`.
+ */
+MIXLLM_API mixllm_status mixllm_kv4_read(const uint8_t *codes, const uint32_t *meta, int64_t pages, int32_t kv_heads,
+                                         int32_t head_dim, int32_t page_size, const int64_t *slots, int64_t n_slots,
+                                         void *k_f16, void *v_f16, void *stream);
+
+/*
+ * Bytes of workspace mixllm_kv4_attention needs, in *bytes.  Pure host
+ * function; arguments as there.
+ */
+MIXLLM_API mixllm_status mixllm_kv4_attention_workspace_bytes(int64_t requests, int64_t max_q, int32_t q_heads,
+                                                              int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                                                              int64_t table_width, size_t *bytes);
+
+/*
+ * Attention of ragged queries over the cache: request b's queries are rows
+ * cu_q[b] .. cu_q[b+1] of q (at most max_q of them, 0 allowed), its keys and
+ * values the seq_lens[b] cached tokens of its pages.  Query i of n (n =
+ * cu_q[b+1] - cu_q[b]) stands at position seq_lens[b] - n + i and sees the
+ * tokens up to its own position (causal != 0) or all seq_lens[b] of them:
+ *   out[i, h] = sum_t softmax_t(scale * q[i, h] . k[t, h / g]) v[t, h / g],
+ * g = q_heads / kv_heads.  Scores, softmax statistics and sums are fp32; the
+ * probabilities, times the values' scales, are rounded once to fp16 for the
+ * tensor cores.  A query that sees no token gets zeros (and lse -infinity).
+ * Only the first ceil(seq_lens[b] / page_size) entries of a request's row of
+ * the table are read.  Rows of q and out outside every request are neither read
+ * nor written.
+ *   q, out   device fp16 [n_tokens, q_heads, head_dim], heads contiguous,
+ *            tokens q_stride / out_stride elements apart (multiples of 8),
+ *            16-byte aligned; out overlaps no input
+ *   lse      device fp32 [n_tokens, q_heads]: the natural logarithm of the
+ *            softmax's denominator, or NULL
+ *   workspace  device, at least mixllm_kv4_attention_workspace_bytes() bytes,
+ *            256-byte aligned, zero-filled before its first use; calls leave
+ *            its counters (the first 4096 bytes) at zero, so it stays ready
+ *            for calls of any sizes it is large enough for.  Two calls that run
+ *            at the same time must not share one.  After MIXLLM_ERR_TIMEOUT
+ *            zero it again.
+ * The lengths stay on the device: a captured graph serves any lengths within
+ * requests, max_q and table_width.  At most 16384 requests.  The result does
+ * not depend on timing.  Asynchronous on `stream`.
+ */
+MIXLLM_API mixllm_status mixllm_kv4_attention(const void *q_f16, int64_t q_stride, int64_t n_tokens, int32_t q_heads,
+                                              const uint8_t *codes, const uint32_t *meta, int64_t pages,
+                                              int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                                              const int32_t *block_table, int64_t table_stride, int64_t table_width,
+                                              const int32_t *seq_lens, const int32_t *cu_q, int64_t requests,
+                                              int64_t max_q, float scale, int32_t causal, void *out_f16,
+                                              int64_t out_stride, float *lse, void *workspace,
+                                              size_t workspace_bytes, void *stream);
+
+/*
  * Waits for `stream`, then reads and clears the device status word of the
  * current device.  Returns MIXLLM_ERR_TIMEOUT if a kernel of this library
- * gave up a wait since the last call, MIXLLM_ERR_BOUNDS if (checked build
- * only) a range check failed, MIXLLM_ERR_CUDA if the stream reports a CUDA
+ * gave up a wait since the last call, MIXLLM_ERR_BOUNDS if a KV-cache kernel
+ * met a page, slot, position or length out of range or (checked build only) a
+ * range check failed, MIXLLM_ERR_CUDA if the stream reports a CUDA
  * error, MIXLLM_OK otherwise.  SYNCHRONOUS.
  */
 MIXLLM_API mixllm_status mixllm_sync_status(void *stream);

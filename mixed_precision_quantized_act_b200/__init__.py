@@ -43,4 +43,22 @@ from ._lib import (  # noqa: F401
     sync_status,
     version,
 )
+from .kv4 import (  # noqa: F401
+    KV4Cache,
+    kv4_append_into,
+    kv4_assign_into,
+    kv4_attention,
+    kv4_attention_into,
+    kv4_attention_workspace,
+    kv4_attention_workspace_bytes,
+    kv4_cache,
+    kv4_read_into,
+    rope_table,
+)
+from .norm import (  # noqa: F401
+    dequantize_act,
+    dequantize_act_into,
+    residual_norm_into,
+    residual_norm_quantize_into,
+)
 from .packfile import load_packed, save_packed  # noqa: F401

@@ -22,6 +22,7 @@ _NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT", 
 
 # Every entry point declared in include/mixllm.h, with (restype, argtypes).
 _i64, _i32, _u32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_void_p
+_f32 = ctypes.c_float
 SIGNATURES = {
     "mixllm_version": (ctypes.c_int, []),
     "mixllm_last_error": (ctypes.c_char_p, []),
@@ -59,6 +60,19 @@ SIGNATURES = {
     "mixllm_small_m_debug_partials": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64,
                                                      _vp, _vp, _vp, _i64, ctypes.c_int32, _vp, _vp, _vp,
                                                      ctypes.c_size_t, _vp]),
+    "mixllm_dequantize_act": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i32, _vp, _vp]),
+    "mixllm_residual_norm": (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _f32, _vp, _i64, _vp, _f32,
+                                            _i64, _i64, _vp, _vp, _vp, _vp]),
+    "mixllm_kv4_assign": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp,
+                                         _i64, _vp, _vp, _vp]),
+    "mixllm_kv4_append": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                         _i32, _vp, _i64, _vp, _vp, _i64, _i32, _vp]),
+    "mixllm_kv4_read": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp]),
+    "mixllm_kv4_attention_workspace_bytes": (ctypes.c_int, [_i64, _i64, _i32, _i32, _i32, _i32, _i64,
+                                                            ctypes.POINTER(ctypes.c_size_t)]),
+    "mixllm_kv4_attention": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _i64,
+                                            _vp, _vp, _i64, _i64, _f32, _i32, _vp, _i64, _vp, _vp, ctypes.c_size_t,
+                                            _vp]),
     "mixllm_sync_status": (ctypes.c_int, [_vp]),
     "mixllm_selftest_wait_timeout": (ctypes.c_int, [_u32, _vp]),
     "mixllm_checked_build": (ctypes.c_int, []),

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 namespace mixllm {
@@ -91,6 +92,95 @@ cudaError_t launch_channel_salience(const float *W, int64_t N, int64_t K, const 
 size_t select_top_t_workspace_bytes(int64_t n);
 cudaError_t launch_select_top_t(const float *S, int64_t n, int64_t T, uint8_t *is8, void *ws, cudaStream_t stream,
                                 const char **msg);
+
+// The norms around a block (norm.cuh).
+struct NormArgs {
+  int64_t M, K;
+  const __half *x;  // the block's output, or null: r is only normalized
+  int64_t x_stride;
+  const __half *w_post;  // the norm after the block, or null
+  const __half *gate;    // or null; gate_stride 0: one row for all tokens
+  int64_t gate_stride;
+  float scale;
+  const void *r;  // the residual stream, fp16 or fp32
+  int64_t r_stride;
+  bool r_fp32;
+  void *r_out;  // or null
+  int64_t r_out_stride;
+  const __half *w;
+  float eps;
+  __half *y;   // fp16 [M, K], or null
+  int8_t *A_q;  // codes and scales of y, or null
+  float *s_a;
+};
+cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t stream);
+cudaError_t launch_dequantize_act(const int8_t *A_q, const float *s_a, int64_t M, int64_t K, void *X,
+                                  cudaStream_t stream);
+
+// The paged 4-bit KV cache (kv4_cache.cuh) and the attention over it
+// (kv4_attention.cuh).
+constexpr int kKv4MaxRequests = 16384;
+
+struct Kv4Cache {
+  uint8_t *codes;
+  uint32_t *meta;
+  int64_t pages;
+  int H, D, page_log2;
+};
+
+struct AssignArgs {
+  const int32_t *ctx_lens, *new_lens;
+  int B;
+  int32_t *table;
+  int64_t table_stride;
+  int W;
+  const int32_t *free_pages;
+  int n_free;
+  const int32_t *count;
+  int page_log2;
+  int32_t *seq_lens, *cu_new;
+  int64_t *slots;
+  int32_t *positions;
+  int64_t T;
+  int32_t *left, *status;
+};
+cudaError_t launch_kv4_assign(const AssignArgs &a, cudaStream_t stream, const char **msg);
+
+struct AppendArgs {
+  Kv4Cache cache;
+  int64_t T;
+  const int64_t *slots;
+  const __half *k, *v, *q;  // q or null (Hq = 0)
+  int64_t k_stride, v_stride, q_stride;
+  int Hq;
+  __half *q_out;
+  int64_t q_out_stride;
+  const int32_t *positions;
+  const float *rope;  // [max_pos][rotary]: cosines, then sines; or null
+  int64_t max_pos;
+  int rotary;
+};
+cudaError_t launch_kv4_append(const AppendArgs &a, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4Cache &c, const int64_t *slots, int64_t T, void *k, void *v,
+                            cudaStream_t stream);
+
+struct AttendArgs {
+  Kv4Cache cache;
+  const __half *q;
+  int64_t q_stride, T;
+  int Hq, B, max_q;
+  const int32_t *table;
+  int64_t table_stride;
+  int W;
+  const int32_t *kv_lens, *cu_q;
+  float scale;
+  int causal;
+  __half *out;
+  int64_t out_stride;
+  float *lse;  // [T][Hq], or null
+};
+size_t kv4_attention_workspace_bytes(int B, int max_q, int Hq, int H, int D, int page_log2, int W);
+cudaError_t launch_kv4_attention(const AttendArgs &a, void *ws, cudaStream_t stream, const char **msg);
 
 int64_t padded_channels(int64_t n);  // n rounded up to a multiple of 256
 

@@ -5,6 +5,7 @@
 // launches kernels; every step of the layer's arithmetic runs on the GPU.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -13,7 +14,10 @@
 #include "gemm_w4w8a8.cuh"
 #include "gemm_small_m.cuh"
 #include "search.cuh"
+#include "kv4_attention.cuh"
+#include "kv4_cache.cuh"
 #include "launch.h"
+#include "norm.cuh"
 #include "pack_host.cuh"
 #include "quant.cuh"
 
@@ -110,6 +114,41 @@ mixllm_status gemm_common(const int8_t *A_q, const float *s_a, int64_t M, int64_
   if (e == cudaErrorNotSupported) return fail(MIXLLM_ERR_UNSUPPORTED, "%s", msg);
   if (e != cudaSuccess) return fail(MIXLLM_ERR_CUDA, "%s: %s", msg, cudaGetErrorString(e));
   return ok();
+}
+
+int page_log2_of(int32_t page_size) {
+  for (int l = 4; l <= 8; ++l)
+    if (page_size == 1 << l) return l;
+  return -1;
+}
+
+// The cache's shape and buffers (a cache of no pages may have null buffers).
+mixllm_status check_kv4(uint8_t *codes, uint32_t *meta, int64_t pages, int32_t kv_heads, int32_t head_dim,
+                        int32_t page_size, mixllm::Kv4Cache *cache) {
+  const int page_log2 = page_log2_of(page_size);
+  if (page_log2 < 0) return fail(MIXLLM_ERR_UNSUPPORTED, "page size %d is not 16, 32, 64, 128 or 256", page_size);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(MIXLLM_ERR_UNSUPPORTED, "head size %d is not 64 or 128", head_dim);
+  if (kv_heads < 1 || kv_heads > 65536) return fail(MIXLLM_ERR_INVALID_ARG, "%d key heads", kv_heads);
+  if (pages < 0 || pages > 0x7FFFFFFF) return fail(MIXLLM_ERR_INVALID_ARG, "bad number of pages");
+  if (pages > 0 && (!codes || !meta)) return fail(MIXLLM_ERR_INVALID_ARG, "null cache buffer");
+  if (!aligned(codes, 16) || !aligned(meta, 16))
+    return fail(MIXLLM_ERR_INVALID_ARG, "the cache's buffers must be 16-byte aligned");
+  *cache = mixllm::Kv4Cache{codes, meta, pages, kv_heads, head_dim, page_log2};
+  return MIXLLM_OK;
+}
+
+mixllm_status check_kv4_heads(int64_t requests, int64_t max_q, int32_t q_heads, int64_t table_width,
+                              const mixllm::Kv4Cache &cache) {
+  if (q_heads < cache.H || q_heads % cache.H != 0 || q_heads > 65536)
+    return fail(MIXLLM_ERR_INVALID_ARG, "%d query heads are no multiple of the %d key heads", q_heads, cache.H);
+  if (requests < 0 || max_q < 0 || table_width < 0) return fail(MIXLLM_ERR_INVALID_ARG, "negative size");
+  if (requests > mixllm::kKv4MaxRequests)
+    return fail(MIXLLM_ERR_UNSUPPORTED, "%lld requests are beyond %d", static_cast<long long>(requests),
+                mixllm::kKv4MaxRequests);
+  if (max_q > 0x7FFFFF00 / (q_heads / cache.H) || table_width > 0x7FFFFF00 >> cache.page_log2)
+    return fail(MIXLLM_ERR_INVALID_ARG, "queries or cached tokens of a request beyond the supported 2^31 range");
+  return MIXLLM_OK;
 }
 
 }  // namespace
@@ -509,6 +548,244 @@ mixllm_status mixllm_select_top_t(const float *S, int64_t n, int64_t T, uint8_t 
   if (st != MIXLLM_OK) return st;
   const char *msg = "";
   cudaError_t e = mixllm::launch_select_top_t(S, n, T, is8, workspace, static_cast<cudaStream_t>(stream), &msg);
+  if (e != cudaSuccess) return fail(MIXLLM_ERR_CUDA, "%s: %s", msg, cudaGetErrorString(e));
+  return ok();
+}
+
+mixllm_status mixllm_dequantize_act(const int8_t *A_q, const float *s_a, int64_t M, int64_t K, int32_t group,
+                                    void *X_f16, void *stream) {
+  mixllm_status st = check_k(K, group);
+  if (st != MIXLLM_OK) return st;
+  if (M < 0) return fail(MIXLLM_ERR_INVALID_ARG, "M < 0");
+  if (M > (1ll << 40)) return fail(MIXLLM_ERR_INVALID_ARG, "M is too large");
+  if (M == 0) return ok();
+  if (!X_f16 || !A_q || !s_a) return fail(MIXLLM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(X_f16, 16) || !aligned(A_q, 8) || !aligned(s_a, 4))
+    return fail(MIXLLM_ERR_INVALID_ARG, "X must be 16-byte aligned, A_q 8-byte and s_a 4-byte aligned");
+  st = check_device();
+  if (st != MIXLLM_OK) return st;
+  cudaError_t e = mixllm::launch_dequantize_act(A_q, s_a, M, K, X_f16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dequantize_act launch");
+  return ok();
+}
+
+mixllm_status mixllm_residual_norm(const void *r, int64_t r_stride, int32_t r_is_f32, const void *x_f16,
+                                   int64_t x_stride, const void *w_post_f16, const void *gate_f16,
+                                   int64_t gate_stride, float scale, void *r_out, int64_t r_out_stride,
+                                   const void *w_f16, float eps, int64_t M, int64_t K, void *y_f16, int8_t *A_q,
+                                   float *s_a, void *stream) {
+  mixllm_status st = check_k(K, MIXLLM_GROUP);
+  if (st != MIXLLM_OK) return st;
+  if (K > 32768) return fail(MIXLLM_ERR_UNSUPPORTED, "K = %lld is beyond 32768", static_cast<long long>(K));
+  if (M < 0 || M > 0x7FFFFFFF) return fail(MIXLLM_ERR_INVALID_ARG, "need 0 <= M < 2^31");
+  if (!(eps >= 0.0f)) return fail(MIXLLM_ERR_INVALID_ARG, "eps must not be negative");
+  if (M == 0) return ok();
+  if (!r || !w_f16) return fail(MIXLLM_ERR_INVALID_ARG, "null r or w");
+  if (!y_f16 && !A_q) return fail(MIXLLM_ERR_INVALID_ARG, "null output");
+  if (!A_q != !s_a) return fail(MIXLLM_ERR_INVALID_ARG, "A_q and s_a go together");
+  if (!x_f16 && (w_post_f16 || gate_f16 || r_out))
+    return fail(MIXLLM_ERR_INVALID_ARG, "w_post, gate and r_out need x");
+  if (!aligned(r, 16) || !aligned(x_f16, 16) || !aligned(w_post_f16, 16) || !aligned(gate_f16, 16) ||
+      !aligned(r_out, 16) || !aligned(w_f16, 16) || !aligned(y_f16, 16) || !aligned(A_q, 8) || !aligned(s_a, 4))
+    return fail(MIXLLM_ERR_INVALID_ARG, "buffers must be 16-byte aligned (A_q: 8, s_a: 4)");
+  const int64_t run = r_is_f32 ? 4 : 8;  // elements of 16 bytes
+  if (r_stride % run != 0 || (r_out && r_out_stride % run != 0) || (x_f16 && x_stride % 8 != 0) ||
+      (gate_f16 && gate_stride % 8 != 0))
+    return fail(MIXLLM_ERR_INVALID_ARG, "row strides must be multiples of 16 bytes");
+  if (M > 1 && r_out && r_out_stride < K) return fail(MIXLLM_ERR_INVALID_ARG, "rows of r_out overlap");
+  st = check_device();
+  if (st != MIXLLM_OK) return st;
+  mixllm::NormArgs a{M,
+                     K,
+                     static_cast<const __half *>(x_f16),
+                     x_stride,
+                     static_cast<const __half *>(w_post_f16),
+                     static_cast<const __half *>(gate_f16),
+                     gate_stride,
+                     scale,
+                     r,
+                     r_stride,
+                     r_is_f32 != 0,
+                     r_out,
+                     r_out_stride,
+                     static_cast<const __half *>(w_f16),
+                     eps,
+                     static_cast<__half *>(y_f16),
+                     A_q,
+                     s_a};
+  cudaError_t e = mixllm::launch_residual_norm(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "residual_norm launch");
+  return ok();
+}
+
+mixllm_status mixllm_kv4_assign(const int32_t *ctx_lens, const int32_t *new_lens, int64_t requests,
+                                int32_t *block_table, int64_t table_stride, int64_t table_width,
+                                const int32_t *free_pages, int64_t n_free, const int32_t *free_count,
+                                int32_t page_size, int32_t *seq_lens, int32_t *cu_new, int64_t *slots,
+                                int32_t *positions, int64_t n_slots, int32_t *free_left, int32_t *status,
+                                void *stream) {
+  const int page_log2 = page_log2_of(page_size);
+  if (page_log2 < 0) return fail(MIXLLM_ERR_UNSUPPORTED, "page size %d is not 16, 32, 64, 128 or 256", page_size);
+  if (requests < 0 || table_width < 0 || n_free < 0 || n_slots < 0)
+    return fail(MIXLLM_ERR_INVALID_ARG, "negative size");
+  if (requests > mixllm::kKv4MaxRequests)
+    return fail(MIXLLM_ERR_UNSUPPORTED, "%lld requests are beyond %d", static_cast<long long>(requests),
+                mixllm::kKv4MaxRequests);
+  if (n_slots > 0x7FFFFFF0 || n_free > 0x7FFFFFF0 || table_width > 0x7FFFFFF0 >> page_log2)
+    return fail(MIXLLM_ERR_INVALID_ARG, "slots, pages or a request's tokens beyond the supported 2^31 range");
+  if (requests > 1 && table_stride < table_width) return fail(MIXLLM_ERR_INVALID_ARG, "rows of the table overlap");
+  if (!cu_new || !free_count || !free_left || !status || (requests > 0 && (!ctx_lens || !new_lens || !seq_lens)) ||
+      (requests > 0 && table_width > 0 && !block_table) || (n_free > 0 && !free_pages) ||
+      (n_slots > 0 && (!slots || !positions)))
+    return fail(MIXLLM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+      !aligned(free_count, 4) || !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(slots, 8) ||
+      !aligned(positions, 4) || !aligned(free_left, 4) || !aligned(status, 4))
+    return fail(MIXLLM_ERR_INVALID_ARG, "buffers must be 4-byte aligned (slots: 8)");
+  mixllm_status st = check_device();
+  if (st != MIXLLM_OK) return st;
+  mixllm::AssignArgs a{ctx_lens, new_lens, static_cast<int>(requests), block_table, table_stride,
+                       static_cast<int>(table_width), free_pages, static_cast<int>(n_free), free_count, page_log2,
+                       seq_lens, cu_new, slots, positions, n_slots, free_left, status};
+  const char *msg = "";
+  cudaError_t e = mixllm::launch_kv4_assign(a, static_cast<cudaStream_t>(stream), &msg);
+  if (e != cudaSuccess) return fail(MIXLLM_ERR_CUDA, "%s: %s", msg, cudaGetErrorString(e));
+  return ok();
+}
+
+mixllm_status mixllm_kv4_append(uint8_t *codes, uint32_t *meta, int64_t pages, int32_t kv_heads, int32_t head_dim,
+                                int32_t page_size, const int64_t *slots, int64_t n_slots, const void *k_f16,
+                                int64_t k_stride, const void *v_f16, int64_t v_stride, const void *q_f16,
+                                int64_t q_stride, int32_t q_heads, void *q_out_f16, int64_t q_out_stride,
+                                const int32_t *positions, const float *rope, int64_t max_pos, int32_t rotary,
+                                void *stream) {
+  mixllm::Kv4Cache cache;
+  mixllm_status st = check_kv4(codes, meta, pages, kv_heads, head_dim, page_size, &cache);
+  if (st != MIXLLM_OK) return st;
+  if (n_slots < 0 || n_slots > 0x7FFFFFFF || q_heads < 0 || q_heads > 65536)
+    return fail(MIXLLM_ERR_INVALID_ARG, "bad number of tokens or heads");
+  if (rotary < 0 || rotary > head_dim || rotary % 16 != 0)
+    return fail(MIXLLM_ERR_UNSUPPORTED, "%d rotated channels: need a multiple of 16 up to the head's %d", rotary, head_dim);
+  if (n_slots == 0) return ok();
+  if (!slots || !k_f16 || !v_f16) return fail(MIXLLM_ERR_INVALID_ARG, "null slots, k or v");
+  if (q_heads > 0 && (!q_f16 || !q_out_f16)) return fail(MIXLLM_ERR_INVALID_ARG, "null q or q_out");
+  if (rotary > 0 && (!rope || !positions || max_pos <= 0))
+    return fail(MIXLLM_ERR_INVALID_ARG, "a rotation needs the table and the positions");
+  if (!aligned(slots, 8) || !aligned(k_f16, 16) || !aligned(v_f16, 16) || !aligned(q_f16, 16) ||
+      !aligned(q_out_f16, 16) || !aligned(rope, 16) || !aligned(positions, 4))
+    return fail(MIXLLM_ERR_INVALID_ARG, "k, v, q, q_out and rope must be 16-byte aligned, slots 8, positions 4");
+  if (k_stride % 8 != 0 || v_stride % 8 != 0 || (q_heads > 0 && (q_stride % 8 != 0 || q_out_stride % 8 != 0)))
+    return fail(MIXLLM_ERR_INVALID_ARG, "token strides must be multiples of 8 elements");
+  if (n_slots > 1 && q_heads > 0 && q_out_stride < static_cast<int64_t>(q_heads) * head_dim)
+    return fail(MIXLLM_ERR_INVALID_ARG, "rows of q_out overlap");
+  st = check_device();
+  if (st != MIXLLM_OK) return st;
+  mixllm::AppendArgs a{cache,
+                       n_slots,
+                       slots,
+                       static_cast<const __half *>(k_f16),
+                       static_cast<const __half *>(v_f16),
+                       static_cast<const __half *>(q_f16),
+                       k_stride,
+                       v_stride,
+                       q_stride,
+                       q_heads,
+                       static_cast<__half *>(q_out_f16),
+                       q_out_stride,
+                       positions,
+                       rotary > 0 ? rope : nullptr,
+                       max_pos,
+                       rotary};
+  cudaError_t e = mixllm::launch_kv4_append(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_append launch");
+  return ok();
+}
+
+mixllm_status mixllm_kv4_read(const uint8_t *codes, const uint32_t *meta, int64_t pages, int32_t kv_heads,
+                              int32_t head_dim, int32_t page_size, const int64_t *slots, int64_t n_slots,
+                              void *k_f16, void *v_f16, void *stream) {
+  mixllm::Kv4Cache cache;
+  mixllm_status st = check_kv4(const_cast<uint8_t *>(codes), const_cast<uint32_t *>(meta), pages, kv_heads, head_dim,
+                               page_size, &cache);
+  if (st != MIXLLM_OK) return st;
+  if (n_slots < 0 || n_slots > 0x7FFFFFFF) return fail(MIXLLM_ERR_INVALID_ARG, "bad number of tokens");
+  if (n_slots == 0) return ok();
+  if (!slots || !k_f16 || !v_f16) return fail(MIXLLM_ERR_INVALID_ARG, "null slots, k or v");
+  if (!aligned(slots, 8) || !aligned(k_f16, 16) || !aligned(v_f16, 16))
+    return fail(MIXLLM_ERR_INVALID_ARG, "k and v must be 16-byte aligned, slots 8");
+  st = check_device();
+  if (st != MIXLLM_OK) return st;
+  cudaError_t e = mixllm::launch_kv4_read(cache, slots, n_slots, k_f16, v_f16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_read launch");
+  return ok();
+}
+
+mixllm_status mixllm_kv4_attention_workspace_bytes(int64_t requests, int64_t max_q, int32_t q_heads, int32_t kv_heads,
+                                                   int32_t head_dim, int32_t page_size, int64_t table_width,
+                                                   size_t *bytes) {
+  if (!bytes) return fail(MIXLLM_ERR_INVALID_ARG, "null bytes");
+  mixllm::Kv4Cache cache;
+  mixllm_status st = check_kv4(nullptr, nullptr, 0, kv_heads, head_dim, page_size, &cache);
+  if (st == MIXLLM_OK) st = check_kv4_heads(requests, max_q, q_heads, table_width, cache);
+  if (st != MIXLLM_OK) return st;
+  *bytes = mixllm::kv4_attention_workspace_bytes(static_cast<int>(requests), static_cast<int>(max_q), q_heads,
+                                                 kv_heads, head_dim, cache.page_log2, static_cast<int>(table_width));
+  return ok();
+}
+
+mixllm_status mixllm_kv4_attention(const void *q_f16, int64_t q_stride, int64_t n_tokens, int32_t q_heads,
+                                   const uint8_t *codes, const uint32_t *meta, int64_t pages, int32_t kv_heads,
+                                   int32_t head_dim, int32_t page_size, const int32_t *block_table,
+                                   int64_t table_stride, int64_t table_width, const int32_t *seq_lens,
+                                   const int32_t *cu_q, int64_t requests, int64_t max_q, float scale, int32_t causal,
+                                   void *out_f16, int64_t out_stride, float *lse, void *workspace,
+                                   size_t workspace_bytes, void *stream) {
+  mixllm::Kv4Cache cache;
+  mixllm_status st = check_kv4(const_cast<uint8_t *>(codes), const_cast<uint32_t *>(meta), pages, kv_heads, head_dim,
+                               page_size, &cache);
+  if (st == MIXLLM_OK) st = check_kv4_heads(requests, max_q, q_heads, table_width, cache);
+  if (st != MIXLLM_OK) return st;
+  if (n_tokens < 0 || n_tokens > 0x7FFFFFFF) return fail(MIXLLM_ERR_INVALID_ARG, "bad number of query tokens");
+  if (!std::isfinite(scale)) return fail(MIXLLM_ERR_INVALID_ARG, "scale must be finite");
+  if (n_tokens == 0 || requests == 0 || max_q == 0) return ok();
+  if (!q_f16 || !out_f16 || !seq_lens || !cu_q || (table_width > 0 && !block_table))
+    return fail(MIXLLM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(q_f16, 16) || !aligned(out_f16, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(cu_q, 4) || !aligned(lse, 4))
+    return fail(MIXLLM_ERR_INVALID_ARG, "q and out must be 16-byte aligned, the other buffers 4-byte aligned");
+  if (q_stride % 8 != 0 || out_stride % 8 != 0)
+    return fail(MIXLLM_ERR_INVALID_ARG, "token strides must be multiples of 8 elements");
+  if (n_tokens > 1 && out_stride < static_cast<int64_t>(q_heads) * head_dim)
+    return fail(MIXLLM_ERR_INVALID_ARG, "rows of out overlap");
+  const size_t need = mixllm::kv4_attention_workspace_bytes(static_cast<int>(requests), static_cast<int>(max_q),
+                                                            q_heads, kv_heads, head_dim, cache.page_log2,
+                                                            static_cast<int>(table_width));
+  if (workspace_bytes < need)
+    return fail(MIXLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu this shape needs",
+                workspace_bytes, need);
+  if (!workspace || !aligned(workspace, 256))
+    return fail(MIXLLM_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device buffer");
+  st = check_device();
+  if (st != MIXLLM_OK) return st;
+  mixllm::AttendArgs a{cache,
+                       static_cast<const __half *>(q_f16),
+                       q_stride,
+                       n_tokens,
+                       q_heads,
+                       static_cast<int>(requests),
+                       static_cast<int>(max_q),
+                       block_table,
+                       table_stride,
+                       static_cast<int>(table_width),
+                       seq_lens,
+                       cu_q,
+                       scale,
+                       causal != 0,
+                       static_cast<__half *>(out_f16),
+                       out_stride,
+                       lse};
+  const char *msg = "";
+  cudaError_t e = mixllm::launch_kv4_attention(a, workspace, static_cast<cudaStream_t>(stream), &msg);
   if (e != cudaSuccess) return fail(MIXLLM_ERR_CUDA, "%s: %s", msg, cudaGetErrorString(e));
   return ok();
 }
