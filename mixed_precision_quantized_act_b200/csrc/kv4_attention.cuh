@@ -22,26 +22,38 @@ namespace mixllm {
 // Few queries per request (decode).  HBM-bound: 2 * (D/2 + 4) bytes per cached
 // token and head.
 //
-// Work is cut into units of 128 tokens of one (request, row tile, key head);
+// Work is cut into units of 256 tokens of one (request, row tile, key head);
 // block c takes the units [c U / P, (c + 1) U / P) of their concatenation, so
 // requests of any lengths load every SM alike, and the lengths stay on the
 // device.  A row tile is 8 NT rows (query token, query head of the group).
-// Within a block a producer warp copies each unit's codes and metadata into a
-// ring of stages by bulk copies, one per page and array, and eight warps take
-// 16 tokens each.  Tokens are the 16-row side of m16n8k16 and the query rows
-// its 8-column side, so that a group of 8 heads fills the instruction and
-// smaller ones waste only tensor work: S^T = K Q^T with K as the A operand,
-// then O^T = V^T P^T with V^T as A.  The codes go from shared memory to the A
-// registers without a shuffle:
+// Within a block each of eight warps takes 32 tokens of every unit and fetches
+// them itself, by cp.async into stages of its own, with no barrier between
+// warps until a segment ends.  Tokens are the 16-row side of m16n8k16 and the
+// query rows its 8-column side, so that a group of 8 heads fills the
+// instruction and smaller ones waste only tensor work: S^T = K Q^T with K as
+// the A operand, then O^T = V^T P^T with V^T as A.
+//
+// What bounds the loop on the way to HBM speed is the unpacking: integer
+// instructions issue at half rate.  So one AND per pair of codes makes fp16
+// subnormals of them, n 2^-24 (low nibbles) or 16 n 2^-24 (high nibbles), which
+// the tensor cores multiply exactly, and nothing is subtracted per code.  The
+// tensor cores align products by their operands' exponents, of which a
+// subnormal has the smallest normal one, so n 2^-24 would lose 10 bits of
+// the fp32 sum; a half-precision multiply on the otherwise idle FMA pipe makes
+// it n 2^-10.  The high nibbles lose 6 bits, 2^-18 of the largest product, and
+// stay as they are.
 //   * K: any permutation of the channels serves as long as Q has the same, so
 //     a lane takes D/4 consecutive channels of a token and pairs nibbles i and
-//     i + 4 of a word, which one AND brings to fp16 form (0x6400 | n is
-//     1024 + n; a high nibble gives 1024 + 16 n and is scaled by 1/16 in the
-//     FMA that subtracts the zero point);
+//     i + 4 of a word.  Low and high nibbles go into accumulators of their own,
+//     joined with their factor; the zero point comes off as z * sum(q).
 //   * V: lane (g, t) takes channels g D/8 .. of four tokens; a byte permute
-//     joins the halves of two tokens' words into (token, token') pairs.  The
-//     output channel of an accumulator is then the lane's own channel range.
-// P^T goes from accumulator to B layout by movmatrix.
+//     joins the halves of two tokens' words into (token, token') pairs.  Low
+//     and high nibbles are different accumulator rows, scaled at the end.  One
+//     more product, with the zero points in the place of codes, gives the sum of
+//     p z that comes off every channel.
+// The differences are taken in fp32 of sums of at most 15 |q| and 15 p: no more
+// is lost than in the sums themselves.  P^T goes from accumulator to B layout
+// by movmatrix.
 //
 // Softmax per warp with lazy rescaling: the running maximum m moves only when
 // a score passes it by more than 8 (in log2 units), so p <= 2^8.  The values'
@@ -54,24 +66,24 @@ namespace mixllm {
 // the last block to arrive adds them in the order of the tokens, so the result
 // does not depend on timing.
 // ---------------------------------------------------------------------------
-constexpr int kKvTile = 128;       // tokens per unit
-constexpr int kKvWarps = kKvTile / 16;
-constexpr int kKvThreads = 32 * (kKvWarps + 1);
-constexpr int kKvMaxPieces = kKvTile / 16;  // pages of a unit at the smallest page
+constexpr int kKvWarps = 8;
+constexpr int kKvThreads = 32 * kKvWarps;
+constexpr int kKvTile = 32 * kKvWarps;  // tokens per unit
 constexpr float kKvNoMax = -3.0e38f;
 
 template <int D, int NT>
 struct KvCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kRowBytes = D / 2;
-  static constexpr int kCodes = kKvTile * kRowBytes;  // bytes of one unit's key (or value) codes
-  static constexpr int kMeta = kKvTile * 4;
-  static constexpr int kStage = 2 * (kCodes + kMeta);
-  static constexpr int kPitch = D + 4;  // floats per row of the join buffer
+  static constexpr int kCodes = 32 * kRowBytes;  // bytes of 32 tokens' key (or value) codes
+  static constexpr int kStage = 2 * (kCodes + 32 * 4);
+  static constexpr int kStages = D == 128 && NT == 1 ? 2 : 4;
+  static constexpr int kRing = kStages * kStage;  // of one warp
+  static constexpr int kPitch = D + 4;            // floats per row of the join buffer
   static constexpr int kJoin = kKvWarps * kRows * kPitch * 4;
-  static constexpr int kStages = NT == 1 ? 4 : 5;
   static constexpr int kBlocksPerSm = NT == 1 ? 2 : 1;
-  static constexpr int kSmem = kStages * kStage + kJoin + 2 * kKvWarps * kRows * 4;
+  static constexpr int kSmem = kKvWarps * kRing + kJoin + 2 * kKvWarps * kRows * 4;
+  static_assert(kBlocksPerSm * (kSmem + 2048) <= 228 * 1024, "resident blocks per SM");
 };
 constexpr int kKvMaxGrid = 2 * 148;
 
@@ -125,6 +137,87 @@ struct KvWalk {
   }
 };
 
+// A warp's fetching: 32 tokens of each of its block's units in turn, codes and
+// metadata, into the next stage of its ring.  Half a warp copies 16 tokens:
+// a page holds a multiple of 16, so they lie in one.
+template <typename C>
+struct KvFetch {
+  uint32_t ring;     // shared address of this lane's first bytes in stage 0
+  uint32_t present;  // bits 2s, 2s + 1: the halves of stage s are tokens of a page that exists
+  int stage;
+  int b, rt, h, tile, batch, id;
+  int64_t left;
+  KvReq r;
+
+  __device__ __forceinline__ void start(const KvWalk &w, int lane, const uint8_t *to) {
+    ring = smem_u32(to) + (lane >> 4) * (16 * C::kRowBytes) + (lane & 15) * 16;
+    present = 0;
+    stage = 0;
+    b = w.b, rt = w.rt, h = w.h, tile = w.tile, r = w.r;
+    left = w.left;
+    batch = -1;
+  }
+
+  __device__ __forceinline__ void unit(const AttendArgs &a, int warp, int lane) {
+    if (left > 0) {
+      const int page_log2 = a.cache.page_log2;
+      if ((tile >> 4) != batch) {
+        // the pages of the warp's tokens in 16 units: lane 2u + i has unit u's half i
+        batch = tile >> 4;
+        const int64_t token = (static_cast<int64_t>(batch) << 4) * kKvTile + (lane >> 1) * kKvTile + 32 * warp + 16 * (lane & 1);
+        id = -1;
+        if (token < r.kv) {
+          id = a.table[static_cast<int64_t>(b) * a.table_stride + (token >> page_log2)];
+          if (id < 0 || id >= a.cache.pages) {
+            record_status(kStatusBounds);
+            id = -1;
+          }
+        }
+      }
+      const int page = __shfl_sync(0xFFFFFFFFu, id, (tile & 15) * 2 + (lane >> 4));
+      const uint32_t halves = __ballot_sync(0xFFFFFFFFu, page >= 0);
+      present = (present & ~(3u << 2 * stage)) | ((halves & 1u) | (halves >> 30 & 2u)) << 2 * stage;
+      if (page >= 0) {
+        const int row = (tile * kKvTile + 32 * warp + (lane & 16)) & ((1 << page_log2) - 1);
+        const int64_t at = static_cast<int64_t>(page) * (2 * a.cache.H << page_log2) + ((h << page_log2) + row);
+        const int64_t to_value = static_cast<int64_t>(a.cache.H) << page_log2;  // rows from a key to its value
+        const uint8_t *k = a.cache.codes + at * C::kRowBytes + (lane & 15) * 16;
+        const uint8_t *v = k + to_value * C::kRowBytes;
+        const uint32_t dst = ring + stage * C::kStage;
+#pragma unroll
+        for (int i = 0; i < 16 * C::kRowBytes; i += 256) {
+          cp_async_16_u32(dst + i, k + i);
+          cp_async_16_u32(dst + C::kCodes + i, v + i);
+        }
+        if ((lane & 15) < 8) {  // key metadata of 16 tokens, then value metadata
+          const int part = lane & 3, kv = lane >> 2 & 1;
+          const uint32_t to = dst - (lane >> 4) * (16 * C::kRowBytes) - (lane & 15) * 16 + 2 * C::kCodes + kv * 128 +
+                              (lane >> 4) * 64 + part * 16;
+          cp_async_16_u32(to, a.cache.meta + at + (kv ? to_value : 0) + part * 4);
+        }
+      }
+      --left;
+      if (++tile == r.tiles) {
+        tile = 0;
+        batch = -1;
+        if (++h == a.cache.H) {
+          h = 0;
+          if (++rt == r.row_tiles) {
+            rt = 0;
+            while (left > 0 && ++b < a.B) {
+              r = kv_req(a, b, C::kRows);
+              if (r.tiles > 0) break;
+            }
+            if (b >= a.B) left = 0;
+          }
+        }
+      }
+    }
+    cp_async_commit();  // one group per unit, empty or not, so that waiting counts units
+    if (++stage == C::kStages) stage = 0;
+  }
+};
+
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -141,29 +234,21 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-// Two nibbles of w at bits 0 and 16 (low) or 4 and 20 (high) as fp16 integers
-// minus the zero points in c: exact (integers below 2048, and multiples of
-// 1/16 below 128).
-__device__ __forceinline__ uint32_t nib_lo(uint32_t w, uint32_t c) {
-  const uint32_t x = (w & 0x000F000Fu) | 0x64006400u;
-  uint32_t r;
-  asm("add.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t nib_hi(uint32_t w, uint32_t c) {
-  const uint32_t x = (w & 0x00F000F0u) | 0x64006400u;
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0x2C002C00u), "r"(c));
-  return r;
-}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float meta_scale(uint32_t m) {
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(m & 0xFFFFu)));
+// A row's scale, and its zero point as the subnormal z 2^-24.
+__device__ __forceinline__ float2 meta_pair(uint32_t m) { return __half22float2(*reinterpret_cast<const __half2 *>(&m)); }
+// Pairs of codes as fp16: low nibbles as n 2^-10, high ones as n 2^-20.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w & 0x000F000Fu), "r"(0x74007400u));  // by 2^14
+  return r;
 }
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return w & 0x00F000F0u; }
+constexpr float kHighToLow = 0x1p10f;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_decode_kernel(const AttendArgs a,
@@ -172,26 +257,14 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
   using C = KvCfg<D, NT>;
   constexpr int kRows = C::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t *ring = smem;
-  float *join = reinterpret_cast<float *>(smem + C::kStages * C::kStage);
+  float *join = reinterpret_cast<float *>(smem + kKvWarps * C::kRing);
   float *join_m = join + kKvWarps * kRows * C::kPitch, *join_l = join_m + kKvWarps * kRows;
-  __shared__ uint64_t full[C::kStages], empty[C::kStages];
-  __shared__ uint32_t present[C::kStages];  // bit j: piece j of the stage was copied
-  __shared__ volatile int abort_flag;
   __shared__ int first_b, last_here;
-  __shared__ long long first_rem, warp_units[kKvWarps + 1];
+  __shared__ long long first_rem, warp_units[kKvWarps];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int group = a.Hq / a.cache.H, page_log2 = a.cache.page_log2;
-  if (tid == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kKvWarps);
-    }
-    fence_mbar_init();
-    abort_flag = 0;
-    first_b = a.B;
-  }
+  const int group = a.Hq / a.cache.H;
+  if (tid == 0) first_b = a.B;
   __syncthreads();
 
   // ---- this block's units
@@ -213,7 +286,7 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
       if (lane == 31) warp_units[warp] = incl;
       __syncthreads();
       long long before = base;
-      for (int w = 0; w <= kKvWarps; ++w) {
+      for (int w = 0; w < kKvWarps; ++w) {
         if (w < warp) before += warp_units[w];
         base += warp_units[w];
       }
@@ -248,92 +321,29 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
   w0.seg_first = start - w0.tile;
   w0.settle(a, kRows);
 
-  if (warp == kKvWarps) {
-    // ------------------------------------------------------------ producer
-    const int page = 1 << page_log2;
-    const int piece = page < kKvTile ? page : kKvTile;  // tokens per copy
-    const int pieces = kKvTile / piece;
-    const uint32_t piece_bytes = 2u * piece * (C::kRowBytes + 4);
-    const int64_t page_rows = static_cast<int64_t>(a.cache.H) << page_log2;
-    int stage = 0;
-    uint32_t phase = 0, issued = 0;
-    for (KvWalk w = w0; w.left > 0; w.next(a, kRows)) {
-      const int used = (w.r.kv + page - 1) >> page_log2;
-      const int32_t *table = a.table + static_cast<int64_t>(w.b) * a.table_stride;
-      // the page numbers of 32 pieces at a time, one per lane
-      int batch = -1, id = -1;
-      for (int i = 0; i < w.count; ++i) {
-        const int tile = w.tile + i;
-        const int first = tile * pieces;  // in pieces of the segment
-        if (first / 32 != batch) {
-          batch = first / 32;
-          const int64_t token = (static_cast<int64_t>(batch) * 32 + lane) * piece;
-          const int64_t entry = token >> page_log2;
-          id = -1;
-          if (entry < used) {
-            id = table[entry];
-            if (id < 0 || id >= a.cache.pages) {
-              record_status(kStatusBounds);
-              id = -1;
-            }
-          }
-        }
-        warp_wait(&empty[stage], phase ^ 1, &abort_flag);
-        // pieces divides 32, so a unit's pieces lie in one batch
-        const int src_lane = (first & 31) + (lane >> 2);
-        const int my_id = __shfl_sync(0xFFFFFFFFu, id, src_lane & 31);
-        const bool mine = (lane >> 2) < pieces && my_id >= 0 && !abort_flag;
-        const uint32_t have = __ballot_sync(0xFFFFFFFFu, mine);  // four lanes per piece
-        if (lane == 0) {
-          uint32_t bits = 0;
-          for (int j = 0; j < kKvMaxPieces; ++j) bits |= (have >> (4 * j) & 1u) << j;
-          present[stage] = bits;
-          mbar_arrive_expect_tx(&full[stage], piece_bytes * __popc(bits));
-        }
-        __syncwarp();
-        if (mine) {
-          const int j = lane >> 2, what = lane & 3;  // key codes, value codes, key meta, value meta
-          const int kv = what & 1;
-          const int row = static_cast<int>((static_cast<int64_t>(tile) * kKvTile + j * piece) & (page - 1));
-          const int64_t at = (static_cast<int64_t>(my_id) * 2 + kv) * page_rows + (static_cast<int64_t>(w.h) << page_log2) + row;
-          uint8_t *dst = ring + stage * C::kStage;
-          if (what < 2)
-            bulk_load(dst + kv * C::kCodes + j * piece * C::kRowBytes, a.cache.codes + at * C::kRowBytes,
-                      piece * C::kRowBytes, &full[stage]);
-          else
-            bulk_load(dst + 2 * C::kCodes + kv * C::kMeta + j * piece * 4, a.cache.meta + at, piece * 4, &full[stage]);
-        }
-        ++issued;
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-    }
-    if (abort_flag) {  // a wait gave up: let the copies in flight land before the block ends
-      for (uint32_t i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
-        mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1, 1ll << 28);
-    }
-    return;
-  }
+  KvFetch<C> fetch;
+  fetch.start(w0, lane, smem + warp * C::kRing);
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) fetch.unit(a, warp, lane);
 
-  // -------------------------------------------------------------- consumers
   const int g = lane >> 2, t = lane & 3;
   // accumulator row r of the score tile is token r ^ (r >> 1 & 1): the value
   // rows that four lanes read together then alternate in the 32 banks
-  const int row_a = 16 * warp + (g ^ (g >> 1 & 1)), row_b = row_a + 8;
-  const int vr0 = 16 * warp + ((2 * t) ^ (t & 1)), vr1 = 16 * warp + ((2 * t + 1) ^ (t & 1));
+  const int row_a = g ^ (g >> 1 & 1);
+  const int vr0 = (2 * t) ^ (t & 1), vr1 = (2 * t + 1) ^ (t & 1);
+  const uint32_t z_order = t & 1 ? 0x3276u : 0x7632u;  // zero points of tokens (vr0, vr1) from those of (2t, 2t + 1)
   constexpr int kWords = D / 32;   // words of a lane's key chunk
   constexpr int kMTiles = D / 16;  // 16-channel tiles of O^T
-  const float scale2 = a.scale * 1.4426950408889634f;
+  const float scale2 = a.scale * 1.4426950408889634f * 0x1p10f;  // to log2 units, from products with n 2^-10
+  const uint8_t *ring = smem + warp * C::kRing;
   int stage = 0;
-  uint32_t phase = 0;
 
   for (KvWalk w = w0; w.left > 0; w.next(a, kRows)) {
     const int rows = w.r.n * group;
     const int row0 = w.rt * kRows;
-    // ---- the query rows' B fragments, channels permuted as the keys' nibbles
+    // ---- the query rows' B fragments, channels permuted as the keys' nibbles, and their sums
     uint32_t qf[NT][kWords * 4];
+    float qs[NT][2];
     int lim[NT][2];  // keys seen by columns 2t and 2t + 1
 #pragma unroll
     for (int ni = 0; ni < NT; ++ni) {
@@ -343,17 +353,27 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
         const int tok = r / group;
         src = a.q + (static_cast<int64_t>(w.r.q0) + tok) * a.q_stride + (w.h * group + (r - tok * group)) * D + t * (D / 4);
       }
+      float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (src) v = *reinterpret_cast<const uint4 *>(src + 8 * i);
-        qf[ni][4 * i + 0] = __byte_perm(v.x, v.z, 0x5410);
-        qf[ni][4 * i + 1] = __byte_perm(v.x, v.z, 0x7632);
-        qf[ni][4 * i + 2] = __byte_perm(v.y, v.w, 0x5410);
-        qf[ni][4 * i + 3] = __byte_perm(v.y, v.w, 0x7632);
+        qf[ni][4 * i + 0] = __byte_perm(v.x, v.z, 0x5410);  // channels 0, 4: low nibbles
+        qf[ni][4 * i + 1] = __byte_perm(v.y, v.w, 0x5410);  // 2, 6
+        qf[ni][4 * i + 2] = __byte_perm(v.x, v.z, 0x7632);  // 1, 5: high nibbles
+        qf[ni][4 * i + 3] = __byte_perm(v.y, v.w, 0x7632);  // 3, 7
+        const uint32_t h2[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2[j]));
+          sum += f.x + f.y;
+        }
       }
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        qs[ni][j] = __shfl_sync(0xFFFFFFFFu, sum, (2 * t + j) * 4) * 0x1p14f;  // meets z 2^-24
         const int rj = row0 + ni * 8 + 2 * t + j;
         lim[ni][j] = a.causal && rj < rows ? w.r.kv - w.r.n + rj / group + 1 : w.r.kv;
       }
@@ -363,104 +383,98 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
     const int last_row = min(rows, row0 + kRows) - 1;
     const int lim_max = a.causal ? w.r.kv - w.r.n + last_row / group + 1 : w.r.kv;
 
-    float o[NT][kMTiles][4];
+    float o[NT][kMTiles][4], oz[NT][4];  // oz: sums of p z, the same in every row
     float m[NT][2], l[NT][2];
     float S = 0x1p-24f, inv_S = 0x1p24f;
 #pragma unroll
     for (int ni = 0; ni < NT; ++ni) {
       m[ni][0] = m[ni][1] = kKvNoMax;
       l[ni][0] = l[ni][1] = 0.0f;
+      oz[ni][0] = oz[ni][1] = oz[ni][2] = oz[ni][3] = 0.0f;
 #pragma unroll
       for (int i = 0; i < kMTiles; ++i) o[ni][i][0] = o[ni][i][1] = o[ni][i][2] = o[ni][i][3] = 0.0f;
     }
 
     for (int i = 0; i < w.count; ++i) {
-      const int base = (w.tile + i) * kKvTile;
-      warp_wait(&full[stage], phase, &abort_flag);
+      const int base = (w.tile + i) * kKvTile + 32 * warp;
+      cp_async_wait<C::kStages - 2>();
+      __syncwarp();  // every lane's copies of this stage are here, and every lane is done with the stage before
+      const uint32_t have = fetch.present >> 2 * stage & 3u;
+      fetch.unit(a, warp, lane);
       const uint8_t *st = ring + stage * C::kStage;
-      const uint8_t *vs = st + C::kCodes;
-      const uint32_t *km = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes), *vm = km + kKvTile;
-      const uint32_t have = present[stage];
-      uint32_t ka[kWords], kb[kWords], v0[kWords / 2], v1[kWords / 2], v2[kWords / 2], v3[kWords / 2];
-      if constexpr (D == 128) {
-        *reinterpret_cast<uint4 *>(ka) = *reinterpret_cast<const uint4 *>(st + row_a * C::kRowBytes + t * 16);
-        *reinterpret_cast<uint4 *>(kb) = *reinterpret_cast<const uint4 *>(st + row_b * C::kRowBytes + t * 16);
-        *reinterpret_cast<uint2 *>(v0) = *reinterpret_cast<const uint2 *>(vs + vr0 * C::kRowBytes + g * 8);
-        *reinterpret_cast<uint2 *>(v1) = *reinterpret_cast<const uint2 *>(vs + vr1 * C::kRowBytes + g * 8);
-        *reinterpret_cast<uint2 *>(v2) = *reinterpret_cast<const uint2 *>(vs + (vr0 + 8) * C::kRowBytes + g * 8);
-        *reinterpret_cast<uint2 *>(v3) = *reinterpret_cast<const uint2 *>(vs + (vr1 + 8) * C::kRowBytes + g * 8);
-      } else {
-        *reinterpret_cast<uint2 *>(ka) = *reinterpret_cast<const uint2 *>(st + row_a * C::kRowBytes + t * 8);
-        *reinterpret_cast<uint2 *>(kb) = *reinterpret_cast<const uint2 *>(st + row_b * C::kRowBytes + t * 8);
-        v0[0] = *reinterpret_cast<const uint32_t *>(vs + vr0 * C::kRowBytes + g * 4);
-        v1[0] = *reinterpret_cast<const uint32_t *>(vs + vr1 * C::kRowBytes + g * 4);
-        v2[0] = *reinterpret_cast<const uint32_t *>(vs + (vr0 + 8) * C::kRowBytes + g * 4);
-        v3[0] = *reinterpret_cast<const uint32_t *>(vs + (vr1 + 8) * C::kRowBytes + g * 4);
-      }
-      const uint32_t kma = km[row_a], kmb = km[row_b], vma = vm[row_a], vmb = vm[row_b];
-      const uint32_t z0 = vm[vr0] >> 16 & 15u, z1 = vm[vr1] >> 16 & 15u;
-      const uint32_t z2 = vm[vr0 + 8] >> 16 & 15u, z3 = vm[vr1 + 8] >> 16 & 15u;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      if (++stage == C::kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
-      if (base + 16 * warp >= lim_max) continue;  // nothing of these 16 tokens is seen
+      if (++stage == C::kStages) stage = 0;
+      if (base >= lim_max || have == 0) continue;  // nothing of these 32 tokens is seen
 
-      // ---- scores
-      float sc[NT][4];
+      // ---- scores of two 16-token blocks
+      float sc[2][NT][4];
+      float sv[2][2];
 #pragma unroll
-      for (int ni = 0; ni < NT; ++ni) sc[ni][0] = sc[ni][1] = sc[ni][2] = sc[ni][3] = 0.0f;
-      {
-        const uint32_t za = kma >> 16 & 15u, zb = kmb >> 16 & 15u;
-        const uint32_t la = 0xE400E400u | za * 0x00010001u, ha = 0xD400D400u | za * 0x00100010u;
-        const uint32_t lb = 0xE400E400u | zb * 0x00010001u, hb = 0xD400D400u | zb * 0x00100010u;
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) {
-          const uint32_t a0 = nib_lo(ka[j], la), a2 = nib_hi(ka[j], ha);
-          const uint32_t a1 = nib_lo(kb[j], lb), a3 = nib_hi(kb[j], hb);
-          const uint32_t xa = ka[j] >> 8, xb = kb[j] >> 8;
-          const uint32_t b0 = nib_lo(xa, la), b2 = nib_hi(xa, ha);
-          const uint32_t b1 = nib_lo(xb, lb), b3 = nib_hi(xb, hb);
-#pragma unroll
-          for (int ni = 0; ni < NT; ++ni) {
-            mma_f16(sc[ni], a0, a1, a2, a3, qf[ni][4 * j], qf[ni][4 * j + 1]);
-            mma_f16(sc[ni], b0, b1, b2, b3, qf[ni][4 * j + 2], qf[ni][4 * j + 3]);
-          }
+      for (int x = 0; x < 2; ++x) {
+        const uint8_t *kr = st + (16 * x + row_a) * C::kRowBytes + t * (D / 8);
+        uint32_t ka[kWords], kb[kWords];
+        if constexpr (D == 128) {
+          *reinterpret_cast<uint4 *>(ka) = *reinterpret_cast<const uint4 *>(kr);
+          *reinterpret_cast<uint4 *>(kb) = *reinterpret_cast<const uint4 *>(kr + 8 * C::kRowBytes);
+        } else {
+          *reinterpret_cast<uint2 *>(ka) = *reinterpret_cast<const uint2 *>(kr);
+          *reinterpret_cast<uint2 *>(kb) = *reinterpret_cast<const uint2 *>(kr + 8 * C::kRowBytes);
         }
-      }
-      const float fa = meta_scale(kma) * scale2, fb = meta_scale(kmb) * scale2;
-      float sva = meta_scale(vma), svb = meta_scale(vmb);
-#pragma unroll
-      for (int ni = 0; ni < NT; ++ni) {
-        sc[ni][0] *= fa, sc[ni][1] *= fa;
-        sc[ni][2] *= fb, sc[ni][3] *= fb;
-      }
-      const bool whole = base + kKvTile <= lim_min && have == (1u << (kKvTile >> min(page_log2, 7))) - 1u;
-      if (!whole) {
-        const int ta = base + row_a, tb = base + row_b;
-        const int shift = min(page_log2, 7);
-        const bool pa = have >> (row_a >> shift) & 1u, pb = have >> (row_b >> shift) & 1u;
+        const uint32_t *km = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes) + 16 * x + row_a;
+        const float2 ma = meta_pair(km[0]), mb = meta_pair(km[8]);
+        sv[x][0] = meta_pair(km[32]).x;
+        sv[x][1] = meta_pair(km[40]).x;
+        float lo[NT][4], hi[NT][4];
 #pragma unroll
         for (int ni = 0; ni < NT; ++ni)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (!pa || ta >= lim[ni][j]) sc[ni][j] = -INFINITY;
-            if (!pb || tb >= lim[ni][j]) sc[ni][2 + j] = -INFINITY;
+          for (int j = 0; j < 4; ++j) lo[ni][j] = hi[ni][j] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          const uint32_t xa = ka[j] >> 8, xb = kb[j] >> 8;
+#pragma unroll
+          for (int ni = 0; ni < NT; ++ni) {
+            mma_f16(lo[ni], low_codes(ka[j]), low_codes(kb[j]), low_codes(xa), low_codes(xb), qf[ni][4 * j],
+                    qf[ni][4 * j + 1]);
+            mma_f16(hi[ni], high_codes(ka[j]), high_codes(kb[j]), high_codes(xa), high_codes(xb), qf[ni][4 * j + 2],
+                    qf[ni][4 * j + 3]);
           }
-        // rows that no query may see hold anything: keep their scales out of S and of 0 * NaN
-        if (!pa || ta >= lim_max) sva = 0.0f;
-        if (!pb || tb >= lim_max) svb = 0.0f;
+        }
+        const float fa = ma.x * scale2, fb = mb.x * scale2;
+#pragma unroll
+        for (int ni = 0; ni < NT; ++ni)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sc[x][ni][j] =
+                fmaf(-(j < 2 ? ma.y : mb.y), qs[ni][j & 1], fmaf(hi[ni][j], kHighToLow, lo[ni][j])) * (j < 2 ? fa : fb);
+      }
+      const bool whole = base + 32 <= lim_min && have == 3u;
+      if (!whole) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int ta = have >> x & 1u ? base + 16 * x + row_a : 0x7FFFFF00, tb = ta + 8;
+#pragma unroll
+          for (int ni = 0; ni < NT; ++ni)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if ((j < 2 ? ta : tb) >= lim[ni][j & 1]) sc[x][ni][j] = -INFINITY;
+          // rows that no query may see hold anything: keep their scales out of S
+          if (ta >= lim_max) sv[x][0] = 0.0f;
+          if (tb >= lim_max) sv[x][1] = 0.0f;
+        }
       }
       // ---- running maximum
-      bool move = fmaxf(sva, svb) > 4.0f * S;
+      const float sv_max = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
+      bool move = sv_max > 4.0f * S;
+      float top[NT][2];
 #pragma unroll
       for (int ni = 0; ni < NT; ++ni)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) move |= fmaxf(sc[ni][j], sc[ni][2 + j]) > m[ni][j] + 8.0f;
+        for (int j = 0; j < 2; ++j) {
+          top[ni][j] = fmaxf(fmaxf(sc[0][ni][j], sc[0][ni][2 + j]), fmaxf(sc[1][ni][j], sc[1][ni][2 + j]));
+          move |= top[ni][j] > m[ni][j] + 8.0f;
+        }
       if (__any_sync(0xFFFFFFFFu, move)) {
-        float s_new = fmaxf(S, fmaxf(sva, svb));
+        float s_new = fmaxf(S, sv_max);
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) s_new = fmaxf(s_new, __shfl_xor_sync(0xFFFFFFFFu, s_new, x));
         const float down = __fdividef(S, s_new);
@@ -470,12 +484,13 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
         for (int ni = 0; ni < NT; ++ni)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float mx = fmaxf(m[ni][j], fmaxf(sc[ni][j], sc[ni][2 + j]));
+            float mx = fmaxf(m[ni][j], top[ni][j]);
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
             const float keep = ex2(m[ni][j] - mx);
             m[ni][j] = mx;
             l[ni][j] *= keep;
+            oz[ni][j] *= keep * down;
 #pragma unroll
             for (int k = 0; k < kMTiles; ++k) {
               o[ni][k][j] *= keep * down;
@@ -483,29 +498,47 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
             }
           }
       }
-      // ---- probabilities
-      const float wa = sva * inv_S, wb = svb * inv_S;
-      uint32_t pf[NT][2];
 #pragma unroll
-      for (int ni = 0; ni < NT; ++ni) {
-        float p[4];
+      for (int x = 0; x < 2; ++x) {
+        // ---- probabilities
+        const float wa = sv[x][0] * inv_S, wb = sv[x][1] * inv_S;
+        uint32_t pf[NT][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = ex2(sc[ni][j] - m[ni][j & 1]);
-        l[ni][0] += p[0] + p[2];
-        l[ni][1] += p[1] + p[3];
-        p[0] *= wa, p[1] *= wa;
-        p[2] *= wb, p[3] *= wb;
-        if (!whole) {  // a scale may be NaN: no product with the zero of a key that is not seen
+        for (int ni = 0; ni < NT; ++ni) {
+          float p[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) p[j] = sc[ni][j] == -INFINITY ? 0.0f : p[j];
+          for (int j = 0; j < 4; ++j) p[j] = ex2(sc[x][ni][j] - m[ni][j & 1]);
+          l[ni][0] += p[0] + p[2];
+          l[ni][1] += p[1] + p[3];
+          p[0] *= wa, p[1] *= wa;
+          p[2] *= wb, p[3] *= wb;
+          if (!whole) {  // a scale may be NaN: no product with the zero of a key that is not seen
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = sc[x][ni][j] == -INFINITY ? 0.0f : p[j];
+          }
+          pf[ni][0] = transpose8x8(half2_bits(p[0], p[1]));
+          pf[ni][1] = transpose8x8(half2_bits(p[2], p[3]));
         }
-        pf[ni][0] = transpose8x8(half2_bits(p[0], p[1]));
-        pf[ni][1] = transpose8x8(half2_bits(p[2], p[3]));
-      }
-      // ---- values
-      {
-        const uint32_t l01 = 0xE400E400u | z0 | z1 << 16, h01 = 0xD400D400u | z0 << 4 | z1 << 20;
-        const uint32_t l23 = 0xE400E400u | z2 | z3 << 16, h23 = 0xD400D400u | z2 << 4 | z3 << 20;
+        // ---- values
+        const uint8_t *vs = st + C::kCodes + 16 * x * C::kRowBytes + g * (D / 16);
+        uint32_t v0[kWords / 2], v1[kWords / 2], v2[kWords / 2], v3[kWords / 2];
+        if constexpr (D == 128) {
+          *reinterpret_cast<uint2 *>(v0) = *reinterpret_cast<const uint2 *>(vs + vr0 * C::kRowBytes);
+          *reinterpret_cast<uint2 *>(v1) = *reinterpret_cast<const uint2 *>(vs + vr1 * C::kRowBytes);
+          *reinterpret_cast<uint2 *>(v2) = *reinterpret_cast<const uint2 *>(vs + (vr0 + 8) * C::kRowBytes);
+          *reinterpret_cast<uint2 *>(v3) = *reinterpret_cast<const uint2 *>(vs + (vr1 + 8) * C::kRowBytes);
+        } else {
+          v0[0] = *reinterpret_cast<const uint32_t *>(vs + vr0 * C::kRowBytes);
+          v1[0] = *reinterpret_cast<const uint32_t *>(vs + vr1 * C::kRowBytes);
+          v2[0] = *reinterpret_cast<const uint32_t *>(vs + (vr0 + 8) * C::kRowBytes);
+          v3[0] = *reinterpret_cast<const uint32_t *>(vs + (vr1 + 8) * C::kRowBytes);
+        }
+        const uint2 *vm = reinterpret_cast<const uint2 *>(st + 2 * C::kCodes + 128 + 64 * x) + t;
+        const uint2 m01 = vm[0], m23 = vm[4];
+        const uint32_t z01 = low_codes(__byte_perm(m01.x, m01.y, z_order));
+        const uint32_t z23 = low_codes(__byte_perm(m23.x, m23.y, z_order));
+#pragma unroll
+        for (int ni = 0; ni < NT; ++ni) mma_f16(oz[ni], z01, z01, z23, z23, pf[ni][0], pf[ni][1]);
 #pragma unroll
         for (int j = 0; j < kWords / 2; ++j) {
 #pragma unroll
@@ -514,11 +547,10 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
             uint32_t x23 = __byte_perm(v2[j], v3[j], half ? 0x7632 : 0x5410);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const uint32_t a0 = nib_lo(x01, l01), a1 = nib_hi(x01, h01);
-              const uint32_t a2 = nib_lo(x23, l23), a3 = nib_hi(x23, h23);
-              const int k = 4 * j + 2 * half + q;
 #pragma unroll
-              for (int ni = 0; ni < NT; ++ni) mma_f16(o[ni][k], a0, a1, a2, a3, pf[ni][0], pf[ni][1]);
+              for (int ni = 0; ni < NT; ++ni)
+                mma_f16(o[ni][4 * j + 2 * half + q], low_codes(x01), high_codes(x01), low_codes(x23), high_codes(x23),
+                        pf[ni][0], pf[ni][1]);
               x01 >>= 8;
               x23 >>= 8;
             }
@@ -541,12 +573,14 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
           join_l[warp * kRows + r] = sum;
         }
         float *dst = join + (warp * kRows + r) * C::kPitch + g * (D / 8);
+        const float back = S * 0x1p10f, z = oz[ni][j];
 #pragma unroll
         for (int k = 0; k < kMTiles; k += 2)
-          *reinterpret_cast<float4 *>(dst + 2 * k) =
-              make_float4(o[ni][k][j] * S, o[ni][k][2 + j] * S, o[ni][k + 1][j] * S, o[ni][k + 1][2 + j] * S);
+          *reinterpret_cast<float4 *>(dst + 2 * k) = make_float4(
+              (o[ni][k][j] - z) * back, fmaf(o[ni][k][2 + j], kHighToLow, -z) * back, (o[ni][k + 1][j] - z) * back,
+              fmaf(o[ni][k + 1][2 + j], kHighToLow, -z) * back);
       }
-    named_bar_sync(1, 32 * kKvWarps);
+    __syncthreads();
     const bool cut = w.count < w.r.tiles;
     const int64_t seg_end = w.seg_first + w.r.tiles;
     // parts of the segment: the blocks that hold units of it
@@ -577,14 +611,14 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
       if (d0 == 0) mine[kRows * D + 2 * r] = mx, mine[kRows * D + 2 * r + 1] = sum;
       const int c0 = block_of(w.seg_first), c1 = block_of(seg_end - 1);
       __threadfence();
-      named_bar_sync(1, 32 * kKvWarps);
+      __syncthreads();
       if (tid == 0) {
         // a block's end cuts one segment at most, so the first block of a segment names its counter
         const uint32_t before = atom_add_acq_rel_gpu_u32(counters + c0, 1u);
         last_here = before == static_cast<uint32_t>(c1 - c0);
         if (last_here) counters[c0] = 0;
       }
-      named_bar_sync(1, 32 * kKvWarps);
+      __syncthreads();
       writes = last_here;
       if (writes) {
         __threadfence();
@@ -612,7 +646,7 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
       if (a.lse && d0 == 0)
         a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
     }
-    named_bar_sync(1, 32 * kKvWarps);  // the join buffer is free again
+    __syncthreads();  // the join buffer is free again
   }
 }
 

@@ -64,7 +64,16 @@ def attention(q, codes, meta, table, kv_lens, cu_q, scale, causal, bad_pages=())
         relative error in p of at most e = (D + 16) 2^-24 max_t sum |q k| scale +
         2^-20, which moves numerator and denominator by e A and e |o|;
       * the remaining fp32 sums over n terms (in tiles of 16 and a few parts)
-        by (n / 16 + 64) 2^-24 A at most."""
+        by (n / 16 + 64) 2^-24 A at most;
+      * the sum of p s (code - z) is taken as sum p s code - sum p s z, each of
+        non-negative terms and at most 15 B, B = sum p s / sum p: where code = z
+        carries nearly all the weight, A is far below B.  A tensor-core step
+        adds 16 products to the running sum: aligning them to the largest one's
+        exponent drops at most 2^-17 of the largest p s, in units of a code (24 bits
+        below a product of up to 2^4 codes, with a factor 2^2 for the
+        unnormalized high nibbles and one 2^1 for the addends), and the sum is
+        cut to 24 bits, 2^-23 of up to 15 B; n / 16 + 1 steps, two sums:
+        2 (2^-17 + (n / 16 + 1) 15 2^-23) B."""
     T, Hq, D = q.shape
     H, page = codes.shape[2], codes.shape[3]
     g = Hq // H
@@ -103,5 +112,6 @@ def attention(q, codes, meta, table, kv_lens, cu_q, scale, causal, bad_pages=())
                 small = (p * sv < 2.0 ** -14 * big).sum()
                 e = (D + 16) * 2.0 ** -24 * float(((k.abs() @ x.abs()) * abs(scale)).max()) + 2.0 ** -20
                 tol[first + i, h] = (2.0 ** -11 * (A + o.abs()) + 2.0 ** -25 + small * 2.0 ** -25 * 15 * big / p.sum()
-                                     + e * (A + o.abs()) + (see / 16 + 64) * 2.0 ** -24 * A)
+                                     + e * (A + o.abs()) + (see / 16 + 64) * 2.0 ** -24 * A
+                                     + 2 * (2.0 ** -17 + (see / 16 + 1) * 15 * 2.0 ** -23) * (w @ sv))
     return out, lse, tol
