@@ -22,16 +22,19 @@ namespace mixllm {
 // Few queries per request (decode).  HBM-bound: 2 * (D/2 + 4) bytes per cached
 // token and head.
 //
-// Work is cut into units of 256 tokens of one (request, row tile, key head);
-// block c takes the units [c U / P, (c + 1) U / P) of their concatenation, so
-// requests of any lengths load every SM alike, and the lengths stay on the
-// device.  A row tile is 8 NT rows (query token, query head of the group).
-// Within a block each of eight warps takes 32 tokens of every unit and fetches
-// them itself, by cp.async into stages of its own, with no barrier between
-// warps until a segment ends.  Tokens are the 16-row side of m16n8k16 and the
-// query rows its 8-column side, so that a group of 8 heads fills the
-// instruction and smaller ones waste only tensor work: S^T = K Q^T with K as
-// the A operand, then O^T = V^T P^T with V^T as A.
+// Work is cut into units of 32 tokens of one (request, row tile, key head);
+// block c takes the units [c U / P, (c + 1) U / P) of their concatenation and
+// its eight warps an eighth of them each, so requests of any lengths load every
+// SM alike, and the lengths stay on the device.  A row tile is 8 NT rows (query
+// token, query head of the group).  A warp fetches its tokens itself, by
+// cp.async into stages of its own, and meets the others only when all of the
+// block's units are done: the latencies where one request or head ends and the
+// next begins are then one warp's in sixteen, and few (with 256-token units
+// shared by the block's warps, every such step was a barrier for all of them:
+// 97 us instead of 66 for 64 requests of about 4100 tokens).  Tokens are the
+// 16-row side of m16n8k16 and the query rows its 8-column side, so that a group
+// of 8 heads fills the instruction and smaller ones waste only tensor work:
+// S^T = K Q^T with K as the A operand, then O^T = V^T P^T with V^T as A.
 //
 // What bounds the loop on the way to HBM speed is the unpacking: integer
 // instructions issue at half rate.  So one AND per pair of codes makes fp16
@@ -61,31 +64,32 @@ namespace mixllm {
 // maximum of s_v (moved when passed by a factor of 4); the accumulators hold
 // O / S.  p s_v is rounded once, to fp16's 11 bits; sums stay in fp32.
 //
-// At a segment's end the eight warps' (m, S, l, O) are joined in shared
-// memory; a segment cut between blocks leaves its parts in the workspace and
-// the last block to arrive adds them in the order of the tokens, so the result
-// does not depend on timing.
+// A segment (the units of one request, row tile and head) that one warp holds
+// whole is written by it.  Parts of one that is cut between warps are joined by
+// the block at its end, and those cut between blocks left in the workspace,
+// where the last block to arrive adds them; always in the order of the tokens,
+// so the result does not depend on timing.
 // ---------------------------------------------------------------------------
-constexpr int kKvWarps = 8;
-constexpr int kKvThreads = 32 * kKvWarps;
-constexpr int kKvTile = 32 * kKvWarps;  // tokens per unit
+constexpr int kKvTile = 32;  // tokens per unit
+constexpr int kKvJoinThreads = 256;
 constexpr float kKvNoMax = -3.0e38f;
 
 template <int D, int NT>
 struct KvCfg {
+  static constexpr int kWarps = NT == 1 ? 16 : 8;  // by registers: 128 and 255 a thread
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NT;
   static constexpr int kRowBytes = D / 2;
   static constexpr int kCodes = 32 * kRowBytes;  // bytes of 32 tokens' key (or value) codes
   static constexpr int kStage = 2 * (kCodes + 32 * 4);
-  static constexpr int kStages = D == 128 && NT == 1 ? 2 : 4;
+  static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kRing = kStages * kStage;  // of one warp
-  static constexpr int kPitch = D + 4;            // floats per row of the join buffer
-  static constexpr int kJoin = kKvWarps * kRows * kPitch * 4;
-  static constexpr int kBlocksPerSm = NT == 1 ? 2 : 1;
-  static constexpr int kSmem = kKvWarps * kRing + kJoin + 2 * kKvWarps * kRows * 4;
-  static_assert(kBlocksPerSm * (kSmem + 2048) <= 228 * 1024, "resident blocks per SM");
+  static constexpr int kPart = kRows * (D + 2);   // floats of one part: sums, then (m, l) per row
+  static constexpr int kSmem = kWarps * kRing;
+  static_assert(kWarps * kPart * 4 <= kSmem, "the warps' last parts take the ring's place");
+  static_assert(kSmem + 4096 <= 227 * 1024, "shared memory of a block");
 };
-constexpr int kKvMaxGrid = 2 * 148;
+constexpr int kKvMaxGrid = 148;
 
 // One request's share of the work.
 struct KvReq {
@@ -109,11 +113,11 @@ __device__ __forceinline__ KvReq kv_req(const AttendArgs &a, int b, int rows_per
   return r;
 }
 
-// Walks a block's units as segments: runs of units of one (request, row tile,
+// Walks a warp's units as segments: runs of units of one (request, row tile,
 // key head).
 struct KvWalk {
-  int b, rt, h, tile, count;  // the segment: its first unit's tile and its units in this block
-  int64_t left;               // units of the block from the segment's first on
+  int b, rt, h, tile, count;  // the segment: its first unit's tile and its units in this warp
+  int64_t left;               // units of the warp from the segment's first on
   int64_t seg_first;          // unit index of the whole segment's first tile
   KvReq r;
 
@@ -137,7 +141,7 @@ struct KvWalk {
   }
 };
 
-// A warp's fetching: 32 tokens of each of its block's units in turn, codes and
+// A warp's fetching: the 32 tokens of its units in turn, codes and
 // metadata, into the next stage of its ring.  Half a warp copies 16 tokens:
 // a page holds a multiple of 16, so they lie in one.
 template <typename C>
@@ -158,13 +162,13 @@ struct KvFetch {
     batch = -1;
   }
 
-  __device__ __forceinline__ void unit(const AttendArgs &a, int warp, int lane) {
+  __device__ __forceinline__ void unit(const AttendArgs &a, int lane) {
     if (left > 0) {
       const int page_log2 = a.cache.page_log2;
       if ((tile >> 4) != batch) {
-        // the pages of the warp's tokens in 16 units: lane 2u + i has unit u's half i
+        // the pages of 16 units: lane 2u + i has unit u's half i
         batch = tile >> 4;
-        const int64_t token = (static_cast<int64_t>(batch) << 4) * kKvTile + (lane >> 1) * kKvTile + 32 * warp + 16 * (lane & 1);
+        const int64_t token = (static_cast<int64_t>(batch) * 32 + lane) * 16;
         id = -1;
         if (token < r.kv) {
           id = a.table[static_cast<int64_t>(b) * a.table_stride + (token >> page_log2)];
@@ -178,7 +182,7 @@ struct KvFetch {
       const uint32_t halves = __ballot_sync(0xFFFFFFFFu, page >= 0);
       present = (present & ~(3u << 2 * stage)) | ((halves & 1u) | (halves >> 30 & 2u)) << 2 * stage;
       if (page >= 0) {
-        const int row = (tile * kKvTile + 32 * warp + (lane & 16)) & ((1 << page_log2) - 1);
+        const int row = (tile * kKvTile + (lane & 16)) & ((1 << page_log2) - 1);
         const int64_t at = static_cast<int64_t>(page) * (2 * a.cache.H << page_log2) + ((h << page_log2) + row);
         const int64_t to_value = static_cast<int64_t>(a.cache.H) << page_log2;  // rows from a key to its value
         const uint8_t *k = a.cache.codes + at * C::kRowBytes + (lane & 15) * 16;
@@ -250,81 +254,171 @@ __device__ __forceinline__ uint32_t low_codes(uint32_t w) {
 __device__ __forceinline__ uint32_t high_codes(uint32_t w) { return w & 0x00F000F0u; }
 constexpr float kHighToLow = 0x1p10f;
 
+// A segment's place, for who joins its parts.
+struct KvSeg {
+  int rt, h, tiles, q0, n;
+};
+
+// Joining parts: a thread holds kCh channels of one row.  The 32 or 16
+// neighbouring lanes that share a row hold the weights of as many parts.
 template <int D, int NT>
-__global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_decode_kernel(const AttendArgs a,
-                                                                                          uint32_t *__restrict__ counters,
-                                                                                          float *__restrict__ parts) {
+struct KvRow {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kThreadsPerRow = kKvJoinThreads / kRows;  // 32 or 16
+  static constexpr int kCh = D / kThreadsPerRow;             // 2, 4 or 8
+  int r, d0;
+  float top, sum, acc[kCh];
+
+  __device__ __forceinline__ void clear() {
+    r = threadIdx.x / kThreadsPerRow, d0 = threadIdx.x % kThreadsPerRow * kCh;
+    top = kKvNoMax;
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kCh; ++k) acc[k] = 0.0f;
+  }
+  static __device__ __forceinline__ float max_lanes(float v) {
+#pragma unroll
+    for (int x = kThreadsPerRow / 2; x > 0; x >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, x));
+    return v;
+  }
+  static __device__ __forceinline__ float sum_lanes(float v) {
+#pragma unroll
+    for (int x = kThreadsPerRow / 2; x > 0; x >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, x);
+    return v;
+  }
+  template <bool kGlobal>
+  __device__ __forceinline__ void add(const float *part, float f) {
+#pragma unroll
+    for (int k = 0; k < kCh; k += 2) {
+      const float2 *from = reinterpret_cast<const float2 *>(part + r * D + d0 + k);
+      const float2 v = kGlobal ? __ldcg(from) : *from;
+      acc[k] = fmaf(v.x, f, acc[k]), acc[k + 1] = fmaf(v.y, f, acc[k + 1]);
+    }
+  }
+  __device__ __forceinline__ void leave(float *part) {
+#pragma unroll
+    for (int k = 0; k < kCh; k += 2) *reinterpret_cast<float2 *>(part + r * D + d0 + k) = make_float2(acc[k], acc[k + 1]);
+    if (d0 == 0) *reinterpret_cast<float2 *>(part + kRows * D + 2 * r) = make_float2(top, sum);
+  }
+  __device__ __forceinline__ void write(const AttendArgs &a, const KvSeg &g) {
+    const int group = a.Hq / a.cache.H, row = g.rt * kRows + r;
+    if (row >= g.n * group) return;
+    const int tok = row / group, head = g.h * group + row - tok * group;
+    const int64_t token = static_cast<int64_t>(g.q0) + tok;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row that saw no key is zero
+    __half *dst = a.out + token * a.out_stride + static_cast<int64_t>(head) * D + d0;
+#pragma unroll
+    for (int k = 0; k < kCh; k += 2)
+      *reinterpret_cast<__half2 *>(dst + k) = __floats2half2_rn(acc[k] * inv, acc[k + 1] * inv);
+    if (a.lse && d0 == 0)
+      a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(const AttendArgs a,
+                                                                                          uint32_t *counters,
+                                                                                          float *block_parts,
+                                                                                          float *warp_parts) {
   using C = KvCfg<D, NT>;
-  constexpr int kRows = C::kRows;
+  constexpr int kRows = C::kRows, kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
-  float *join = reinterpret_cast<float *>(smem + kKvWarps * C::kRing);
-  float *join_m = join + kKvWarps * kRows * C::kPitch, *join_l = join_m + kKvWarps * kRows;
-  __shared__ int first_b, last_here;
-  __shared__ long long first_rem, warp_units[kKvWarps];
+  __shared__ int first_b[kWarps], join_blocks[2][2];
+  __shared__ uint64_t pace;
+  __shared__ volatile int abort_flag;
+  __shared__ KvSeg part_at[kWarps][2], cut_at[2];
+  // part_first: the segment (its first unit) of a part that a warp left, or -1:
+  // [0] in the workspace (behind its first segment), [1] in shared memory (its last one)
+  __shared__ long long first_rem[kWarps], warp_units[kWarps], part_first[kWarps][2], cut_first[2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.Hq / a.cache.H;
-  if (tid == 0) first_b = a.B;
-  __syncthreads();
+  if (tid == 0) {
+    mbar_init(&pace, kWarps);
+    fence_mbar_init();
+    abort_flag = 0;
+  }
+  if (tid < 2) cut_first[tid] = -1;
+  if (tid < kWarps) {
+    first_b[tid] = a.B;
+    part_first[tid][0] = part_first[tid][1] = -1;
+  }
 
-  // ---- this block's units
+  // ---- this block's units: a prefix sum over the requests, in chunks of one per thread
   int P = gridDim.x;
   const int c = blockIdx.x;
-  int64_t U = 0, start = 0;
-  auto units_of = [&](const KvReq &r) { return static_cast<long long>(r.tiles) * r.row_tiles * a.cache.H; };
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kKvThreads) {
-      const int b = b0 + tid;
-      const long long u = b < a.B ? units_of(kv_req(a, b, kRows)) : 0;
-      long long incl = u;
+  int64_t U = 0;
+  const int chunks = (a.B + kThreads - 1) / kThreads;
+  long long u = 0, incl = 0;
+  auto scan_chunk = [&](int chunk, int64_t base) {  // u, incl of request chunk * threads + tid; returns base + the chunk's sum
+    const int b = chunk * kThreads + tid;
+    u = 0;
+    if (b < a.B) {
+      const KvReq r = kv_req(a, b, kRows);
+      u = static_cast<long long>(r.tiles) * r.row_tiles * a.cache.H;
+    }
+    incl = u;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (lane == 31) warp_units[warp] = incl;
-      __syncthreads();
-      long long before = base;
-      for (int w = 0; w < kKvWarps; ++w) {
-        if (w < warp) before += warp_units[w];
-        base += warp_units[w];
-      }
-      incl += before;
-      if (pass == 1 && u > 0 && start >= incl - u && start < incl) {
-        first_b = b;
-        first_rem = start - (incl - u);
-      }
-      __syncthreads();
-      if (pass == 1 && base > start) break;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
     }
-    if (pass == 0) {
-      U = base;
-      if (U < P) P = static_cast<int>(U);  // every block that takes part has a unit
-      if (c >= P) return;
-      start = U / P * c + U % P * c / P;
+    if (lane == 31) warp_units[warp] = incl;
+    __syncthreads();
+    incl += base;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) {
+      if (x < warp) incl += warp_units[x];
+      base += warp_units[x];
+    }
+    __syncthreads();
+    return base;
+  };
+  for (int k = 0; k < chunks; ++k) U = scan_chunk(k, U);
+  if (U < static_cast<int64_t>(P) * kWarps) P = static_cast<int>(U + kWarps - 1) / kWarps;
+  if (c >= P) return;  // every other block has a unit
+  const int64_t share = U < 1ll << 32 ? static_cast<uint32_t>(U) / static_cast<uint32_t>(P) : U / P;
+  const int rest = static_cast<int>(U - share * P);
+  const auto block_start = [&](int b) { return share * b + rest * b / P; };  // rest, b < 2^10
+  const int64_t start = block_start(c);
+  const int64_t mine = block_start(c + 1) - start;
+  const auto warp_start = [&](int x) { return start + mine * x / kWarps; };
+  int64_t base = 0;
+  for (int k = 0; k < chunks && base <= warp_start(kWarps - 1); ++k) {
+    if (chunks > 1) base = scan_chunk(k, base);
+    else base = U;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) {
+      const int64_t at = warp_start(x);
+      if (at >= incl - u && at < incl) {
+        first_b[x] = k * kThreads + tid;
+        first_rem[x] = at - (incl - u);
+      }
     }
   }
-  const int64_t end = U / P * (c + 1) + U % P * (c + 1) / P;
+  __syncthreads();
+  const int64_t my_start = warp_start(warp), my_end = warp_start(warp + 1);
   KvWalk w0;
-  w0.b = first_b;
-  w0.left = end - start;
-  if (w0.left <= 0 || w0.b >= a.B) return;
-  w0.r = kv_req(a, w0.b, kRows);
-  {
-    const int64_t per_rt = static_cast<int64_t>(w0.r.tiles) * a.cache.H;
-    w0.rt = static_cast<int>(first_rem / per_rt);
-    const int64_t rem = first_rem - w0.rt * per_rt;
-    w0.h = static_cast<int>(rem / w0.r.tiles);
-    w0.tile = static_cast<int>(rem - static_cast<int64_t>(w0.h) * w0.r.tiles);
+  w0.b = first_b[warp];
+  w0.left = w0.b < a.B ? my_end - my_start : 0;
+  w0.rt = w0.h = w0.tile = 0;
+  w0.r = KvReq{0, 0, 0, 0, 0};
+  if (w0.left > 0) {
+    w0.r = kv_req(a, w0.b, kRows);
+    const int64_t seg = first_rem[warp] < 1ll << 32
+                            ? static_cast<uint32_t>(first_rem[warp]) / static_cast<uint32_t>(w0.r.tiles)
+                            : first_rem[warp] / w0.r.tiles;
+    w0.tile = static_cast<int>(first_rem[warp] - seg * w0.r.tiles);
+    w0.rt = static_cast<int>(seg / a.cache.H);
+    w0.h = static_cast<int>(seg - static_cast<int64_t>(w0.rt) * a.cache.H);
   }
-  w0.seg_first = start - w0.tile;
+  w0.seg_first = my_start - w0.tile;
   w0.settle(a, kRows);
 
   KvFetch<C> fetch;
   fetch.start(w0, lane, smem + warp * C::kRing);
 #pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) fetch.unit(a, warp, lane);
+  for (int i = 0; i < C::kStages - 1; ++i) fetch.unit(a, lane);
 
   const int g = lane >> 2, t = lane & 3;
   // accumulator row r of the score tile is token r ^ (r >> 1 & 1): the value
@@ -338,6 +432,38 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
   const uint8_t *ring = smem + warp * C::kRing;
   int stage = 0;
 
+  float o[NT][kMTiles][4], oz[NT][4];  // oz: sums of p z, the same in every row
+  float m[NT][2], l[NT][2];
+  float S, inv_S;
+  // this warp's part of a segment: S O, and (m, l) per row
+  const auto leave = [&](float *part) {
+#pragma unroll
+    for (int ni = 0; ni < NT; ++ni)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = ni * 8 + 2 * t + j;
+        const float back = S * 0x1p10f, z = oz[ni][j];
+        float *dst = part + r * D + g * (D / 8);
+#pragma unroll
+        for (int k = 0; k < kMTiles; k += 2)
+          *reinterpret_cast<float4 *>(dst + 2 * k) = make_float4(
+              (o[ni][k][j] - z) * back, fmaf(o[ni][k][2 + j], kHighToLow, -z) * back, (o[ni][k + 1][j] - z) * back,
+              fmaf(o[ni][k + 1][2 + j], kHighToLow, -z) * back);
+        if (g == 0) *reinterpret_cast<float2 *>(part + kRows * D + 2 * r) = make_float2(m[ni][j], l[ni][j]);
+      }
+  };
+  // Warps keep in step: none begins its step s + 1 before all have begun step s.
+  // The scheduler prefers the older of two ready warps; left alone, half of an
+  // SM's warps end at 0.8 of the time and the rest run on with too few to hide
+  // their latencies.  (A wait that gives up costs speed only.)
+  int step = 0;
+  const int steps = static_cast<int>(warp_start(kWarps) - warp_start(kWarps - 1));  // the last warp has the most
+  const auto keep_pace = [&] {
+    if (step > 0) warp_wait(&pace, (step - 1) & 1, &abort_flag);
+    if (lane == 0) mbar_arrive(&pace);
+    ++step;
+  };
+  bool in_registers = false;  // the last segment's part, cut at one of the warp's ends
   for (KvWalk w = w0; w.left > 0; w.next(a, kRows)) {
     const int rows = w.r.n * group;
     const int row0 = w.rt * kRows;
@@ -383,9 +509,7 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
     const int last_row = min(rows, row0 + kRows) - 1;
     const int lim_max = a.causal ? w.r.kv - w.r.n + last_row / group + 1 : w.r.kv;
 
-    float o[NT][kMTiles][4], oz[NT][4];  // oz: sums of p z, the same in every row
-    float m[NT][2], l[NT][2];
-    float S = 0x1p-24f, inv_S = 0x1p24f;
+    S = 0x1p-24f, inv_S = 0x1p24f;
 #pragma unroll
     for (int ni = 0; ni < NT; ++ni) {
       m[ni][0] = m[ni][1] = kKvNoMax;
@@ -396,11 +520,12 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
     }
 
     for (int i = 0; i < w.count; ++i) {
-      const int base = (w.tile + i) * kKvTile + 32 * warp;
+      const int base = (w.tile + i) * kKvTile;
+      keep_pace();
       cp_async_wait<C::kStages - 2>();
       __syncwarp();  // every lane's copies of this stage are here, and every lane is done with the stage before
       const uint32_t have = fetch.present >> 2 * stage & 3u;
-      fetch.unit(a, warp, lane);
+      fetch.unit(a, lane);
       const uint8_t *st = ring + stage * C::kStage;
       if (++stage == C::kStages) stage = 0;
       if (base >= lim_max || have == 0) continue;  // nothing of these 32 tokens is seen
@@ -559,94 +684,141 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
       }
     }
 
-    // ---- join the warps: each brings (m, l, S O) per row
+    // ---- the segment's end, or the warp's
 #pragma unroll
     for (int ni = 0; ni < NT; ++ni)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float sum = l[ni][j];
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-        const int r = ni * 8 + 2 * t + j;
-        if (g == 0) {
-          join_m[warp * kRows + r] = m[ni][j];
-          join_l[warp * kRows + r] = sum;
+        for (int x = 4; x < 32; x <<= 1) l[ni][j] += __shfl_xor_sync(0xFFFFFFFFu, l[ni][j], x);
+    if (w.count == w.r.tiles) {
+#pragma unroll
+      for (int ni = 0; ni < NT; ++ni)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = row0 + ni * 8 + 2 * t + j;
+          if (r >= rows) continue;
+          const int tok = r / group, head = w.h * group + r - tok * group;
+          const int64_t token = static_cast<int64_t>(w.r.q0) + tok;
+          const float inv = l[ni][j] == 0.0f ? 0.0f : S * 0x1p10f / l[ni][j];  // a row that saw no key is zero
+          const float z = oz[ni][j];
+          uint32_t packed[kMTiles];
+#pragma unroll
+          for (int k = 0; k < kMTiles; ++k)
+            packed[k] = half2_bits((o[ni][k][j] - z) * inv, fmaf(o[ni][k][2 + j], kHighToLow, -z) * inv);
+          uint4 *dst = reinterpret_cast<uint4 *>(a.out + token * a.out_stride + static_cast<int64_t>(head) * D + g * (D / 8));
+#pragma unroll
+          for (int k = 0; k < kMTiles; k += 4) dst[k / 4] = make_uint4(packed[k], packed[k + 1], packed[k + 2], packed[k + 3]);
+          if (a.lse && g == 0)
+            a.lse[token * a.Hq + head] = l[ni][j] == 0.0f ? -INFINITY : (m[ni][j] + log2f(l[ni][j])) * 0.6931471805599453f;
         }
-        float *dst = join + (warp * kRows + r) * C::kPitch + g * (D / 8);
-        const float back = S * 0x1p10f, z = oz[ni][j];
-#pragma unroll
-        for (int k = 0; k < kMTiles; k += 2)
-          *reinterpret_cast<float4 *>(dst + 2 * k) = make_float4(
-              (o[ni][k][j] - z) * back, fmaf(o[ni][k][2 + j], kHighToLow, -z) * back, (o[ni][k + 1][j] - z) * back,
-              fmaf(o[ni][k + 1][2 + j], kHighToLow, -z) * back);
+    } else {
+      in_registers = w.count == w.left;
+      const int side = in_registers ? 1 : 0;
+      if (!in_registers) leave(warp_parts + (c * kWarps + warp) * C::kPart);
+      if (lane == 0) {
+        part_first[warp][side] = w.seg_first;
+        part_at[warp][side] = KvSeg{w.rt, w.h, w.r.tiles, w.r.q0, w.r.n};
       }
-    __syncthreads();
-    const bool cut = w.count < w.r.tiles;
-    const int64_t seg_end = w.seg_first + w.r.tiles;
-    // parts of the segment: the blocks that hold units of it
-    const auto block_of = [&](int64_t u) { return static_cast<int>(((u + 1) * P - 1) / U); };
-    const auto block_start = [&](int b) { return U / P * b + U % P * b / P; };
-    const int part_floats = kRows * (D + 2);
-    const auto part_of = [&](int b) {
-      return parts + (static_cast<int64_t>(b) * 2 + (block_start(b) <= w.seg_first ? 1 : 0)) * part_floats;
-    };
-    constexpr int kLanesPerRow = 32 * kKvWarps / kRows;  // threads of one row
-    constexpr int kCh = D / kLanesPerRow;                // channels of one thread
-    const int r = tid / kLanesPerRow, d0 = (tid % kLanesPerRow) * kCh;
-    float mx = kKvNoMax, sum = 0.0f, acc[kCh];
-#pragma unroll
-    for (int k = 0; k < kCh; ++k) acc[k] = 0.0f;
-    for (int x = 0; x < kKvWarps; ++x) mx = fmaxf(mx, join_m[x * kRows + r]);
-    for (int x = 0; x < kKvWarps; ++x) {
-      const float f = ex2(join_m[x * kRows + r] - mx);
-      sum += join_l[x * kRows + r] * f;
-#pragma unroll
-      for (int k = 0; k < kCh; ++k) acc[k] += join[(x * kRows + r) * C::kPitch + d0 + k] * f;
     }
-    bool writes = true;
-    if (cut) {
-      float *mine = part_of(c);
-#pragma unroll
-      for (int k = 0; k < kCh; ++k) mine[r * D + d0 + k] = acc[k];
-      if (d0 == 0) mine[kRows * D + 2 * r] = mx, mine[kRows * D + 2 * r + 1] = sum;
-      const int c0 = block_of(w.seg_first), c1 = block_of(seg_end - 1);
-      __threadfence();
-      __syncthreads();
+  }
+  while (step < steps) keep_pace();
+  float *last_parts = reinterpret_cast<float *>(smem);
+  __threadfence_block();
+  __syncthreads();  // no warp needs its ring any more
+  if (in_registers) leave(last_parts + warp * C::kPart);
+  __syncthreads();
+
+  // ---- the block's parts, segment by segment; lane i looks after part i.
+  // A segment's parts are neighbours among those that there are.
+  constexpr int kLanes = 2 * kWarps;  // and as many lanes share a row
+  static_assert(kLanes == KvRow<D, NT>::kThreadsPerRow, "one part per lane of a row");
+  if (warp >= kKvJoinThreads / 32) return;
+  const int me = lane & (kLanes - 1);
+  constexpr uint32_t kAll = kLanes == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+  const int64_t part_seg = part_first[me >> 1][me & 1];
+  const uint32_t there = __ballot_sync(0xFFFFFFFFu, part_seg >= 0) & kAll;
+  const uint32_t before_me = there & ((1u << me) - 1u);
+  const int64_t seg_before = __shfl_sync(0xFFFFFFFFu, part_seg, before_me ? 31 - __clz(before_me) : 0);
+  uint32_t firsts = __ballot_sync(0xFFFFFFFFu, part_seg >= 0 && (!before_me || seg_before != part_seg)) & kAll;
+  const float *my_part = me & 1 ? last_parts + (me >> 1) * C::kPart : warp_parts + (c * kWarps + (me >> 1)) * C::kPart;
+  while (firsts) {
+    const int first = __ffs(firsts) - 1;
+    firsts &= firsts - 1;
+    uint32_t these = there & ~((1u << first) - 1u);
+    if (firsts) these &= (firsts & -firsts) - 1u;
+    const int64_t seg_first = part_first[first >> 1][first & 1];
+    const KvSeg seg = part_at[first >> 1][first & 1];
+    KvRow<D, NT> row;
+    row.clear();
+    const bool in = these >> me & 1u;
+    const float2 ml = in ? *reinterpret_cast<const float2 *>(my_part + kRows * D + 2 * row.r) : make_float2(kKvNoMax, 0.0f);
+    row.top = row.max_lanes(ml.x);
+    const float f = in ? ex2(ml.x - row.top) : 0.0f;
+    row.sum = row.sum_lanes(ml.y * f);
+#pragma unroll 1
+    for (; these; these &= these - 1) {
+      const int i = __ffs(these) - 1;
+      row.template add<false>(i & 1 ? last_parts + (i >> 1) * C::kPart : warp_parts + (c * kWarps + (i >> 1)) * C::kPart,
+                              __shfl_sync(0xFFFFFFFFu, f, i, kLanes));
+    }
+    if (seg_first >= start && seg_first + seg.tiles <= start + mine) {
+      row.write(a, seg);
+    } else {
+      const int side = start <= seg_first ? 1 : 0;  // the block's end cuts it, or its beginning
+      row.leave(block_parts + (c * 2 + side) * C::kPart);
       if (tid == 0) {
-        // a block's end cuts one segment at most, so the first block of a segment names its counter
-        const uint32_t before = atom_add_acq_rel_gpu_u32(counters + c0, 1u);
-        last_here = before == static_cast<uint32_t>(c1 - c0);
-        if (last_here) counters[c0] = 0;
-      }
-      __syncthreads();
-      writes = last_here;
-      if (writes) {
-        __threadfence();
-        mx = kKvNoMax, sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kCh; ++k) acc[k] = 0.0f;
-        for (int b = c0; b <= c1; ++b) mx = fmaxf(mx, __ldcg(part_of(b) + kRows * D + 2 * r));
-        for (int b = c0; b <= c1; ++b) {
-          const float *p = part_of(b);
-          const float f = ex2(__ldcg(p + kRows * D + 2 * r) - mx);
-          sum += __ldcg(p + kRows * D + 2 * r + 1) * f;
-#pragma unroll
-          for (int k = 0; k < kCh; ++k) acc[k] += __ldcg(p + r * D + d0 + k) * f;
-        }
+        cut_first[side] = seg_first;
+        cut_at[side] = seg;
       }
     }
-    if (writes && row0 + r < rows) {
-      const int tok = (row0 + r) / group, head = w.h * group + (row0 + r) % group;
-      const int64_t token = static_cast<int64_t>(w.r.q0) + tok;
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row that saw no key is zero
-      __half *dst = a.out + token * a.out_stride + static_cast<int64_t>(head) * D + d0;
-#pragma unroll
-      for (int k = 0; k < kCh; k += 2)
-        *reinterpret_cast<__half2 *>(dst + k) = __floats2half2_rn(acc[k] * inv, acc[k + 1] * inv);
-      if (a.lse && d0 == 0)
-        a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+  }
+
+  // ---- segments cut between blocks: the last block to get here joins the parts
+  named_bar_sync(1, kKvJoinThreads);
+  if (tid < 2) {
+    join_blocks[tid][1] = -1;
+    if (cut_first[tid] >= 0) {
+      // blocks that hold units of the segment: the one with unit x is ((x + 1) P - 1) / U
+      const int c0 = static_cast<int>(((cut_first[tid] + 1) * P - 1) / U);
+      const int c1 = static_cast<int>(((cut_first[tid] + cut_at[tid].tiles) * P - 1) / U);
+      // a block's end cuts one segment at most, so the first block of a segment names its counter
+      __threadfence();
+      const uint32_t before = atom_add_acq_rel_gpu_u32(counters + c0, 1u);
+      if (before == static_cast<uint32_t>(c1 - c0)) {
+        counters[c0] = 0;
+        join_blocks[tid][0] = c0;
+        join_blocks[tid][1] = c1;
+      }
     }
-    __syncthreads();  // the join buffer is free again
+  }
+  named_bar_sync(1, kKvJoinThreads);
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const int c0 = join_blocks[side][0], c1 = join_blocks[side][1];
+    if (c1 < 0) continue;
+    __threadfence();
+    KvRow<D, NT> row;
+    row.clear();
+    // the segment is the first block's last one and every other's first one
+    const auto part_of = [&](int b) { return block_parts + (b * 2 + (b == c0 ? 1 : 0)) * C::kPart; };
+    float top = kKvNoMax;
+    for (int b = c0 + me; b <= c1; b += kLanes) top = fmaxf(top, __ldcg(part_of(b) + kRows * D + 2 * row.r));
+    row.top = row.max_lanes(top);
+    float sum = 0.0f;
+    for (int b0 = c0; b0 <= c1; b0 += kLanes) {
+      float f = 0.0f;
+      if (b0 + me <= c1) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_of(b0 + me) + kRows * D + 2 * row.r));
+        f = ex2(ml.x - row.top);
+        sum = fmaf(ml.y, f, sum);
+      }
+      const int n = min(kLanes, c1 - b0 + 1);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) row.template add<true>(part_of(b0 + i), __shfl_sync(0xFFFFFFFFu, f, i, kLanes));
+    }
+    row.sum = row.sum_lanes(sum);
+    row.write(a, cut_at[side]);
   }
 }
 
@@ -658,13 +830,13 @@ __global__ void __launch_bounds__(kKvThreads, KvCfg<D, NT>::kBlocksPerSm) kv4_de
 static int kv4_decode_nt(int max_q, int group) { return static_cast<int64_t>(max_q) * group > 8 ? 2 : 1; }
 
 // Workspace: one counter per block, always in the same place, then the parts
-// of cut segments (two per block), which need no initial value.
+// of cut segments (two per block, one per warp), which need no initial value.
 constexpr size_t kKvCounterBytes = 4096;
 static_assert(kKvMaxGrid * sizeof(uint32_t) <= kKvCounterBytes, "one counter per block");
 
 size_t kv4_attention_workspace_bytes(int, int max_q, int Hq, int H, int D, int, int) {
   const int rows = 8 * kv4_decode_nt(max_q, Hq / H);
-  return kKvCounterBytes + static_cast<size_t>(kKvMaxGrid) * 2 * rows * (D + 2) * sizeof(float);
+  return kKvCounterBytes + static_cast<size_t>(kKvMaxGrid) * (2 + 16) * rows * (D + 2) * sizeof(float);
 }
 
 template <int D, int NT>
@@ -687,11 +859,12 @@ static cudaError_t launch_kv4_decode(const AttendArgs &a, void *ws, cudaStream_t
   const int64_t tiles = ((static_cast<int64_t>(a.W) << a.cache.page_log2) + kKvTile - 1) / kKvTile;
   const int64_t row_tiles = (static_cast<int64_t>(a.max_q) * (a.Hq / a.cache.H) + C::kRows - 1) / C::kRows;
   const int64_t units = a.B * row_tiles * a.cache.H * (tiles > 0 ? tiles : 1);
-  int64_t grid = static_cast<int64_t>(device_sm_count()) * C::kBlocksPerSm;
+  int64_t grid = device_sm_count();
   if (grid > kKvMaxGrid) grid = kKvMaxGrid;
-  if (grid > units) grid = units;
-  kern<<<static_cast<unsigned>(grid), kKvThreads, C::kSmem, stream>>>(
-      a, static_cast<uint32_t *>(ws), reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kKvCounterBytes));
+  if (grid > (units + C::kWarps - 1) / C::kWarps) grid = (units + C::kWarps - 1) / C::kWarps;
+  float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kKvCounterBytes);
+  kern<<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, stream>>>(a, static_cast<uint32_t *>(ws), parts,
+                                                                      parts + kKvMaxGrid * 2 * C::kPart);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) *msg = "launch of the decode attention failed";
   return e;
