@@ -834,13 +834,13 @@ static int kv4_decode_nt(int max_q, int group) { return static_cast<int64_t>(max
 constexpr size_t kKvCounterBytes = 4096;
 static_assert(kKvMaxGrid * sizeof(uint32_t) <= kKvCounterBytes, "one counter per block");
 
-size_t kv4_attention_workspace_bytes(int, int max_q, int Hq, int H, int D, int, int) {
-  const int rows = 8 * kv4_decode_nt(max_q, Hq / H);
+static size_t kv4_decode_workspace_bytes(int max_q, int group, int D) {
+  const int rows = 8 * kv4_decode_nt(max_q, group);
   return kKvCounterBytes + static_cast<size_t>(kKvMaxGrid) * (2 + 16) * rows * (D + 2) * sizeof(float);
 }
 
 template <int D, int NT>
-static cudaError_t launch_kv4_decode(const AttendArgs &a, void *ws, cudaStream_t stream,
+static cudaError_t launch_kv4_decode_type(const AttendArgs &a, void *ws, cudaStream_t stream,
                                      const char **msg) {
   using C = KvCfg<D, NT>;
   auto kern = kv4_decode_kernel<D, NT>;
@@ -870,11 +870,11 @@ static cudaError_t launch_kv4_decode(const AttendArgs &a, void *ws, cudaStream_t
   return e;
 }
 
-cudaError_t launch_kv4_attention(const AttendArgs &a, void *ws, cudaStream_t stream, const char **msg) {
+static cudaError_t launch_kv4_decode(const AttendArgs &a, void *ws, cudaStream_t stream, const char **msg) {
   const bool one = kv4_decode_nt(a.max_q, a.Hq / a.cache.H) == 1;
   if (a.cache.D == 128)
-    return one ? launch_kv4_decode<128, 1>(a, ws, stream, msg) : launch_kv4_decode<128, 2>(a, ws, stream, msg);
-  return one ? launch_kv4_decode<64, 1>(a, ws, stream, msg) : launch_kv4_decode<64, 2>(a, ws, stream, msg);
+    return one ? launch_kv4_decode_type<128, 1>(a, ws, stream, msg) : launch_kv4_decode_type<128, 2>(a, ws, stream, msg);
+  return one ? launch_kv4_decode_type<64, 1>(a, ws, stream, msg) : launch_kv4_decode_type<64, 2>(a, ws, stream, msg);
 }
 
 }  // namespace mixllm

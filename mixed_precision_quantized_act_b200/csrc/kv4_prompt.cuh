@@ -1,0 +1,767 @@
+// kv4_prompt.cuh -- attention of prompts (many query rows per request and key
+// head) over the paged 4-bit KV cache, on tcgen05.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <atomic>
+#include <cstdint>
+
+#include "gemm_w4w8a8.cuh"  // device_sm_count
+#include "kv4_attention.cuh"
+#include "launch.h"
+#include "ptx_sm100.cuh"
+
+namespace mixllm {
+
+// ---------------------------------------------------------------------------
+// Rows of a request and key head are (query token, query head of the group),
+// token by token.  A block takes 256 of them as two tiles of 128 and runs over
+// the cached tokens in tiles of 128:
+//   S = Q K^T      two 128 x 128 products, fp32 in tensor memory
+//   P = softmax    one thread per row; fp16, over S in tensor memory
+//   O += P V       A from tensor memory, accumulated there in fp32
+// Warps 0-3 and 4-7 are the softmax of either tile, warps 8-11 unpack keys and
+// values, warp 12 issues the products.  The two tiles take turns on the tensor
+// core while the other one's softmax runs.
+//
+// Unpacking: one thread per token.  A word's nibbles i and i + 4 become fp16
+// integers 1024 + n (or 1024 + 16 n) by one AND-OR, and code - z by one add (or
+// FMA with 1/16): exact.  Both operands are stored with the channels of each
+// eight in the order 0 4 1 5 2 6 3 7; Q is laid out in the same order, and the
+// output's columns are put back by the epilogue.  Keys are a K-major operand
+// (channels along K), values an MN-major one (channels along N), so both are rows
+// of tokens in the same 128-byte swizzle and nothing is transposed.
+//
+// Scales: a key's scale multiplies its column of S in the softmax, a value's
+// scale its column of P before the rounding to fp16 (the one rounding of the
+// weights).  The exponent's reference R is the running maximum plus the
+// logarithm of the largest value scale, both moved only when passed by 8 and 2
+// (in log2 units), so p s_v stays within 2^10; O is then rescaled in tensor
+// memory, which is rare.
+//
+// Bound by the tensor core (4 D flops per row and token) and, close behind, by
+// the exponentials: 16 a clock and SM make a 128 x 128 tile 1024 clocks, its two
+// products at D = 128 take 1024.  Blocks take equal shares of all (tile
+// pair, head, token tile) units in one sequence; the ends of a share cut a
+// pair's tokens in two, and the parts are joined as in the decode kernel.  The
+// sequence depends on lengths that only the device knows: a small kernel before
+// this one lists the pairs and the running sum of their tiles.
+// ---------------------------------------------------------------------------
+constexpr int kPmThreads = 512;
+constexpr int kPmTile = 128;
+constexpr int kPmRows = 256;
+constexpr int kPmMaxGrid = 148;
+constexpr int kPmScaleRing = 4;
+
+template <int D>
+struct PmCfg {
+  static constexpr int kPanel = 128 * 128;  // bytes of 128 rows of 64 channels
+  static constexpr int kOperand = D / 64 * kPanel;
+  static constexpr int kSmem = 6 * kOperand + kPmScaleRing * 2 * kPmTile * 4 + 1024;
+  static constexpr int64_t kPart = static_cast<int64_t>(kPmRows) * (D + 2);  // floats
+  static_assert(kSmem + 1024 <= 227 * 1024, "shared memory of a block");
+};
+
+// The list of tile pairs: (request, pair), and the token tiles before each.
+struct PmPlan {
+  int *entries;
+  int64_t *cum;  // [entries + 1]
+  int2 *ent;     // [entries]
+};
+
+constexpr int kPmPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPmPlanThreads) kv4_prompt_plan_kernel(const AttendArgs a, const PmPlan plan) {
+  extern __shared__ int pair_base[];  // pairs before each request
+  __shared__ long long warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = a.Hq / a.cache.H;
+  // exclusive sum of v over the block, plus `base`; moves base on by the block's sum
+  auto scan = [&](long long v, long long &base) {
+    long long incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long before = base + incl - v;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      base += warp_sum[w];
+    }
+    __syncthreads();
+    return before;
+  };
+  long long pairs = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPmPlanThreads) {
+    const int b = b0 + tid;
+    const long long n = b < a.B ? kv_req(a, b, kPmRows).row_tiles : 0;
+    const long long before = scan(n, pairs);
+    if (b < a.B) pair_base[b] = static_cast<int>(before);
+  }
+  __syncthreads();
+  const int E = static_cast<int>(pairs);
+  long long tiles = 0;
+  for (int e0 = 0; e0 < E; e0 += kPmPlanThreads) {
+    const int e = e0 + tid;
+    long long n = 0;
+    if (e < E) {
+      const int b = owner_of(pair_base, a.B, e), p = e - pair_base[b];
+      const KvReq r = kv_req(a, b, kPmRows);
+      const int last = min(r.n * group, (p + 1) * kPmRows) - 1;
+      const int seen = a.causal ? r.kv - r.n + last / group + 1 : r.kv;  // by the pair's last row, which sees most
+      n = max(1, (seen + kPmTile - 1) / kPmTile);
+      plan.ent[e] = make_int2(b, p);
+    }
+    const long long before = scan(n, tiles);
+    if (e < E) plan.cum[e] = before;
+  }
+  if (tid == 0) {
+    plan.cum[E] = tiles;
+    *plan.entries = E;
+  }
+}
+
+// Walks a block's units as segments: runs of token tiles of one pair and head.
+struct PmWalk {
+  int e, h, tile, count, tiles, pair, b;
+  int left;           // units of the block from the segment's first on
+  int64_t seg_first;  // unit index of the whole segment's first tile
+  int q0, n, kv;
+
+  __device__ __forceinline__ void load(const AttendArgs &a, const PmPlan &plan) {
+    const int2 v = plan.ent[e];
+    b = v.x, pair = v.y;
+    tiles = static_cast<int>(plan.cum[e + 1] - plan.cum[e]);
+    q0 = a.cu_q[b];
+    n = a.cu_q[b + 1] - q0;
+    kv = a.kv_lens[b];
+  }
+  __device__ __forceinline__ void next(const AttendArgs &a, const PmPlan &plan) {
+    left -= count;
+    seg_first += tiles;
+    tile = 0;
+    if (++h == a.cache.H) {
+      h = 0;
+      ++e;
+      if (left > 0) load(a, plan);
+    }
+    count = min(left, tiles);
+  }
+  __device__ __forceinline__ int rows(int group) const { return min(kPmRows, n * group - pair * kPmRows); }
+};
+
+// Instruction descriptor of tcgen05.mma kind::f16: fp16 operands, fp32
+// accumulator; A K-major, B K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D[tmem] (+)= A[smem] . B[smem], and with A in tensor memory (two fp16 per
+// 32-bit column).
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Descriptor of an MN-major operand in the 128-byte swizzle: rows (along K) of
+// 128 bytes (64 elements along MN), 8-row atoms `stride` apart along K
+// (1024 bytes), the next 64 elements along MN one panel further.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t panel) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(panel >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ uint64_t pack_f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ ulonglong2 lds_2x2f(const float *p) { return *reinterpret_cast<const ulonglong2 *>(p); }
+
+// Codes minus zero point of eight channels (order 0 4 1 5 2 6 3 7), exact.
+__device__ __forceinline__ uint4 unpack_codes(uint32_t w, uint32_t zlo, uint32_t zhi) {
+  const uint32_t x = w >> 8;
+  uint4 r;
+  asm("add.f16x2 %0, %1, %2;" : "=r"(r.x) : "r"((w & 0x000F000Fu) | 0x64006400u), "r"(zlo));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r.y) : "r"((w & 0x00F000F0u) | 0x64006400u), "r"(0x2C002C00u), "r"(zhi));
+  asm("add.f16x2 %0, %1, %2;" : "=r"(r.z) : "r"((x & 0x000F000Fu) | 0x64006400u), "r"(zlo));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r.w) : "r"((x & 0x00F000F0u) | 0x64006400u), "r"(0x2C002C00u), "r"(zhi));
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendArgs a, const PmPlan plan,
+                                                                 uint32_t *counters, float *parts) {
+  using C = PmCfg<D>;
+  constexpr int kPanel = C::kPanel, kOperand = C::kOperand;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t *q_s = smem, *k_s = smem + 2 * kOperand, *v_s = smem + 4 * kOperand;
+  float *k_scale = reinterpret_cast<float *>(smem + 6 * kOperand);  // [ring][128], to log2 units
+  float *v_scale = k_scale + kPmScaleRing * kPmTile;
+  __shared__ uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  __shared__ uint32_t seen[kPmScaleRing][4];   // bit t: token t's page exists
+  __shared__ float v_top[kPmScaleRing][4];     // largest value scales of 32 tokens each
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ int first_e;
+  __shared__ long long cut_first[2];
+  __shared__ int cut_seg[2][5];  // pair, head, q0, n, tiles
+  __shared__ int join_blocks[2][2];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = a.Hq / a.cache.H, H = a.cache.H;
+  const int c = blockIdx.x;
+  const int E = *plan.entries;
+  const int64_t U = plan.cum[E] * H;
+  const int P = U < gridDim.x ? static_cast<int>(U) : static_cast<int>(gridDim.x);
+  if (c >= P) return;  // every other block has a unit
+  const int64_t share = U / P;
+  const int rest = static_cast<int>(U - share * P);
+  const auto block_start = [&](int b) { return share * b + rest * b / P; };
+  const int64_t start = block_start(c), end = block_start(c + 1);
+
+  if (warp == 0) {  // the pair that holds unit `start`: the last e with cum[e] H <= start
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const uint32_t below = __ballot_sync(0xFFFFFFFFu, at < hi && plan.cum[at] * H <= start);
+      lo += (31 - __clz(below)) * step;
+      hi = min(hi, lo + step);
+    }
+    if (lane == 0) first_e = lo;
+  }
+  if (tid == 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&k_full[i], 128);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 128);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 2);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+      cut_first[i] = -1;
+    }
+    fence_mbar_init();
+    abort_flag = 0;
+  }
+  if (warp == 12) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  PmWalk w;
+  w.e = first_e;
+  w.left = static_cast<int>(end - start);
+  w.load(a, plan);
+  {
+    const int64_t in = start - plan.cum[w.e] * H;
+    w.h = static_cast<int>(in / w.tiles);
+    w.tile = static_cast<int>(in - static_cast<int64_t>(w.h) * w.tiles);
+  }
+  w.seg_first = start - w.tile;
+  w.count = min(w.left, w.tiles - w.tile);
+
+  if (warp >= 12) {
+    // ------------------------------------------------------------ products
+    regs_dec<64>();
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t kQk = idesc_f16(128, 128, false), kPv = idesc_f16(128, D, true);
+      uint32_t it = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      bool ok = true;
+      const auto qk = [&](int i, int s) {
+        const uint32_t qa = smem_u32(q_s) + i * kOperand, ka = smem_u32(k_s) + s * kOperand;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
+          mma_f16_ss(tmem + i * 128, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off), kQk, k > 0);
+        }
+        mma_commit(&s_full[i]);
+        mbar_arrive(&s_full[i]);  // passes on what this thread saw of the unpacking warps' scales
+      };
+      for (; w.left > 0 && ok; w.next(a, plan)) {
+        const int tiles = w.rows(group) > 128 ? 2 : 1;
+        ok = ok && mbar_wait(&k_full[it & 1], it >> 1 & 1, &abort_flag);
+        tc_fence_after();
+        for (int i = 0; i < tiles && ok; ++i) {
+          ok = mbar_wait(&q_full[i], q_phase[i], &abort_flag);
+          q_phase[i] ^= 1;
+          tc_fence_after();
+          qk(i, it & 1);
+        }
+        mma_commit(&k_empty[it & 1]);
+        for (int j = 0; j < w.count && ok; ++j, ++it) {
+          const int s = it & 1;
+          const bool more = j + 1 < w.count;
+          for (int i = 0; i < tiles && ok; ++i) {
+            ok = mbar_wait(&p_full[i], p_phase[i], &abort_flag);
+            p_phase[i] ^= 1;
+            if (i == 0) ok = ok && mbar_wait(&v_full[s], it >> 1 & 1, &abort_flag);
+            if (i == 0 && more) ok = ok && mbar_wait(&k_full[s ^ 1], (it + 1) >> 1 & 1, &abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t va = smem_u32(v_s) + s * kOperand;
+#pragma unroll
+            for (int k = 0; k < kPmTile / 16; ++k)
+              mma_f16_ts(tmem + 256 + i * D, tmem + i * 128 + k * 8, sw128_mnmajor_desc(va + k * 2048, D > 64 ? kPanel : 16), kPv,
+                         j > 0 || k > 0);
+            if (more) qk(i, s ^ 1);
+            else mma_commit(&o_full[i]);
+          }
+          mma_commit(&v_empty[s]);
+          if (more) mma_commit(&k_empty[s ^ 1]);
+        }
+      }
+      if (!ok) {  // let the products in flight end before tensor memory goes
+        mma_commit(&o_full[0]);
+        mbar_wait_drain(&o_full[0], 0, 1ll << 24);
+        __nanosleep(100000);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ unpacking: thread = token of the tile
+    regs_dec<96>();
+    const int tk = tid - 256;
+    const float scale2 = a.scale * 1.4426950408889634f;
+    const int page_log2 = a.cache.page_log2;
+    const int64_t to_value = static_cast<int64_t>(H) << page_log2;
+    constexpr int kVec = D / 32;  // 16-byte loads of a row's codes
+    PmWalk n = w;  // one unit ahead of w
+    int left = w.left;
+    uint4 kr[kVec], vr[kVec];
+    uint32_t km, vm;
+    int64_t row;   // of the token whose codes are loaded next, or -1
+    bool page_ok;  // false: the table names a page that does not exist
+    const auto look_up = [&] {
+      const int64_t token = static_cast<int64_t>(n.tile) * kPmTile + tk;
+      row = -1;
+      page_ok = true;
+      if (token < n.kv) {
+        const int id = a.table[static_cast<int64_t>(n.b) * a.table_stride + (token >> page_log2)];
+        page_ok = id >= 0 && id < a.cache.pages;
+        if (page_ok)
+          row = ((static_cast<int64_t>(id) * 2 * H + n.h) << page_log2) + (token & ((1 << page_log2) - 1));
+        else
+          record_status(kStatusBounds);
+      }
+    };
+    const auto load = [&](int64_t r, uint4 (&codes)[kVec], uint32_t &meta) {
+      meta = 0;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) codes[i] = make_uint4(0, 0, 0, 0);
+      if (r >= 0) {
+        meta = a.cache.meta[r];
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.cache.codes + r * (D / 2));
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) codes[i] = src[i];
+      }
+    };
+    const auto store = [&](uint8_t *to, const uint4 (&codes)[kVec], uint32_t meta) {
+      const uint32_t z = meta >> 16 & 15u;
+      const uint32_t zlo = 0xE400E400u | z * 0x00010001u, zhi = 0xD400D400u | z * 0x00100010u;
+      uint8_t *line = to + tk * 128;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const uint32_t words[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int chunk = 4 * i + j;
+          *reinterpret_cast<uint4 *>(line + (chunk >> 3) * kPanel + (((chunk & 7) ^ (tk & 7)) << 4)) =
+              unpack_codes(words[j], zlo, zhi);
+        }
+      }
+      fence_proxy_async_smem();
+    };
+    look_up();
+    load(row, kr, km);
+    load(row < 0 ? row : row + to_value, vr, vm);
+    bool ok_now = page_ok;
+    for (uint32_t it = 0; left > 0; --left, ++it) {
+      const int s = it & 1;
+      const uint32_t phase = it >> 1 & 1;
+      // the next unit
+      if (left > 1) {
+        if (++n.tile == n.tiles) {
+          n.tile = 0;
+          if (++n.h == H) {
+            n.h = 0;
+            ++n.e;
+            n.load(a, plan);
+          }
+        }
+        look_up();
+      }
+      const bool next_ok = page_ok;
+      if (!mbar_wait(&k_empty[s], phase ^ 1, &abort_flag)) break;
+      const int at = it & (kPmScaleRing - 1);
+      {
+        const float2 ks = __half22float2(*reinterpret_cast<const __half2 *>(&km));
+        const float2 vs = __half22float2(*reinterpret_cast<const __half2 *>(&vm));
+        k_scale[at * kPmTile + tk] = ks.x * scale2;
+        v_scale[at * kPmTile + tk] = vs.x;
+        float top = vs.x;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, ok_now);
+        if (lane == 0) {
+          v_top[at][warp - 8] = top;
+          seen[at][warp - 8] = bits;
+        }
+      }
+      store(k_s + s * kOperand, kr, km);
+      mbar_arrive(&k_full[s]);
+      if (left > 1) load(row, kr, km);
+      if (!mbar_wait(&v_empty[s], phase ^ 1, &abort_flag)) break;
+      store(v_s + s * kOperand, vr, vm);
+      mbar_arrive(&v_full[s]);
+      if (left > 1) load(row < 0 ? row : row + to_value, vr, vm);
+      ok_now = next_ok;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax: thread = row of a tile
+    regs_inc<176>();
+    const int i = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * D;
+    uint32_t it = 0, s_phase = 0, o_phase = 0;
+    bool ok = true;
+    for (; w.left > 0 && ok; it += w.count, w.next(a, plan)) {
+      const int rows = w.rows(group);
+      if (i * 128 >= rows) continue;
+      const int row = w.pair * kPmRows + i * 128 + r;
+      const bool valid = i * 128 + r < rows;
+      const int tok = row / group, head = w.h * group + row - tok * group;
+      const int64_t token = static_cast<int64_t>(w.q0) + tok;
+      {
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (valid ? token * a.q_stride + static_cast<int64_t>(head) * D : 0));
+        uint8_t *line = q_s + i * kOperand + r * 128;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (valid) v = src[k];
+          *reinterpret_cast<uint4 *>(line + (k >> 3) * kPanel + (((k & 7) ^ (r & 7)) << 4)) =
+              make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                         __byte_perm(v.y, v.w, 0x7632));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&q_full[i]);
+      }
+      // keys this row sees; rows behind the last one see what the request has
+      const int lim = valid && a.causal ? w.kv - w.n + tok + 1 : w.kv;
+      const int lim_min = __shfl_sync(0xFFFFFFFFu, lim, 0);
+      float m = kKvNoMax, log_s = -24.0f;  // the reference is m + log_s
+      uint64_t sum2 = 0;
+      for (int j = 0; j < w.count; ++j) {
+        const int base = (w.tile + j) * kPmTile, at = (it + j) & (kPmScaleRing - 1);
+        ok = mbar_wait(&s_full[i], s_phase, &abort_flag);
+        s_phase ^= 1;
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t x[4][32];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tmem_ld_32x32b_x32(s_at + b * 32, x[b]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) reg_fence(x[b]);
+        const float *ks = k_scale + at * kPmTile, *vs = v_scale + at * kPmTile;
+        uint64_t y[64];
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const ulonglong2 f = lds_2x2f(ks + 4 * k);
+          uint32_t *xk = &x[k >> 3][(k & 7) * 4];
+          y[2 * k] = mul_f2(pack_f2(__uint_as_float(xk[0]), __uint_as_float(xk[1])), f.x);
+          y[2 * k + 1] = mul_f2(pack_f2(__uint_as_float(xk[2]), __uint_as_float(xk[3])), f.y);
+        }
+        const uint4 there = *reinterpret_cast<const uint4 *>(seen[at]);
+        const bool whole = base + kPmTile <= lim_min && (there.x & there.y & there.z & there.w) == 0xFFFFFFFFu;
+        if (!whole) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            const uint32_t word = k < 16 ? there.x : (k < 32 ? there.y : (k < 48 ? there.z : there.w));
+            float2 v = unpack_f2(y[k]);
+            if (base + 2 * k >= lim || !(word >> (2 * k & 31) & 1u)) v.x = -INFINITY;
+            if (base + 2 * k + 1 >= lim || !(word >> (2 * k + 1 & 31) & 1u)) v.y = -INFINITY;
+            y[k] = pack_f2(v.x, v.y);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          const float2 v = unpack_f2(y[k]);
+          top = fmaxf(top, fmaxf(v.x, v.y));
+        }
+        const float4 st = *reinterpret_cast<const float4 *>(v_top[at]);
+        const float log_top = __log2f(fmaxf(fmaxf(st.x, st.y), fmaxf(fmaxf(st.z, st.w), 0x1p-24f)));
+        // ---- the reference
+        const bool move = top > m + 8.0f || log_top > log_s + 2.0f;
+        if (__any_sync(0xFFFFFFFFu, move)) {
+          const float m_new = fmaxf(m, top), ls_new = fmaxf(log_s, log_top);
+          const float keep = ex2((m - m_new) + (log_s - ls_new));
+          m = m_new, log_s = ls_new;
+          const uint64_t keep2 = pack_f2(keep, keep);
+          sum2 = mul_f2(sum2, keep2);
+          if (j > 0) {  // the products into O are done: s_full followed them
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(o_at + b * 32, o);
+              tmem_ld_wait();
+              reg_fence(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+              tmem_st_32x32b_x32(o_at + b * 32, o);
+            }
+          }
+        }
+        const float ref = -(m + log_s);
+        const uint64_t ref2 = pack_f2(ref, ref);
+        // ---- probabilities, times the values' scales
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[32];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const ulonglong2 f = lds_2x2f(vs + 64 * half + 4 * k);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float2 v = unpack_f2(add_f2(y[32 * half + 2 * k + q], ref2));
+              const uint64_t e = pack_f2(ex2(v.x), ex2(v.y));
+              sum2 = add_f2(sum2, e);
+              const float2 pv = unpack_f2(mul_f2(e, q ? f.y : f.x));
+              p[2 * k + q] = half2_bits(pv.x, pv.y);
+            }
+          }
+          if (!whole) {  // a scale may be NaN: no product with the zero of a key that is not seen
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float2 v = unpack_f2(y[32 * half + k]);
+              if (v.x == -INFINITY) p[k] &= 0xFFFF0000u;
+              if (v.y == -INFINITY) p[k] &= 0x0000FFFFu;
+            }
+          }
+          tmem_st_32x32b_x32(s_at + 32 * half, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[i]);
+      }
+      if (!ok) break;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[i], o_phase, &abort_flag));
+      o_phase ^= 1;
+      if (!ok) break;
+      tc_fence_after();
+      const float2 both = unpack_f2(sum2);
+      const float sum = both.x + both.y, ref = m + log_s;
+      const bool cut = w.count < w.tiles;
+      const int side = start <= w.seg_first ? 1 : 0;  // the block's end cuts it, or its beginning
+      float *part = parts + (static_cast<int64_t>(c) * 2 + side) * C::kPart;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row that saw no key is zero
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(o_at + b * 32, o);
+        tmem_ld_wait();
+        reg_fence(o);
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {  // columns 0 4 1 5 2 6 3 7 back in order
+          float v[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(o[k + (x < 4 ? 2 * x : 2 * x - 7)]);
+          if (cut) {
+            float4 *dst = reinterpret_cast<float4 *>(part + static_cast<int64_t>(i * 128 + r) * D + b * 32 + k);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          } else if (valid) {
+            *reinterpret_cast<uint4 *>(a.out + token * a.out_stride + static_cast<int64_t>(head) * D + b * 32 + k) =
+                make_uint4(half2_bits(v[0] * inv, v[1] * inv), half2_bits(v[2] * inv, v[3] * inv),
+                           half2_bits(v[4] * inv, v[5] * inv), half2_bits(v[6] * inv, v[7] * inv));
+          }
+        }
+      }
+      tc_fence_before();
+      if (cut) {
+        *reinterpret_cast<float2 *>(part + static_cast<int64_t>(kPmRows) * D + 2 * (i * 128 + r)) = make_float2(ref, sum);
+        if (tid == 0) {
+          cut_first[side] = w.seg_first;
+          cut_seg[side][0] = w.pair, cut_seg[side][1] = w.h, cut_seg[side][2] = w.q0, cut_seg[side][3] = w.n;
+          cut_seg[side][4] = w.tiles;
+        }
+      } else if (valid && a.lse) {
+        a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp >= 8) return;
+
+  // ---- segments cut between blocks: the last block to get here joins the parts
+  if (tid < 2) {
+    join_blocks[tid][1] = -1;
+    if (cut_first[tid] >= 0) {
+      const int c0 = static_cast<int>(((cut_first[tid] + 1) * P - 1) / U);
+      const int c1 = static_cast<int>(((cut_first[tid] + cut_seg[tid][4]) * P - 1) / U);
+      __threadfence();
+      const uint32_t before = atom_add_acq_rel_gpu_u32(counters + c0, 1u);
+      if (before == static_cast<uint32_t>(c1 - c0)) {
+        counters[c0] = 0;
+        join_blocks[tid][0] = c0;
+        join_blocks[tid][1] = c1;
+      }
+    }
+  }
+  named_bar_sync(1, 256);
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const int c0 = join_blocks[side][0], c1 = join_blocks[side][1];
+    if (c1 < 0) continue;
+    __threadfence();
+    const int pair = cut_seg[side][0], h = cut_seg[side][1], q0 = cut_seg[side][2], n = cut_seg[side][3];
+    const int rows = min(kPmRows, n * group - pair * kPmRows);
+    // the segment is the first block's last one and every other's first one
+    const auto part_of = [&](int b) { return parts + (static_cast<int64_t>(b) * 2 + (b == c0 ? 1 : 0)) * C::kPart; };
+    constexpr int kPer = D / 8;  // threads of a row, eight channels each
+    for (int x = tid; x < rows * kPer; x += 256) {
+      const int r = x / kPer, d0 = x % kPer * 8;
+      float top = -INFINITY;
+      for (int b = c0; b <= c1; ++b) top = fmaxf(top, __ldcg(part_of(b) + static_cast<int64_t>(kPmRows) * D + 2 * r));
+      float sum = 0.0f, acc[8] = {};
+#pragma unroll 2
+      for (int b = c0; b <= c1; ++b) {
+        const float *p = part_of(b);
+        const float2 rl = __ldcg(reinterpret_cast<const float2 *>(p + static_cast<int64_t>(kPmRows) * D + 2 * r));
+        const float f = ex2(rl.x - top);
+        sum = fmaf(rl.y, f, sum);
+        const float4 *src = reinterpret_cast<const float4 *>(p + static_cast<int64_t>(r) * D + d0);
+        const float4 u = __ldcg(src), v = __ldcg(src + 1);
+        acc[0] = fmaf(u.x, f, acc[0]), acc[1] = fmaf(u.y, f, acc[1]), acc[2] = fmaf(u.z, f, acc[2]);
+        acc[3] = fmaf(u.w, f, acc[3]), acc[4] = fmaf(v.x, f, acc[4]), acc[5] = fmaf(v.y, f, acc[5]);
+        acc[6] = fmaf(v.z, f, acc[6]), acc[7] = fmaf(v.w, f, acc[7]);
+      }
+      const int row = pair * kPmRows + r, tok = row / group, head = h * group + row - tok * group;
+      const int64_t token = static_cast<int64_t>(q0) + tok;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      *reinterpret_cast<uint4 *>(a.out + token * a.out_stride + static_cast<int64_t>(head) * D + d0) =
+          make_uint4(half2_bits(acc[0] * inv, acc[1] * inv), half2_bits(acc[2] * inv, acc[3] * inv),
+                     half2_bits(acc[4] * inv, acc[5] * inv), half2_bits(acc[6] * inv, acc[7] * inv));
+      if (a.lse && d0 == 0)
+        a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// Most tile pairs a call can have.
+static int64_t pm_max_entries(int B, int max_q, int group) {
+  return static_cast<int64_t>(B) * ((static_cast<int64_t>(max_q) * group + kPmRows - 1) / kPmRows);
+}
+static size_t pm_plan_bytes(int64_t entries) { return (256 + (entries + 1) * 8 + entries * 8 + 255) / 256 * 256; }
+
+static size_t kv4_prompt_workspace_bytes(int B, int max_q, int group, int D) {
+  return kKvCounterBytes + pm_plan_bytes(pm_max_entries(B, max_q, group)) +
+         static_cast<size_t>(kPmMaxGrid) * 2 * kPmRows * (D + 2) * sizeof(float);
+}
+
+template <int D>
+static cudaError_t launch_kv4_prompt(const AttendArgs &a, void *ws, cudaStream_t stream, const char **msg) {
+  using C = PmCfg<D>;
+  auto kern = kv4_prompt_kernel<D>;
+  static std::atomic<unsigned long long> configured{0};  // one bit per device ordinal
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !(configured.load() & (1ull << dev))) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kv4_prompt_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kKv4MaxRequests * static_cast<int>(sizeof(int)));
+    if (e != cudaSuccess) {
+      *msg = "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed";
+      return e;
+    }
+    if (dev < 64) configured.fetch_or(1ull << dev);
+  }
+  const int group = a.Hq / a.cache.H;
+  const int64_t entries = pm_max_entries(a.B, a.max_q, group);
+  uint8_t *at = static_cast<uint8_t *>(ws) + kKvCounterBytes;
+  PmPlan plan;
+  plan.entries = reinterpret_cast<int *>(at);
+  plan.cum = reinterpret_cast<int64_t *>(at + 256);
+  plan.ent = reinterpret_cast<int2 *>(at + 256 + (entries + 1) * 8);
+  float *parts = reinterpret_cast<float *>(at + pm_plan_bytes(entries));
+  kv4_prompt_plan_kernel<<<1, kPmPlanThreads, a.B * sizeof(int), stream>>>(a, plan);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    const int64_t tiles = ((static_cast<int64_t>(a.W) << a.cache.page_log2) + kPmTile - 1) / kPmTile;
+    const int64_t units = entries * a.cache.H * (tiles > 0 ? tiles : 1);
+    int64_t grid = device_sm_count();
+    if (grid > kPmMaxGrid) grid = kPmMaxGrid;
+    if (grid > units) grid = units;
+    kern<<<static_cast<unsigned>(grid), kPmThreads, C::kSmem, stream>>>(a, plan, static_cast<uint32_t *>(ws), parts);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) *msg = "launch of the prompt attention failed";
+  return e;
+}
+
+// ---------------------------------------------------------------------------
+// Which kernel: the decode kernel takes requests of up to 16 rows per key head
+// (its second 8-row tile costs a quarter more than one), above that the tensor
+// core's 128-row tiles.
+// ---------------------------------------------------------------------------
+static bool kv4_is_decode(int max_q, int group) { return static_cast<int64_t>(max_q) * group <= 16; }
+
+size_t kv4_attention_workspace_bytes(int B, int max_q, int Hq, int H, int D, int, int) {
+  return kv4_is_decode(max_q, Hq / H) ? kv4_decode_workspace_bytes(max_q, Hq / H, D)
+                                      : kv4_prompt_workspace_bytes(B, max_q, Hq / H, D);
+}
+
+cudaError_t launch_kv4_attention(const AttendArgs &a, void *ws, cudaStream_t stream, const char **msg) {
+  if (kv4_is_decode(a.max_q, a.Hq / a.cache.H)) return launch_kv4_decode(a, ws, stream, msg);
+  return a.cache.D == 128 ? launch_kv4_prompt<128>(a, ws, stream, msg) : launch_kv4_prompt<64>(a, ws, stream, msg);
+}
+
+}  // namespace mixllm

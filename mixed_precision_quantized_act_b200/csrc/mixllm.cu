@@ -16,6 +16,7 @@
 #include "search.cuh"
 #include "kv4_attention.cuh"
 #include "kv4_cache.cuh"
+#include "kv4_prompt.cuh"
 #include "launch.h"
 #include "norm.cuh"
 #include "pack_host.cuh"
