@@ -20,9 +20,11 @@ namespace mixllm {
 //   S = Q K^T      two 128 x 128 products, fp32 in tensor memory
 //   P = softmax    one thread per row; fp16, over S in tensor memory
 //   O += P V       A from tensor memory, accumulated there in fp32
-// Warps 0-3 and 4-7 are the softmax of either tile, warps 8-11 unpack keys and
-// values, warp 12 issues the products.  The two tiles take turns on the tensor
-// core while the other one's softmax runs.
+// Warp 0 issues the products, warps 4-7 unpack keys and values, warps 8-11 and
+// 12-15 are the softmax of either tile (in this order because the scheduler
+// prefers older warps, and the tensor core waits for warp 0's every
+// instruction).  The two tiles take turns on the tensor core while the other
+// one's softmax runs.
 //
 // Unpacking: one thread per token.  A word's nibbles i and i + 4 become fp16
 // integers 1024 + n (or 1024 + 16 n) by one AND-OR, and code - z by one add (or
@@ -189,6 +191,13 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t p
   return d;
 }
 
+// True on one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint64_t pack_f2(float x, float y) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
@@ -254,7 +263,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
   const auto block_start = [&](int b) { return share * b + rest * b / P; };
   const int64_t start = block_start(c), end = block_start(c + 1);
 
-  if (warp == 0) {  // the pair that holds unit `start`: the last e with cum[e] H <= start
+  if (warp == 15) {  // the pair that holds unit `start`: the last e with cum[e] H <= start
     int lo = 0, hi = E;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, at = lo + lane * step;
@@ -279,7 +288,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
     fence_mbar_init();
     abort_flag = 0;
   }
-  if (warp == 12) {
+  if (warp == 0) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
@@ -299,67 +308,81 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
   w.seg_first = start - w.tile;
   w.count = min(w.left, w.tiles - w.tile);
 
-  if (warp >= 12) {
+  if (warp < 4) {
     // ------------------------------------------------------------ products
     regs_dec<64>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 0) {
+      // The whole warp walks and waits; one elected lane issues.  (With the
+      // walk itself inside a one-lane branch a product cost about 300 clocks to
+      // issue, ten times the tensor core's: its operands were not known to be
+      // uniform.)
       constexpr uint32_t kQk = idesc_f16(128, 128, false), kPv = idesc_f16(128, D, true);
-      uint32_t it = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const uint64_t q_desc = sw128_kmajor_desc(smem_u32(q_s)), k_desc = sw128_kmajor_desc(smem_u32(k_s));
+      const uint64_t v_desc = sw128_mnmajor_desc(smem_u32(v_s), D > 64 ? kPanel : 16);
+      uint32_t it = 0, q_phase = 0, p_phase = 0;  // bit i: tile i
       bool ok = true;
-      const auto qk = [&](int i, int s) {
-        const uint32_t qa = smem_u32(q_s) + i * kOperand, ka = smem_u32(k_s) + s * kOperand;
+      const auto qk = [&](int i, int s) {  // elected lane
+        const uint64_t qa = q_desc + i * (kOperand >> 4), ka = k_desc + s * (kOperand >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
-          mma_f16_ss(tmem + i * 128, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off), kQk, k > 0);
+          const uint32_t off = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
+          mma_f16_ss(tm + i * 128, qa + off, ka + off, kQk, k > 0);
         }
         mma_commit(&s_full[i]);
         mbar_arrive(&s_full[i]);  // passes on what this thread saw of the unpacking warps' scales
       };
       for (; w.left > 0 && ok; w.next(a, plan)) {
         const int tiles = w.rows(group) > 128 ? 2 : 1;
-        ok = ok && mbar_wait(&k_full[it & 1], it >> 1 & 1, &abort_flag);
-        tc_fence_after();
+        ok = warp_wait(&k_full[it & 1], it >> 1 & 1, &abort_flag);
         for (int i = 0; i < tiles && ok; ++i) {
-          ok = mbar_wait(&q_full[i], q_phase[i], &abort_flag);
-          q_phase[i] ^= 1;
+          ok = warp_wait(&q_full[i], q_phase >> i & 1, &abort_flag);
+          if (!ok) break;
+          q_phase ^= 1u << i;
           tc_fence_after();
-          qk(i, it & 1);
+          if (elect_one()) {
+            qk(i, it & 1);
+            if (i + 1 == tiles) mma_commit(&k_empty[it & 1]);
+          }
+          __syncwarp();
         }
-        mma_commit(&k_empty[it & 1]);
         for (int j = 0; j < w.count && ok; ++j, ++it) {
           const int s = it & 1;
           const bool more = j + 1 < w.count;
-          for (int i = 0; i < tiles && ok; ++i) {
-            ok = mbar_wait(&p_full[i], p_phase[i], &abort_flag);
-            p_phase[i] ^= 1;
-            if (i == 0) ok = ok && mbar_wait(&v_full[s], it >> 1 & 1, &abort_flag);
-            if (i == 0 && more) ok = ok && mbar_wait(&k_full[s ^ 1], (it + 1) >> 1 & 1, &abort_flag);
+          for (int i = 0; i < tiles; ++i) {
+            ok = warp_wait(&p_full[i], p_phase >> i & 1, &abort_flag);
+            if (i == 0) ok = ok && warp_wait(&v_full[s], it >> 1 & 1, &abort_flag);
+            if (i == 0 && more) ok = ok && warp_wait(&k_full[s ^ 1], (it + 1) >> 1 & 1, &abort_flag);
             if (!ok) break;
+            p_phase ^= 1u << i;
             tc_fence_after();
-            const uint32_t va = smem_u32(v_s) + s * kOperand;
+            if (elect_one()) {
+              const uint64_t va = v_desc + s * (kOperand >> 4);
 #pragma unroll
-            for (int k = 0; k < kPmTile / 16; ++k)
-              mma_f16_ts(tmem + 256 + i * D, tmem + i * 128 + k * 8, sw128_mnmajor_desc(va + k * 2048, D > 64 ? kPanel : 16), kPv,
-                         j > 0 || k > 0);
-            if (more) qk(i, s ^ 1);
-            else mma_commit(&o_full[i]);
+              for (int k = 0; k < kPmTile / 16; ++k)
+                mma_f16_ts(tm + 256 + i * D, tm + i * 128 + k * 8, va + k * (2048 >> 4), kPv, j > 0 || k > 0);
+              if (more) qk(i, s ^ 1);
+              else mma_commit(&o_full[i]);
+              if (i + 1 == tiles) {
+                mma_commit(&v_empty[s]);
+                if (more) mma_commit(&k_empty[s ^ 1]);
+              }
+            }
+            __syncwarp();
           }
-          mma_commit(&v_empty[s]);
-          if (more) mma_commit(&k_empty[s ^ 1]);
         }
       }
-      if (!ok) {  // let the products in flight end before tensor memory goes
+      if (!ok && elect_one()) {  // let the products in flight end before tensor memory goes
         mma_commit(&o_full[0]);
         mbar_wait_drain(&o_full[0], 0, 1ll << 24);
         __nanosleep(100000);
       }
     }
     __syncwarp();
-  } else if (warp >= 8) {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ unpacking: thread = token of the tile
     regs_dec<96>();
-    const int tk = tid - 256;
+    const int tk = tid - 128;
     const float scale2 = a.scale * 1.4426950408889634f;
     const int page_log2 = a.cache.page_log2;
     const int64_t to_value = static_cast<int64_t>(H) << page_log2;
@@ -442,8 +465,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
         for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
         const uint32_t bits = __ballot_sync(0xFFFFFFFFu, ok_now);
         if (lane == 0) {
-          v_top[at][warp - 8] = top;
-          seen[at][warp - 8] = bits;
+          v_top[at][warp - 4] = top;
+          seen[at][warp - 4] = bits;
         }
       }
       store(k_s + s * kOperand, kr, km);
@@ -458,7 +481,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
   } else {
     // ------------------------------------------------------------ softmax: thread = row of a tile
     regs_inc<176>();
-    const int i = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int i = (warp >> 2) - 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * D;
     uint32_t it = 0, s_phase = 0, o_phase = 0;
@@ -622,7 +645,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       tc_fence_before();
       if (cut) {
         *reinterpret_cast<float2 *>(part + static_cast<int64_t>(kPmRows) * D + 2 * (i * 128 + r)) = make_float2(ref, sum);
-        if (tid == 0) {
+        if (tid == 256) {
           cut_first[side] = w.seg_first;
           cut_seg[side][0] = w.pair, cut_seg[side][1] = w.h, cut_seg[side][2] = w.q0, cut_seg[side][3] = w.n;
           cut_seg[side][4] = w.tiles;
@@ -633,21 +656,22 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
     }
   }
   __syncthreads();
-  if (warp == 12) tmem_dealloc(tmem, 512);
-  if (warp >= 8) return;
+  if (warp == 0) tmem_dealloc(tmem, 512);
+  if (warp < 8) return;
+  const int me = tid - 256;
 
   // ---- segments cut between blocks: the last block to get here joins the parts
-  if (tid < 2) {
-    join_blocks[tid][1] = -1;
-    if (cut_first[tid] >= 0) {
-      const int c0 = static_cast<int>(((cut_first[tid] + 1) * P - 1) / U);
-      const int c1 = static_cast<int>(((cut_first[tid] + cut_seg[tid][4]) * P - 1) / U);
+  if (me < 2) {
+    join_blocks[me][1] = -1;
+    if (cut_first[me] >= 0) {
+      const int c0 = static_cast<int>(((cut_first[me] + 1) * P - 1) / U);
+      const int c1 = static_cast<int>(((cut_first[me] + cut_seg[me][4]) * P - 1) / U);
       __threadfence();
       const uint32_t before = atom_add_acq_rel_gpu_u32(counters + c0, 1u);
       if (before == static_cast<uint32_t>(c1 - c0)) {
         counters[c0] = 0;
-        join_blocks[tid][0] = c0;
-        join_blocks[tid][1] = c1;
+        join_blocks[me][0] = c0;
+        join_blocks[me][1] = c1;
       }
     }
   }
@@ -662,7 +686,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
     // the segment is the first block's last one and every other's first one
     const auto part_of = [&](int b) { return parts + (static_cast<int64_t>(b) * 2 + (b == c0 ? 1 : 0)) * C::kPart; };
     constexpr int kPer = D / 8;  // threads of a row, eight channels each
-    for (int x = tid; x < rows * kPer; x += 256) {
+    for (int x = me; x < rows * kPer; x += 256) {
       const int r = x / kPer, d0 = x % kPer * 8;
       float top = -INFINITY;
       for (int b = c0; b <= c1; ++b) top = fmaxf(top, __ldcg(part_of(b) + static_cast<int64_t>(kPmRows) * D + 2 * r));
