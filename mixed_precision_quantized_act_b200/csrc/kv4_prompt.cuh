@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "gemm_w4w8a8.cuh"  // device_sm_count
 #include "kv4_attention.cuh"
@@ -216,6 +217,11 @@ __device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 __device__ __forceinline__ ulonglong2 lds_2x2f(const float *p) { return *reinterpret_cast<const ulonglong2 *>(p); }
@@ -521,39 +527,47 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           break;
         }
         tc_fence_after();
-        uint32_t x[4][32];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) tmem_ld_32x32b_x32(s_at + b * 32, x[b]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int b = 0; b < 4; ++b) reg_fence(x[b]);
+        // S is read twice, for the maximum and for the exponentials, 32 columns at a time with the next
+        // 32 on their way: held in registers throughout, a row of 128 spilled
         const float *ks = k_scale + at * kPmTile, *vs = v_scale + at * kPmTile;
-        uint64_t y[64];
-        float top = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const ulonglong2 f = lds_2x2f(ks + 4 * k);
-          uint32_t *xk = &x[k >> 3][(k & 7) * 4];
-          y[2 * k] = mul_f2(pack_f2(__uint_as_float(xk[0]), __uint_as_float(xk[1])), f.x);
-          y[2 * k + 1] = mul_f2(pack_f2(__uint_as_float(xk[2]), __uint_as_float(xk[3])), f.y);
-        }
         const uint4 there = *reinterpret_cast<const uint4 *>(seen[at]);
         const bool whole = base + kPmTile <= lim_min && (there.x & there.y & there.z & there.w) == 0xFFFFFFFFu;
-        if (!whole) {
+        // bit k: column 32 b + k is seen by this row
+        const auto visible = [&](int b) {
+          const int n = lim - base - 32 * b;
+          return (b == 0 ? there.x : b == 1 ? there.y : b == 2 ? there.z : there.w) &
+                 (n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u));
+        };
+        uint32_t x[2][32];
+        float top = -INFINITY;
+        tmem_ld_32x32b_x32(s_at, x[0]);
+        const auto maximum = [&](auto all) {
+          constexpr bool kAll = decltype(all)::value;  // every column is seen by every row of the warp
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            const uint32_t word = k < 16 ? there.x : (k < 32 ? there.y : (k < 48 ? there.z : there.w));
-            float2 v = unpack_f2(y[k]);
-            if (base + 2 * k >= lim || !(word >> (2 * k & 31) & 1u)) v.x = -INFINITY;
-            if (base + 2 * k + 1 >= lim || !(word >> (2 * k + 1 & 31) & 1u)) v.y = -INFINITY;
-            y[k] = pack_f2(v.x, v.y);
+          for (int b = 0; b < 4; ++b) {
+            uint32_t(&c)[32] = x[b & 1];
+            tmem_ld_wait();
+            reg_fence(c);
+            if (b < 3) tmem_ld_32x32b_x32(s_at + 32 * (b + 1), x[(b + 1) & 1]);
+            float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const uint32_t see = kAll ? 0xFFFFFFFFu : visible(b);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const ulonglong2 f = lds_2x2f(ks + 32 * b + 4 * k);
+              float2 u = unpack_f2(mul_f2(pack_f2(__uint_as_float(c[4 * k]), __uint_as_float(c[4 * k + 1])), f.x));
+              float2 v = unpack_f2(mul_f2(pack_f2(__uint_as_float(c[4 * k + 2]), __uint_as_float(c[4 * k + 3])), f.y));
+              if constexpr (!kAll) {
+                u.x = see >> (4 * k) & 1u ? u.x : -INFINITY, u.y = see >> (4 * k + 1) & 1u ? u.y : -INFINITY;
+                v.x = see >> (4 * k + 2) & 1u ? v.x : -INFINITY, v.y = see >> (4 * k + 3) & 1u ? v.y : -INFINITY;
+              }
+              hi[k & 3] = fmaxf(fmaxf(fmaxf(hi[k & 3], u.x), u.y), fmaxf(v.x, v.y));
+            }
+            top = fmaxf(top, fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])));
           }
-        }
-#pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          const float2 v = unpack_f2(y[k]);
-          top = fmaxf(top, fmaxf(v.x, v.y));
-        }
+        };
+        if (whole) maximum(std::true_type{});
+        else maximum(std::false_type{});
+        tmem_ld_32x32b_x32(s_at, x[0]);  // for the second pass
         const float4 st = *reinterpret_cast<const float4 *>(v_top[at]);
         const float log_top = __log2f(fmaxf(fmaxf(st.x, st.y), fmaxf(fmaxf(st.z, st.w), 0x1p-24f)));
         // ---- the reference
@@ -580,31 +594,40 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
         const float ref = -(m + log_s);
         const uint64_t ref2 = pack_f2(ref, ref);
         // ---- probabilities, times the values' scales
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        const auto weights = [&](auto all) {
+          constexpr bool kAll = decltype(all)::value;
           uint32_t p[32];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const ulonglong2 f = lds_2x2f(vs + 64 * half + 4 * k);
+          for (int b = 0; b < 4; ++b) {
+            uint32_t(&c)[32] = x[b & 1];
+            tmem_ld_wait();
+            reg_fence(c);
+            if (b < 3) tmem_ld_32x32b_x32(s_at + 32 * (b + 1), x[(b + 1) & 1]);
+            const uint32_t see = kAll ? 0xFFFFFFFFu : visible(b);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float2 v = unpack_f2(add_f2(y[32 * half + 2 * k + q], ref2));
-              const uint64_t e = pack_f2(ex2(v.x), ex2(v.y));
-              sum2 = add_f2(sum2, e);
-              const float2 pv = unpack_f2(mul_f2(e, q ? f.y : f.x));
-              p[2 * k + q] = half2_bits(pv.x, pv.y);
-            }
-          }
-          if (!whole) {  // a scale may be NaN: no product with the zero of a key that is not seen
+            for (int k = 0; k < 8; ++k) {
+              const ulonglong2 f = lds_2x2f(ks + 32 * b + 4 * k), g = lds_2x2f(vs + 32 * b + 4 * k);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float2 v = unpack_f2(y[32 * half + k]);
-              if (v.x == -INFINITY) p[k] &= 0xFFFF0000u;
-              if (v.y == -INFINITY) p[k] &= 0x0000FFFFu;
+              for (int q = 0; q < 2; ++q) {
+                const int at2 = 4 * k + 2 * q;
+                const float2 v = unpack_f2(
+                    fma_f2(pack_f2(__uint_as_float(c[at2]), __uint_as_float(c[at2 + 1])), q ? f.y : f.x, ref2));
+                float2 e = make_float2(ex2(v.x), ex2(v.y));
+                if constexpr (!kAll) e.x = see >> at2 & 1u ? e.x : 0.0f, e.y = see >> (at2 + 1) & 1u ? e.y : 0.0f;
+                const uint64_t e2 = pack_f2(e.x, e.y);
+                sum2 = add_f2(sum2, e2);
+                float2 pv = unpack_f2(mul_f2(e2, q ? g.y : g.x));
+                // a value's scale may be NaN: select, not multiply
+                if constexpr (!kAll) pv.x = see >> at2 & 1u ? pv.x : 0.0f, pv.y = see >> (at2 + 1) & 1u ? pv.y : 0.0f;
+                p[16 * (b & 1) + 2 * k + q] = half2_bits(pv.x, pv.y);
+              }
             }
+            // over columns of S that this pass has read
+            if (b & 1) tmem_st_32x32b_x32(s_at + 16 * (b - 1), p);
           }
-          tmem_st_32x32b_x32(s_at + 32 * half, p);
-        }
+        };
+        if (whole) weights(std::true_type{});
+        else weights(std::false_type{});
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_full[i]);
