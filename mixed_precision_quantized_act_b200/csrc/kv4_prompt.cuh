@@ -499,20 +499,29 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       const bool valid = i * 128 + r < rows;
       const int tok = row / group, head = w.h * group + row - tok * group;
       const int64_t token = static_cast<int64_t>(w.q0) + tok;
-      {
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (valid ? token * a.q_stride + static_cast<int64_t>(head) * D : 0));
-        uint8_t *line = q_s + i * kOperand + r * 128;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (valid) v = src[k];
-          *reinterpret_cast<uint4 *>(line + (k >> 3) * kPanel + (((k & 7) ^ (r & 7)) << 4)) =
-              make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                         __byte_perm(v.y, v.w, 0x7632));
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&q_full[i]);
+      // Q: D / 8 lanes copy a row of the warp's 32, channels in the unpacked codes' order
+      uint8_t *tile_s = q_s + i * kOperand;
+      constexpr int kChunks = D / 8, kTogether = 32 / kChunks;
+      const int chunk = lane % kChunks, first_rr = (warp & 3) * 32 + lane / kChunks;
+      const int first_tok = (w.pair * kPmRows + i * 128 + first_rr) / group;
+      const int first_head = w.pair * kPmRows + i * 128 + first_rr - first_tok * group;
+      int tok2 = first_tok, head2 = first_head;  // of the row that this lane copies next
+      const auto next_row = [&] {
+        for (head2 += kTogether; head2 >= group; head2 -= group) ++tok2;
+      };
+#pragma unroll 8
+      for (int k = 0; k < 32 / kTogether; ++k, next_row()) {
+        const int rr = first_rr + k * kTogether;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i * 128 + rr < rows)
+          v = *reinterpret_cast<const uint4 *>(a.q + (static_cast<int64_t>(w.q0) + tok2) * a.q_stride +
+                                               static_cast<int64_t>(w.h * group + head2) * D + chunk * 8);
+        *reinterpret_cast<uint4 *>(tile_s + rr * 128 + (chunk >> 3) * kPanel + (((chunk & 7) ^ (rr & 7)) << 4)) =
+            make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                       __byte_perm(v.y, v.w, 0x7632));
       }
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full[i]);
       // keys this row sees; rows behind the last one see what the request has
       const int lim = valid && a.causal ? w.kv - w.n + tok + 1 : w.kv;
       const int lim_min = __shfl_sync(0xFFFFFFFFu, lim, 0);
@@ -527,8 +536,6 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           break;
         }
         tc_fence_after();
-        // S is read twice, for the maximum and for the exponentials, 32 columns at a time with the next
-        // 32 on their way: held in registers throughout, a row of 128 spilled
         const float *ks = k_scale + at * kPmTile, *vs = v_scale + at * kPmTile;
         const uint4 there = *reinterpret_cast<const uint4 *>(seen[at]);
         const bool whole = base + kPmTile <= lim_min && (there.x & there.y & there.z & there.w) == 0xFFFFFFFFu;
@@ -538,65 +545,35 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           return (b == 0 ? there.x : b == 1 ? there.y : b == 2 ? there.z : there.w) &
                  (n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u));
         };
-        uint32_t x[2][32];
-        float top = -INFINITY;
-        tmem_ld_32x32b_x32(s_at, x[0]);
+        // the row's largest score
         const auto maximum = [&](auto all) {
           constexpr bool kAll = decltype(all)::value;  // every column is seen by every row of the warp
+          float top = -INFINITY;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            uint32_t(&c)[32] = x[b & 1];
+            uint32_t c[32];
+            tmem_ld_32x32b_x32(s_at + 32 * b, c);
             tmem_ld_wait();
             reg_fence(c);
-            if (b < 3) tmem_ld_32x32b_x32(s_at + 32 * (b + 1), x[(b + 1) & 1]);
-            float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             const uint32_t see = kAll ? 0xFFFFFFFFu : visible(b);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const ulonglong2 f = lds_2x2f(ks + 32 * b + 4 * k);
-              float2 u = unpack_f2(mul_f2(pack_f2(__uint_as_float(c[4 * k]), __uint_as_float(c[4 * k + 1])), f.x));
-              float2 v = unpack_f2(mul_f2(pack_f2(__uint_as_float(c[4 * k + 2]), __uint_as_float(c[4 * k + 3])), f.y));
-              if constexpr (!kAll) {
-                u.x = see >> (4 * k) & 1u ? u.x : -INFINITY, u.y = see >> (4 * k + 1) & 1u ? u.y : -INFINITY;
-                v.x = see >> (4 * k + 2) & 1u ? v.x : -INFINITY, v.y = see >> (4 * k + 3) & 1u ? v.y : -INFINITY;
-              }
-              hi[k & 3] = fmaxf(fmaxf(fmaxf(hi[k & 3], u.x), u.y), fmaxf(v.x, v.y));
+            for (int k = 0; k < 32; ++k) {
+              const float v = __uint_as_float(c[k]) * ks[32 * b + k];
+              top = fmaxf(top, kAll || (see >> k & 1u) ? v : -INFINITY);
             }
-            top = fmaxf(top, fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])));
           }
+          return top;
         };
-        if (whole) maximum(std::true_type{});
-        else maximum(std::false_type{});
-        tmem_ld_32x32b_x32(s_at, x[0]);  // for the second pass
-        const float4 st = *reinterpret_cast<const float4 *>(v_top[at]);
-        const float log_top = __log2f(fmaxf(fmaxf(st.x, st.y), fmaxf(fmaxf(st.z, st.w), 0x1p-24f)));
-        // ---- the reference
-        const bool move = top > m + 8.0f || log_top > log_s + 2.0f;
-        if (__any_sync(0xFFFFFFFFu, move)) {
-          const float m_new = fmaxf(m, top), ls_new = fmaxf(log_s, log_top);
-          const float keep = ex2((m - m_new) + (log_s - ls_new));
-          m = m_new, log_s = ls_new;
-          const uint64_t keep2 = pack_f2(keep, keep);
-          sum2 = mul_f2(sum2, keep2);
-          if (j > 0) {  // the products into O are done: s_full followed them
-#pragma unroll
-            for (int b = 0; b < D / 32; ++b) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(o_at + b * 32, o);
-              tmem_ld_wait();
-              reg_fence(o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-              tmem_st_32x32b_x32(o_at + b * 32, o);
-            }
-          }
-        }
-        const float ref = -(m + log_s);
-        const uint64_t ref2 = pack_f2(ref, ref);
-        // ---- probabilities, times the values' scales
+        // the row's weights p s_v, relative to the reference; adds sum p to sum2 and returns the largest score
+        // above the reference
+        uint32_t p[64];
         const auto weights = [&](auto all) {
           constexpr bool kAll = decltype(all)::value;
-          uint32_t p[32];
+          const float ref = -(m + log_s);
+          const uint64_t ref2 = pack_f2(ref, ref);
+          uint32_t x[2][32];
+          float hi[2] = {-INFINITY, -INFINITY};
+          tmem_ld_32x32b_x32(s_at, x[0]);
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             uint32_t(&c)[32] = x[b & 1];
@@ -610,24 +587,63 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 const int at2 = 4 * k + 2 * q;
-                const float2 v = unpack_f2(
+                float2 v = unpack_f2(
                     fma_f2(pack_f2(__uint_as_float(c[at2]), __uint_as_float(c[at2 + 1])), q ? f.y : f.x, ref2));
-                float2 e = make_float2(ex2(v.x), ex2(v.y));
-                if constexpr (!kAll) e.x = see >> at2 & 1u ? e.x : 0.0f, e.y = see >> (at2 + 1) & 1u ? e.y : 0.0f;
-                const uint64_t e2 = pack_f2(e.x, e.y);
+                if constexpr (!kAll) v.x = see >> at2 & 1u ? v.x : -INFINITY, v.y = see >> (at2 + 1) & 1u ? v.y : -INFINITY;
+                hi[q] = fmaxf(fmaxf(hi[q], v.x), v.y);
+                const uint64_t e2 = pack_f2(ex2(v.x), ex2(v.y));
                 sum2 = add_f2(sum2, e2);
                 float2 pv = unpack_f2(mul_f2(e2, q ? g.y : g.x));
                 // a value's scale may be NaN: select, not multiply
                 if constexpr (!kAll) pv.x = see >> at2 & 1u ? pv.x : 0.0f, pv.y = see >> (at2 + 1) & 1u ? pv.y : 0.0f;
-                p[16 * (b & 1) + 2 * k + q] = half2_bits(pv.x, pv.y);
+                p[16 * b + 2 * k + q] = half2_bits(pv.x, pv.y);
               }
             }
-            // over columns of S that this pass has read
-            if (b & 1) tmem_st_32x32b_x32(s_at + 16 * (b - 1), p);
+          }
+          return fmaxf(hi[0], hi[1]);
+        };
+        // moves the reference to these, and takes the sums along
+        const auto move_to = [&](float m_new, float ls_new) {
+          const float keep = ex2((m - m_new) + (log_s - ls_new));
+          m = m_new, log_s = ls_new;
+          sum2 = mul_f2(sum2, pack_f2(keep, keep));
+          if (j > 0) {  // the products into O are done: s_full followed them
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(o_at + b * 32, o);
+              tmem_ld_wait();
+              reg_fence(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+              tmem_st_32x32b_x32(o_at + b * 32, o);
+            }
           }
         };
-        if (whole) weights(std::true_type{});
-        else weights(std::false_type{});
+        const float4 st = *reinterpret_cast<const float4 *>(v_top[at]);
+        const float log_top = __log2f(fmaxf(fmaxf(st.x, st.y), fmaxf(fmaxf(st.z, st.w), 0x1p-24f)));
+        // A row's first scores set its reference before they are used.  Later ones are used with the reference
+        // that there is, and once more where they pass it by too much, which is rare.
+        const bool first = __any_sync(0xFFFFFFFFu, m == kKvNoMax);
+        float ls_new = log_top > log_s + 2.0f ? log_top : log_s;
+        float m_new = m;
+        if (first) {
+          const float top = whole ? maximum(std::true_type{}) : maximum(std::false_type{});
+          if (top > m + 8.0f) m_new = top;
+        }
+        if (__any_sync(0xFFFFFFFFu, m_new != m || ls_new != log_s)) move_to(m_new, ls_new);
+        const uint64_t sum_before = sum2;
+        for (int again = 0; again < 2; ++again) {
+          const float over = (whole ? weights(std::true_type{}) : weights(std::false_type{})) + log_s;
+          if (first || !__any_sync(0xFFFFFFFFu, over > 8.0f)) break;
+          sum2 = sum_before;
+          move_to(over > 8.0f ? m + over : m, log_s);
+        }
+        {
+          uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(p), (&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(p + 32);
+          tmem_st_32x32b_x32(s_at, lo);  // over the columns of S
+          tmem_st_32x32b_x32(s_at + 32, hi);
+        }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_full[i]);
@@ -654,16 +670,30 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           float v[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(o[k + (x < 4 ? 2 * x : 2 * x - 7)]);
-          if (cut) {
-            float4 *dst = reinterpret_cast<float4 *>(part + static_cast<int64_t>(i * 128 + r) * D + b * 32 + k);
+          const int ch = 4 * b + k / 8;
+          if (cut) {  // four channels of all rows together: neighbouring rows are neighbouring lanes
+            float4 *dst = reinterpret_cast<float4 *>(part) + 2 * ch * kPmRows + i * 128 + r;
             dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-          } else if (valid) {
-            *reinterpret_cast<uint4 *>(a.out + token * a.out_stride + static_cast<int64_t>(head) * D + b * 32 + k) =
+            dst[kPmRows] = make_float4(v[4], v[5], v[6], v[7]);
+          } else {  // by way of Q's place, which no product reads any more
+            *reinterpret_cast<uint4 *>(tile_s + r * 128 + (ch >> 3) * kPanel + (((ch & 7) ^ (r & 7)) << 4)) =
                 make_uint4(half2_bits(v[0] * inv, v[1] * inv), half2_bits(v[2] * inv, v[3] * inv),
                            half2_bits(v[4] * inv, v[5] * inv), half2_bits(v[6] * inv, v[7] * inv));
           }
         }
+      }
+      if (!cut) {
+        __syncwarp();
+        tok2 = first_tok, head2 = first_head;
+#pragma unroll 8
+        for (int k = 0; k < 32 / kTogether; ++k, next_row()) {
+          const int rr = first_rr + k * kTogether;
+          if (i * 128 + rr >= rows) continue;
+          *reinterpret_cast<uint4 *>(a.out + (static_cast<int64_t>(w.q0) + tok2) * a.out_stride +
+                                     static_cast<int64_t>(w.h * group + head2) * D + chunk * 8) =
+              *reinterpret_cast<const uint4 *>(tile_s + rr * 128 + (chunk >> 3) * kPanel + (((chunk & 7) ^ (rr & 7)) << 4));
+        }
+        __syncwarp();
       }
       tc_fence_before();
       if (cut) {
@@ -708,32 +738,45 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
     const int rows = min(kPmRows, n * group - pair * kPmRows);
     // the segment is the first block's last one and every other's first one
     const auto part_of = [&](int b) { return parts + (static_cast<int64_t>(b) * 2 + (b == c0 ? 1 : 0)) * C::kPart; };
-    constexpr int kPer = D / 8;  // threads of a row, eight channels each
-    for (int x = me; x < rows * kPer; x += 256) {
-      const int r = x / kPer, d0 = x % kPer * 8;
-      float top = -INFINITY;
-      for (int b = c0; b <= c1; ++b) top = fmaxf(top, __ldcg(part_of(b) + static_cast<int64_t>(kPmRows) * D + 2 * r));
-      float sum = 0.0f, acc[8] = {};
+    // thread = row: the parts' weights into shared memory (as many as there are blocks fit), then their sums
+    float *weight = reinterpret_cast<float *>(smem) + me;  // [part][row]
+    const int n_parts = c1 - c0 + 1;
+    constexpr int kAtOnce = 6 * kOperand / (kPmRows * 4);
+    const auto ref_of = [&](int b) {
+      return __ldcg(reinterpret_cast<const float2 *>(part_of(b) + static_cast<int64_t>(kPmRows) * D + 2 * me));
+    };
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
+    for (int b = c0; b <= c1; ++b) top = fmaxf(top, ref_of(b).x);
+#pragma unroll 4
+    for (int b = c0; b <= c1; ++b) {
+      const float2 rl = ref_of(b);
+      const float f = ex2(rl.x - top);
+      sum = fmaf(rl.y, f, sum);
+      if (b - c0 < kAtOnce) weight[(b - c0) * kPmRows] = f;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int row = pair * kPmRows + me, tok = row / group, head = h * group + row - tok * group;
+    const int64_t token = static_cast<int64_t>(q0) + tok;
+    if (me < rows) {
+      __half *dst = a.out + token * a.out_stride + static_cast<int64_t>(head) * D;
 #pragma unroll 2
-      for (int b = c0; b <= c1; ++b) {
-        const float *p = part_of(b);
-        const float2 rl = __ldcg(reinterpret_cast<const float2 *>(p + static_cast<int64_t>(kPmRows) * D + 2 * r));
-        const float f = ex2(rl.x - top);
-        sum = fmaf(rl.y, f, sum);
-        const float4 *src = reinterpret_cast<const float4 *>(p + static_cast<int64_t>(r) * D + d0);
-        const float4 u = __ldcg(src), v = __ldcg(src + 1);
-        acc[0] = fmaf(u.x, f, acc[0]), acc[1] = fmaf(u.y, f, acc[1]), acc[2] = fmaf(u.z, f, acc[2]);
-        acc[3] = fmaf(u.w, f, acc[3]), acc[4] = fmaf(v.x, f, acc[4]), acc[5] = fmaf(v.y, f, acc[5]);
-        acc[6] = fmaf(v.z, f, acc[6]), acc[7] = fmaf(v.w, f, acc[7]);
+      for (int chunk = 0; chunk < D / 8; ++chunk) {
+        float acc[8] = {};
+#pragma unroll 4
+        for (int x = 0; x < n_parts; ++x) {
+          const float f = x < kAtOnce ? weight[x * kPmRows] : ex2(ref_of(c0 + x).x - top);
+          const float4 *src = reinterpret_cast<const float4 *>(part_of(c0 + x)) + 2 * chunk * kPmRows + me;
+          const float4 u = __ldcg(src), v = __ldcg(src + kPmRows);
+          acc[0] = fmaf(u.x, f, acc[0]), acc[1] = fmaf(u.y, f, acc[1]), acc[2] = fmaf(u.z, f, acc[2]);
+          acc[3] = fmaf(u.w, f, acc[3]), acc[4] = fmaf(v.x, f, acc[4]), acc[5] = fmaf(v.y, f, acc[5]);
+          acc[6] = fmaf(v.z, f, acc[6]), acc[7] = fmaf(v.w, f, acc[7]);
+        }
+        *reinterpret_cast<uint4 *>(dst + 8 * chunk) =
+            make_uint4(half2_bits(acc[0] * inv, acc[1] * inv), half2_bits(acc[2] * inv, acc[3] * inv),
+                       half2_bits(acc[4] * inv, acc[5] * inv), half2_bits(acc[6] * inv, acc[7] * inv));
       }
-      const int row = pair * kPmRows + r, tok = row / group, head = h * group + row - tok * group;
-      const int64_t token = static_cast<int64_t>(q0) + tok;
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      *reinterpret_cast<uint4 *>(a.out + token * a.out_stride + static_cast<int64_t>(head) * D + d0) =
-          make_uint4(half2_bits(acc[0] * inv, acc[1] * inv), half2_bits(acc[2] * inv, acc[3] * inv),
-                     half2_bits(acc[4] * inv, acc[5] * inv), half2_bits(acc[6] * inv, acc[7] * inv));
-      if (a.lse && d0 == 0)
-        a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      if (a.lse) a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
   }
 }
