@@ -24,8 +24,12 @@ namespace mixllm {
 // Warp 0 issues the products, warps 4-7 unpack keys and values, warps 8-11 and
 // 12-15 are the softmax of either tile (in this order because the scheduler
 // prefers older warps, and the tensor core waits for warp 0's every
-// instruction).  The two tiles take turns on the tensor core while the other
-// one's softmax runs.
+// instruction).
+//
+// The softmax works on 64 columns at a time: while it is at one half of S, the
+// tensor core multiplies the other half's weights into O and puts the next
+// tile's scores in their place (whole tiles left a tile's softmax waiting for
+// its own products, 1800 of 5000 clocks).  The two tiles do so independently.
 //
 // Unpacking: one thread per token.  A word's nibbles i and i + 4 become fp16
 // integers 1024 + n (or 1024 + 16 n) by one AND-OR, and code - z by one add (or
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
   uint8_t *q_s = smem, *k_s = smem + 2 * kOperand, *v_s = smem + 4 * kOperand;
   float *k_scale = reinterpret_cast<float *>(smem + 6 * kOperand);  // [ring][128], to log2 units
   float *v_scale = k_scale + kPmScaleRing * kPmTile;
-  __shared__ uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  __shared__ uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2];  // s, p: [tile][half]
   __shared__ uint32_t seen[kPmScaleRing][4];   // bit t: token t's page exists
   __shared__ float v_top[kPmScaleRing][4];     // largest value scales of 32 tokens each
   __shared__ uint32_t tmem_slot;
@@ -286,9 +290,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 128);
       mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 2);
-      mbar_init(&p_full[i], 128);
-      mbar_init(&o_full[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s_full[i][h], 2);
+        mbar_init(&p_full[i][h], 128);
+      }
       cut_first[i] = -1;
     }
     fence_mbar_init();
@@ -322,21 +327,23 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       // walk itself inside a one-lane branch a product cost about 300 clocks to
       // issue, ten times the tensor core's: its operands were not known to be
       // uniform.)
-      constexpr uint32_t kQk = idesc_f16(128, 128, false), kPv = idesc_f16(128, D, true);
+      constexpr uint32_t kQk = idesc_f16(128, 64, false), kPv = idesc_f16(128, D, true);
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
       const uint64_t q_desc = sw128_kmajor_desc(smem_u32(q_s)), k_desc = sw128_kmajor_desc(smem_u32(k_s));
       const uint64_t v_desc = sw128_mnmajor_desc(smem_u32(v_s), D > 64 ? kPanel : 16);
-      uint32_t it = 0, q_phase = 0, p_phase = 0;  // bit i: tile i
+      uint32_t it = 0, q_phase = 0, p_phase = 0;  // bit i: tile i; p: bit 2i + h
       bool ok = true;
-      const auto qk = [&](int i, int s) {  // elected lane
-        const uint64_t qa = q_desc + i * (kOperand >> 4), ka = k_desc + s * (kOperand >> 4);
+      const auto qk = [&](int i, int h, int s) {  // elected lane
+        const uint64_t qa = q_desc + i * (kOperand >> 4), ka = k_desc + (s * kOperand + h * 64 * 128 >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
-          mma_f16_ss(tm + i * 128, qa + off, ka + off, kQk, k > 0);
+          mma_f16_ss(tm + i * 128 + h * 64, qa + off, ka + off, kQk, k > 0);
         }
-        mma_commit(&s_full[i]);
-        mbar_arrive(&s_full[i]);  // passes on what this thread saw of the unpacking warps' scales
+      };
+      const auto s_ready = [&](int i, int h) {
+        mma_commit(&s_full[i][h]);
+        mbar_arrive(&s_full[i][h]);  // passes on what this thread saw of the unpacking warps' scales
       };
       for (; w.left > 0 && ok; w.next(a, plan)) {
         const int tiles = w.rows(group) > 128 ? 2 : 1;
@@ -347,7 +354,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           q_phase ^= 1u << i;
           tc_fence_after();
           if (elect_one()) {
-            qk(i, it & 1);
+            for (int h = 0; h < 2; ++h) {
+              qk(i, h, it & 1);
+              s_ready(i, h);
+            }
             if (i + 1 == tiles) mma_commit(&k_empty[it & 1]);
           }
           __syncwarp();
@@ -355,21 +365,22 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
         for (int j = 0; j < w.count && ok; ++j, ++it) {
           const int s = it & 1;
           const bool more = j + 1 < w.count;
-          for (int i = 0; i < tiles; ++i) {
-            ok = warp_wait(&p_full[i], p_phase >> i & 1, &abort_flag);
-            if (i == 0) ok = ok && warp_wait(&v_full[s], it >> 1 & 1, &abort_flag);
-            if (i == 0 && more) ok = ok && warp_wait(&k_full[s ^ 1], (it + 1) >> 1 & 1, &abort_flag);
+          for (int x = 0; x < 2 * tiles; ++x) {
+            const int h = x >= tiles, i = h ? x - tiles : x;
+            ok = warp_wait(&p_full[i][h], p_phase >> (2 * i + h) & 1, &abort_flag);
+            if (x == 0) ok = ok && warp_wait(&v_full[s], it >> 1 & 1, &abort_flag);
+            if (x == 0 && more) ok = ok && warp_wait(&k_full[s ^ 1], (it + 1) >> 1 & 1, &abort_flag);
             if (!ok) break;
-            p_phase ^= 1u << i;
+            p_phase ^= 1u << (2 * i + h);
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t va = v_desc + s * (kOperand >> 4);
+              const uint64_t va = v_desc + (s * kOperand + h * 64 * 128 >> 4);
 #pragma unroll
-              for (int k = 0; k < kPmTile / 16; ++k)
-                mma_f16_ts(tm + 256 + i * D, tm + i * 128 + k * 8, va + k * (2048 >> 4), kPv, j > 0 || k > 0);
-              if (more) qk(i, s ^ 1);
-              else mma_commit(&o_full[i]);
-              if (i + 1 == tiles) {
+              for (int k = 0; k < 4; ++k)
+                mma_f16_ts(tm + 256 + i * D, tm + i * 128 + h * 64 + k * 8, va + k * (2048 >> 4), kPv, x >= tiles || j > 0 || k > 0);
+              if (more) qk(i, h, s ^ 1);
+              s_ready(i, h);  // after the last tile: O has taken this half's weights
+              if (x + 1 == 2 * tiles) {
                 mma_commit(&v_empty[s]);
                 if (more) mma_commit(&k_empty[s ^ 1]);
               }
@@ -379,8 +390,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
         }
       }
       if (!ok && elect_one()) {  // let the products in flight end before tensor memory goes
-        mma_commit(&o_full[0]);
-        mbar_wait_drain(&o_full[0], 0, 1ll << 24);
+        mma_commit(&v_empty[0]);
+        mbar_wait_drain(&v_empty[0], 0, 1ll << 24);
         __nanosleep(100000);
       }
     }
@@ -490,7 +501,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
     const int i = (warp >> 2) - 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * D;
-    uint32_t it = 0, s_phase = 0, o_phase = 0;
+    uint32_t it = 0, s_phase = 0;  // bit h: half h
     bool ok = true;
     for (; w.left > 0 && ok; it += w.count, w.next(a, plan)) {
       const int rows = w.rows(group);
@@ -527,22 +538,24 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       const int lim_min = __shfl_sync(0xFFFFFFFFu, lim, 0);
       float m = kKvNoMax, log_s = -24.0f;  // the reference is m + log_s
       uint64_t sum2 = 0;
-      for (int j = 0; j < w.count; ++j) {
-        const int base = (w.tile + j) * kPmTile, at = (it + j) & (kPmScaleRing - 1);
-        ok = mbar_wait(&s_full[i], s_phase, &abort_flag);
-        s_phase ^= 1;
+      for (int jh = 0; jh < 2 * w.count; ++jh) {
+        const int h = jh & 1, at = (it + (jh >> 1)) & (kPmScaleRing - 1);
+        const int base = (w.tile + (jh >> 1)) * kPmTile + 64 * h;
+        const uint32_t sh_at = s_at + 64 * h;
+        ok = mbar_wait(&s_full[i][h], s_phase >> h & 1, &abort_flag);
+        s_phase ^= 1u << h;
         if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const float *ks = k_scale + at * kPmTile, *vs = v_scale + at * kPmTile;
-        const uint4 there = *reinterpret_cast<const uint4 *>(seen[at]);
-        const bool whole = base + kPmTile <= lim_min && (there.x & there.y & there.z & there.w) == 0xFFFFFFFFu;
+        const float *ks = k_scale + at * kPmTile + 64 * h, *vs = v_scale + at * kPmTile + 64 * h;
+        const uint2 there = *reinterpret_cast<const uint2 *>(&seen[at][2 * h]);
+        const bool whole = base + 64 <= lim_min && (there.x & there.y) == 0xFFFFFFFFu;
         // bit k: column 32 b + k is seen by this row
         const auto visible = [&](int b) {
           const int n = lim - base - 32 * b;
-          return (b == 0 ? there.x : b == 1 ? there.y : b == 2 ? there.z : there.w) &
+          return (b == 0 ? there.x : there.y) &
                  (n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u));
         };
         // the row's largest score
@@ -550,9 +563,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           constexpr bool kAll = decltype(all)::value;  // every column is seen by every row of the warp
           float top = -INFINITY;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
+          for (int b = 0; b < 2; ++b) {
             uint32_t c[32];
-            tmem_ld_32x32b_x32(s_at + 32 * b, c);
+            tmem_ld_32x32b_x32(sh_at + 32 * b, c);
             tmem_ld_wait();
             reg_fence(c);
             const uint32_t see = kAll ? 0xFFFFFFFFu : visible(b);
@@ -566,20 +579,20 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
         };
         // the row's weights p s_v, relative to the reference; adds sum p to sum2 and returns the largest score
         // above the reference
-        uint32_t p[64];
+        uint32_t p[32];
         const auto weights = [&](auto all) {
           constexpr bool kAll = decltype(all)::value;
           const float ref = -(m + log_s);
           const uint64_t ref2 = pack_f2(ref, ref);
           uint32_t x[2][32];
           float hi[2] = {-INFINITY, -INFINITY};
-          tmem_ld_32x32b_x32(s_at, x[0]);
+          tmem_ld_32x32b_x32(sh_at, x[0]);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            uint32_t(&c)[32] = x[b & 1];
+          for (int b = 0; b < 2; ++b) {
+            uint32_t(&c)[32] = x[b];
             tmem_ld_wait();
             reg_fence(c);
-            if (b < 3) tmem_ld_32x32b_x32(s_at + 32 * (b + 1), x[(b + 1) & 1]);
+            if (b == 0) tmem_ld_32x32b_x32(sh_at + 32, x[1]);
             const uint32_t see = kAll ? 0xFFFFFFFFu : visible(b);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -607,7 +620,11 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           const float keep = ex2((m - m_new) + (log_s - ls_new));
           m = m_new, log_s = ls_new;
           sum2 = mul_f2(sum2, pack_f2(keep, keep));
-          if (j > 0) {  // the products into O are done: s_full followed them
+          if (jh > 0) {
+            // no product into O may be under way: this half's last one came before its s_full, the other
+            // half's before the s_full that this thread waits for next
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_full[i][h ^ 1], s_phase >> (h ^ 1) & 1, &abort_flag))) return;
+            tc_fence_after();
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) {
               uint32_t o[32];
@@ -639,18 +656,15 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           sum2 = sum_before;
           move_to(over > 8.0f ? m + over : m, log_s);
         }
-        {
-          uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(p), (&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(p + 32);
-          tmem_st_32x32b_x32(s_at, lo);  // over the columns of S
-          tmem_st_32x32b_x32(s_at + 32, hi);
-        }
+        tmem_st_32x32b_x32(sh_at, p);  // over the half's first columns
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_full[i]);
+        mbar_arrive(&p_full[i][h]);
       }
       if (!ok) break;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[i], o_phase, &abort_flag));
-      o_phase ^= 1;
+      ok = mbar_wait(&s_full[i][0], s_phase & 1, &abort_flag) && mbar_wait(&s_full[i][1], s_phase >> 1 & 1, &abort_flag);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      s_phase ^= 3u;
       if (!ok) break;
       tc_fence_after();
       const float2 both = unpack_f2(sum2);
