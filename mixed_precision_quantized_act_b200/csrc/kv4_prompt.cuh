@@ -49,10 +49,12 @@ namespace mixllm {
 // Bound by the tensor core (4 D flops per row and token) and, close behind, by
 // the exponentials: 16 a clock and SM make a 128 x 128 tile 1024 clocks, its two
 // products at D = 128 take 1024.  Blocks take equal shares of all (tile
-// pair, head, token tile) units in one sequence; the ends of a share cut a
-// pair's tokens in two, and the parts are joined as in the decode kernel.  The
-// sequence depends on lengths that only the device knows: a small kernel before
-// this one lists the pairs and the running sum of their tiles.
+// pair, head, token tile) units in one sequence; where the ends of a share cut a
+// pair's tokens, the parts go to the workspace and a third kernel joins them in
+// the order of the tokens (joined by the last block to arrive, 25 us of one SM's
+// work stood behind everything).  The sequence depends on lengths that only the
+// device knows: a small kernel before this one lists the pairs and the running
+// sum of their tiles.
 // ---------------------------------------------------------------------------
 constexpr int kPmThreads = 512;
 constexpr int kPmTile = 128;
@@ -69,17 +71,26 @@ struct PmCfg {
   static_assert(kSmem + 1024 <= 227 * 1024, "shared memory of a block");
 };
 
-// The list of tile pairs: (request, pair), and the token tiles before each.
+// A segment that the end of a block cuts: the blocks first .. last hold parts
+// of it (last < first: none).
+struct PmCut {
+  int last, pair, h, q0, n;
+};
+
+// The list of tile pairs: (request, pair), and the token tiles before each; and
+// the blocks' cuts.
 struct PmPlan {
   int *entries;
   int64_t *cum;  // [entries + 1]
   int2 *ent;     // [entries]
+  PmCut *cuts;   // [blocks]
 };
 
 constexpr int kPmPlanThreads = 1024;
 
 __global__ void __launch_bounds__(kPmPlanThreads) kv4_prompt_plan_kernel(const AttendArgs a, const PmPlan plan) {
   extern __shared__ int pair_base[];  // pairs before each request
+  pdl_launch_dependents();
   __shared__ long long warp_sum[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.Hq / a.cache.H;
@@ -243,7 +254,7 @@ __device__ __forceinline__ uint4 unpack_codes(uint32_t w, uint32_t zlo, uint32_t
 
 template <int D>
 __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendArgs a, const PmPlan plan,
-                                                                 uint32_t *counters, float *parts) {
+                                                                 float *parts) {
   using C = PmCfg<D>;
   constexpr int kPanel = C::kPanel, kOperand = C::kOperand;
   extern __shared__ uint8_t smem_raw[];
@@ -257,16 +268,31 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ int first_e;
-  __shared__ long long cut_first[2];
-  __shared__ int cut_seg[2][5];  // pair, head, q0, n, tiles
-  __shared__ int join_blocks[2][2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.Hq / a.cache.H, H = a.cache.H;
   const int c = blockIdx.x;
+  if (tid == 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&k_full[i], 128);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 128);
+      mbar_init(&v_empty[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s_full[i][h], 2);
+        mbar_init(&p_full[i][h], 128);
+      }
+    }
+    fence_mbar_init();
+    abort_flag = 0;
+  }
+  pdl_launch_dependents();
+  pdl_wait();  // the plan, and with it all that came before it
   const int E = *plan.entries;
   const int64_t U = plan.cum[E] * H;
   const int P = U < gridDim.x ? static_cast<int>(U) : static_cast<int>(gridDim.x);
+  if (tid == 0) plan.cuts[c].last = -1;
   if (c >= P) return;  // every other block has a unit
   const int64_t share = U / P;
   const int rest = static_cast<int>(U - share * P);
@@ -282,22 +308,6 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       hi = min(hi, lo + step);
     }
     if (lane == 0) first_e = lo;
-  }
-  if (tid == 32) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 128);
-      mbar_init(&k_full[i], 128);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 128);
-      mbar_init(&v_empty[i], 1);
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(&s_full[i][h], 2);
-        mbar_init(&p_full[i][h], 128);
-      }
-      cut_first[i] = -1;
-    }
-    fence_mbar_init();
-    abort_flag = 0;
   }
   if (warp == 0) {
     tmem_alloc(&tmem_slot, 512);
@@ -712,11 +722,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       tc_fence_before();
       if (cut) {
         *reinterpret_cast<float2 *>(part + static_cast<int64_t>(kPmRows) * D + 2 * (i * 128 + r)) = make_float2(ref, sum);
-        if (tid == 256) {
-          cut_first[side] = w.seg_first;
-          cut_seg[side][0] = w.pair, cut_seg[side][1] = w.h, cut_seg[side][2] = w.q0, cut_seg[side][3] = w.n;
-          cut_seg[side][4] = w.tiles;
-        }
+        if (tid == 256 && side == 1)  // the segment's last block: unit x is in block ((x + 1) P - 1) / U
+          plan.cuts[c] = PmCut{static_cast<int>(((w.seg_first + w.tiles) * P - 1) / U), w.pair, w.h, w.q0, w.n};
       } else if (valid && a.lse) {
         a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       }
@@ -724,75 +731,56 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
   }
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 512);
-  if (warp < 8) return;
-  const int me = tid - 256;
+}
 
-  // ---- segments cut between blocks: the last block to get here joins the parts
-  if (me < 2) {
-    join_blocks[me][1] = -1;
-    if (cut_first[me] >= 0) {
-      const int c0 = static_cast<int>(((cut_first[me] + 1) * P - 1) / U);
-      const int c1 = static_cast<int>(((cut_first[me] + cut_seg[me][4]) * P - 1) / U);
-      __threadfence();
-      const uint32_t before = atom_add_acq_rel_gpu_u32(counters + c0, 1u);
-      if (before == static_cast<uint32_t>(c1 - c0)) {
-        counters[c0] = 0;
-        join_blocks[me][0] = c0;
-        join_blocks[me][1] = c1;
-      }
-    }
-  }
-  named_bar_sync(1, 256);
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    const int c0 = join_blocks[side][0], c1 = join_blocks[side][1];
-    if (c1 < 0) continue;
-    __threadfence();
-    const int pair = cut_seg[side][0], h = cut_seg[side][1], q0 = cut_seg[side][2], n = cut_seg[side][3];
-    const int rows = min(kPmRows, n * group - pair * kPmRows);
-    // the segment is the first block's last one and every other's first one
-    const auto part_of = [&](int b) { return parts + (static_cast<int64_t>(b) * 2 + (b == c0 ? 1 : 0)) * C::kPart; };
-    // thread = row: the parts' weights into shared memory (as many as there are blocks fit), then their sums
-    float *weight = reinterpret_cast<float *>(smem) + me;  // [part][row]
-    const int n_parts = c1 - c0 + 1;
-    constexpr int kAtOnce = 6 * kOperand / (kPmRows * 4);
-    const auto ref_of = [&](int b) {
-      return __ldcg(reinterpret_cast<const float2 *>(part_of(b) + static_cast<int64_t>(kPmRows) * D + 2 * me));
-    };
-    float top = -INFINITY, sum = 0.0f;
+// Joins a cut segment's parts, 32 rows a block: lane = row, a warp an eighth of
+// the channels.  Block x's parts are those of the segment that block x of the
+// kernel before was the first to hold.
+template <int D>
+__global__ void __launch_bounds__(256) kv4_prompt_join_kernel(const AttendArgs a, const PmPlan plan,
+                                                              const float *__restrict__ parts) {
+  pdl_wait();
+  using C = PmCfg<D>;
+  const int c0 = blockIdx.x, group = a.Hq / a.cache.H;
+  const PmCut cut = plan.cuts[c0];
+  const int r = blockIdx.y * 32 + (threadIdx.x & 31), row = cut.pair * kPmRows + r;
+  if (cut.last < c0 || row >= cut.n * group) return;
+  constexpr int kVec = D / 32;  // of four channels
+  const int k0 = (threadIdx.x >> 5) * kVec;
+  // the segment is the first block's last one and every other's first one
+  const auto part_of = [&](int b) { return parts + (static_cast<int64_t>(b) * 2 + (b == c0 ? 1 : 0)) * C::kPart; };
+  const auto ref_of = [&](int b) {
+    return *reinterpret_cast<const float2 *>(part_of(b) + static_cast<int64_t>(kPmRows) * D + 2 * r);
+  };
+  float top = -INFINITY, sum = 0.0f;
 #pragma unroll 4
-    for (int b = c0; b <= c1; ++b) top = fmaxf(top, ref_of(b).x);
-#pragma unroll 4
-    for (int b = c0; b <= c1; ++b) {
-      const float2 rl = ref_of(b);
-      const float f = ex2(rl.x - top);
-      sum = fmaf(rl.y, f, sum);
-      if (b - c0 < kAtOnce) weight[(b - c0) * kPmRows] = f;
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int row = pair * kPmRows + me, tok = row / group, head = h * group + row - tok * group;
-    const int64_t token = static_cast<int64_t>(q0) + tok;
-    if (me < rows) {
-      __half *dst = a.out + token * a.out_stride + static_cast<int64_t>(head) * D;
+  for (int b = c0; b <= cut.last; ++b) top = fmaxf(top, ref_of(b).x);
+  float4 acc[kVec];
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 2
-      for (int chunk = 0; chunk < D / 8; ++chunk) {
-        float acc[8] = {};
-#pragma unroll 4
-        for (int x = 0; x < n_parts; ++x) {
-          const float f = x < kAtOnce ? weight[x * kPmRows] : ex2(ref_of(c0 + x).x - top);
-          const float4 *src = reinterpret_cast<const float4 *>(part_of(c0 + x)) + 2 * chunk * kPmRows + me;
-          const float4 u = __ldcg(src), v = __ldcg(src + kPmRows);
-          acc[0] = fmaf(u.x, f, acc[0]), acc[1] = fmaf(u.y, f, acc[1]), acc[2] = fmaf(u.z, f, acc[2]);
-          acc[3] = fmaf(u.w, f, acc[3]), acc[4] = fmaf(v.x, f, acc[4]), acc[5] = fmaf(v.y, f, acc[5]);
-          acc[6] = fmaf(v.z, f, acc[6]), acc[7] = fmaf(v.w, f, acc[7]);
-        }
-        *reinterpret_cast<uint4 *>(dst + 8 * chunk) =
-            make_uint4(half2_bits(acc[0] * inv, acc[1] * inv), half2_bits(acc[2] * inv, acc[3] * inv),
-                       half2_bits(acc[4] * inv, acc[5] * inv), half2_bits(acc[6] * inv, acc[7] * inv));
-      }
-      if (a.lse) a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  for (int b = c0; b <= cut.last; ++b) {
+    const float2 rl = ref_of(b);
+    const float f = ex2(rl.x - top);
+    sum = fmaf(rl.y, f, sum);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const float4 v = reinterpret_cast<const float4 *>(part_of(b))[(k0 + k) * kPmRows + r];
+      acc[k].x = fmaf(v.x, f, acc[k].x), acc[k].y = fmaf(v.y, f, acc[k].y);
+      acc[k].z = fmaf(v.z, f, acc[k].z), acc[k].w = fmaf(v.w, f, acc[k].w);
     }
   }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int tok = row / group, head = cut.h * group + row - tok * group;
+  const int64_t token = static_cast<int64_t>(cut.q0) + tok;
+  uint4 *dst = reinterpret_cast<uint4 *>(a.out + token * a.out_stride + static_cast<int64_t>(head) * D + 4 * k0);
+#pragma unroll
+  for (int k = 0; k < kVec; k += 2) {
+    const float4 u = acc[k], v = acc[k + 1];
+    dst[k / 2] = make_uint4(half2_bits(u.x * inv, u.y * inv), half2_bits(u.z * inv, u.w * inv),
+                            half2_bits(v.x * inv, v.y * inv), half2_bits(v.z * inv, v.w * inv));
+  }
+  if (a.lse && k0 == 0) a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------------------
@@ -803,7 +791,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
 static int64_t pm_max_entries(int B, int max_q, int group) {
   return static_cast<int64_t>(B) * ((static_cast<int64_t>(max_q) * group + kPmRows - 1) / kPmRows);
 }
-static size_t pm_plan_bytes(int64_t entries) { return (256 + (entries + 1) * 8 + entries * 8 + 255) / 256 * 256; }
+constexpr size_t kPmPlanHead = 4096;  // entries, then the blocks' cuts from byte 256
+static_assert(256 + kPmMaxGrid * sizeof(PmCut) <= kPmPlanHead, "room for the cuts");
+static size_t pm_plan_bytes(int64_t entries) { return (kPmPlanHead + (entries + 1) * 8 + entries * 8 + 255) / 256 * 256; }
 
 static size_t kv4_prompt_workspace_bytes(int B, int max_q, int group, int D) {
   return kKvCounterBytes + pm_plan_bytes(pm_max_entries(B, max_q, group)) +
@@ -833,20 +823,34 @@ static cudaError_t launch_kv4_prompt(const AttendArgs &a, void *ws, cudaStream_t
   uint8_t *at = static_cast<uint8_t *>(ws) + kKvCounterBytes;
   PmPlan plan;
   plan.entries = reinterpret_cast<int *>(at);
-  plan.cum = reinterpret_cast<int64_t *>(at + 256);
-  plan.ent = reinterpret_cast<int2 *>(at + 256 + (entries + 1) * 8);
+  plan.cuts = reinterpret_cast<PmCut *>(at + 256);
+  plan.cum = reinterpret_cast<int64_t *>(at + kPmPlanHead);
+  plan.ent = reinterpret_cast<int2 *>(at + kPmPlanHead + (entries + 1) * 8);
   float *parts = reinterpret_cast<float *>(at + pm_plan_bytes(entries));
+  const int64_t tiles = ((static_cast<int64_t>(a.W) << a.cache.page_log2) + kPmTile - 1) / kPmTile;
+  const int64_t units = entries * a.cache.H * (tiles > 0 ? tiles : 1);
+  int64_t grid = device_sm_count();
+  if (grid > kPmMaxGrid) grid = kPmMaxGrid;
+  if (grid > units) grid = units;
   kv4_prompt_plan_kernel<<<1, kPmPlanThreads, a.B * sizeof(int), stream>>>(a, plan);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) {
-    const int64_t tiles = ((static_cast<int64_t>(a.W) << a.cache.page_log2) + kPmTile - 1) / kPmTile;
-    const int64_t units = entries * a.cache.H * (tiles > 0 ? tiles : 1);
-    int64_t grid = device_sm_count();
-    if (grid > kPmMaxGrid) grid = kPmMaxGrid;
-    if (grid > units) grid = units;
-    kern<<<static_cast<unsigned>(grid), kPmThreads, C::kSmem, stream>>>(a, plan, static_cast<uint32_t *>(ws), parts);
-    e = cudaGetLastError();
-  }
+  // the other two start while the one before them ends, and wait for its results themselves
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kPmThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, a, plan, parts);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), kPmRows / 32);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kv4_prompt_join_kernel<D>, a, plan, static_cast<const float *>(parts));
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) *msg = "launch of the prompt attention failed";
   return e;
 }
