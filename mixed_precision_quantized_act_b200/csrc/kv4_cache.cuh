@@ -115,21 +115,37 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const Assign
     const int b = owner_of(off, B, e);
     a.table[static_cast<int64_t>(b) * a.table_stride + pages(ctx[b]) + (e - off[b])] = a.free_pages[count - 1 - e];
   }
-  for (int64_t t = first; t < a.T; t += stride) {
-    int64_t slot = -1;
-    int pos = -1;
-    if (t < total) {
-      const int b = owner_of(cu, B, static_cast<int>(t));
-      pos = ctx[b] + (static_cast<int>(t) - cu[b]);
-      const int j = pos >> a.page_log2, have = static_cast<int>(pages(ctx[b]));
-      // a page of this call is read where it came from: its table entry may still be on its way
-      const int page = j < have ? a.table[static_cast<int64_t>(b) * a.table_stride + j]
-                                : a.free_pages[count - 1 - (off[b] + j - have)];
-      if (page < 0) record_status(kStatusBounds);
-      else slot = (static_cast<int64_t>(page) << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
+  // A warp takes a run of tokens, 32 at a time: one search for the first, then the owner moves along.  Four
+  // times 32 tokens' page loads are under way together.
+  constexpr int kAtOnce = 4;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAssignThreads / 32);
+  const int64_t run = ((a.T + warps - 1) / warps + 31) / 32 * 32;
+  const int64_t begin = (static_cast<int64_t>(blockIdx.x) * (kAssignThreads / 32) + warp) * run;
+  const int64_t stop = begin + run < a.T ? begin + run : a.T;
+  int b = begin + lane < total ? owner_of(cu, B, static_cast<int>(begin) + lane) : 0;
+  for (int64_t t0 = begin + lane; t0 < stop; t0 += 32 * kAtOnce) {
+    int page[kAtOnce], pos[kAtOnce];
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      const int64_t t = t0 + 32 * x;
+      page[x] = pos[x] = -1;
+      if (t < total && t < stop) {
+        while (b + 1 < B && cu[b + 1] <= t) ++b;
+        pos[x] = ctx[b] + (static_cast<int>(t) - cu[b]);
+        const int j = pos[x] >> a.page_log2, have = static_cast<int>(pages(ctx[b]));
+        // a page of this call is read where it came from: its table entry may still be on its way
+        page[x] = j < have ? a.table[static_cast<int64_t>(b) * a.table_stride + j]
+                           : a.free_pages[count - 1 - (off[b] + j - have)];
+      }
     }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      const int64_t t = t0 + 32 * x;
+      if (t >= stop) break;
+      if (t < total && page[x] < 0) record_status(kStatusBounds);
+      a.slots[t] = page[x] < 0 ? -1 : (static_cast<int64_t>(page[x]) << a.page_log2) + (pos[x] & ((1 << a.page_log2) - 1));
+      a.positions[t] = pos[x];
+    }
   }
 }
 
@@ -142,7 +158,9 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const Assign
 // channels (w4_params, w4_code).  A row that holds a NaN or an infinity is
 // stored with a NaN scale: it reads back as NaN instead of as something
 // finite.  HBM-bound: reads 2 bytes and writes 0.5 (keys, values) or 2
-// (queries) a channel.
+// (queries) a channel.  A lane takes `per` heads of its token, so that the
+// table's 8 bytes a channel are read once for all of them, and loads four heads
+// ahead (one head at a time: 62 us for 4099 tokens of 64 + 16 heads of 128).
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 
@@ -153,88 +171,105 @@ __device__ __forceinline__ int64_t kv4_row(const Kv4Cache &c, int64_t slot, int 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const AppendArgs a) {
-  constexpr int kLanes = D / 8;
+__global__ void __launch_bounds__(kAppendThreads, 4) kv4_append_kernel(const AppendArgs a, int per) {
+  constexpr int kLanes = D / 8, kAhead = 4;
   const int sub = threadIdx.x % kLanes;
-  const unsigned mask = (kLanes == 32 ? 0xFFFFFFFFu : ((1u << kLanes) - 1u)) << (threadIdx.x & 31 & ~(kLanes - 1));
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kAppendThreads / kLanes);
+  const unsigned mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
   const int rows = a.Hq + 2 * a.cache.H;
-  const int half = a.rotary / 2;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / kLanes) + threadIdx.x / kLanes;
-       i < a.T * rows; i += stride) {
-    const int64_t t = i / rows;
-    const int h = static_cast<int>(i - t * rows);
-    const int64_t slot = a.slots[t];
-    if (slot < 0) continue;  // padding behind the last token
-    int64_t pos = a.rope ? a.positions[t] : 0;
-    if (slot >= a.cache.pages << a.cache.page_log2 || pos < 0 || (a.rope && pos >= a.max_pos)) {
-      if (sub == 0) record_status(kStatusBounds);
-      continue;
-    }
-    const int kind = h < a.Hq ? 0 : (h < a.Hq + a.cache.H ? 1 : 2);  // query, key, value
-    const int head = kind == 0 ? h : (kind == 1 ? h - a.Hq : h - a.Hq - a.cache.H);
-    const __half *src = kind == 0 ? a.q + t * a.q_stride : (kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride);
-    uint4 raw = *reinterpret_cast<const uint4 *>(src + head * D + sub * 8);
-    if (kind < 2 && half > 0) {
-      const int c0 = sub * 8;  // half is a multiple of 8: a lane lies in one half, or behind both
-      const bool second = c0 >= half;
-      const int other = second ? sub - half / 8 : sub + half / 8;
-      uint4 far;
-      far.x = __shfl_sync(mask, raw.x, other, kLanes);
-      far.y = __shfl_sync(mask, raw.y, other, kLanes);
-      far.z = __shfl_sync(mask, raw.z, other, kLanes);
-      far.w = __shfl_sync(mask, raw.w, other, kLanes);
-      if (c0 < a.rotary) {
-        const float *angle = a.rope + pos * a.rotary + (second ? c0 - half : c0);
-        float cs[8], sn[8], own[8], oth[8];
-        load8(angle, cs);
-        load8(angle + half, sn);
-        const __half2 *h0 = reinterpret_cast<const __half2 *>(&raw), *h1 = reinterpret_cast<const __half2 *>(&far);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / kLanes) + threadIdx.x / kLanes;
+  if (t >= a.T) return;
+  const int64_t slot = a.slots[t];
+  if (slot < 0) return;  // padding behind the last token
+  const int64_t pos = a.rope ? a.positions[t] : 0;
+  if (slot >= a.cache.pages << a.cache.page_log2 || pos < 0 || (a.rope && pos >= a.max_pos)) {
+    if (sub == 0) record_status(kStatusBounds);
+    return;
+  }
+  // a lane lies in one half of the rotated channels, or behind both: half is a multiple of 8
+  const int half = a.rotary / 2, c0 = sub * 8;
+  const bool second = c0 >= half, turned = c0 < a.rotary;
+  const int other = second ? sub - half / 8 : sub + half / 8;
+  float cs[8], sn[8];  // sn negative in the first half: x cos - y sin is x cos + y (-sin), rounding and all
+  if (turned) {
+    const float *angle = a.rope + pos * a.rotary + (second ? c0 - half : c0);
+    load8(angle, cs);
+    load8(angle + half, sn);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 u = __half22float2(h0[j]), w = __half22float2(h1[j]);
-          own[2 * j] = u.x, own[2 * j + 1] = u.y, oth[2 * j] = w.x, oth[2 * j + 1] = w.y;
-        }
+    for (int j = 0; j < 8; ++j) sn[j] = second ? sn[j] : -sn[j];
+  }
+  const __half *q_row = a.q + t * a.q_stride + c0, *k_row = a.k + t * a.k_stride + c0, *v_row = a.v + t * a.v_stride + c0;
+  __half *q_to = a.q_out + t * a.q_out_stride + c0;
+  const int64_t first_row = kv4_row(a.cache, slot, 0, 0), to_value = static_cast<int64_t>(a.cache.H) << a.cache.page_log2;
+  const int h_end = min(rows, static_cast<int>(blockIdx.y + 1) * per);
+  for (int h0 = blockIdx.y * per; h0 < h_end; h0 += kAhead) {
+    uint4 ahead[kAhead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float near_part = __fmul_rn(own[j], cs[j]), far_part = __fmul_rn(oth[j], sn[j]);
-          own[j] = second ? __fadd_rn(near_part, far_part) : __fsub_rn(near_part, far_part);
-        }
-        raw = pack8(own);
+    for (int x = 0; x < kAhead; ++x) {
+      const int h = h0 + x;
+      if (h < h_end) {
+        const __half *src = h < a.Hq ? q_row + h * D
+                                     : (h < a.Hq + a.cache.H ? k_row + (h - a.Hq) * D : v_row + (h - a.Hq - a.cache.H) * D);
+        ahead[x] = *reinterpret_cast<const uint4 *>(src);
       }
     }
-    if (kind == 0) {
-      *reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + head * D + sub * 8) = raw;
-      continue;
-    }
-    const __half2 *h2 = reinterpret_cast<const __half2 *>(&raw);
-    float x[8], lo = 0.0f, hi = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(h2[j]);
-      x[2 * j] = f.x, x[2 * j + 1] = f.y;
-    }
-    bool odd = false;
+    for (int x = 0; x < kAhead; ++x) {
+      const int h = h0 + x;
+      if (h >= h_end) break;
+      uint4 raw = ahead[x];
+      if (half > 0 && h < a.Hq + a.cache.H) {
+        uint4 far;
+        far.x = __shfl_sync(mask, raw.x, other, kLanes);
+        far.y = __shfl_sync(mask, raw.y, other, kLanes);
+        far.z = __shfl_sync(mask, raw.z, other, kLanes);
+        far.w = __shfl_sync(mask, raw.w, other, kLanes);
+        if (turned) {
+          const __half2 *n2 = reinterpret_cast<const __half2 *>(&raw), *f2 = reinterpret_cast<const __half2 *>(&far);
+          float own[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lo = fminf(lo, x[j]), hi = fmaxf(hi, x[j]);
-      odd |= !(fabsf(x[j]) <= 65504.0f);
-    }
+          for (int j = 0; j < 4; ++j) {
+            const float2 u = __half22float2(n2[j]), w = __half22float2(f2[j]);
+            own[2 * j] = __fadd_rn(__fmul_rn(u.x, cs[2 * j]), __fmul_rn(w.x, sn[2 * j]));
+            own[2 * j + 1] = __fadd_rn(__fmul_rn(u.y, cs[2 * j + 1]), __fmul_rn(w.y, sn[2 * j + 1]));
+          }
+          raw = pack8(own);
+        }
+      }
+      if (h < a.Hq) {
+        *reinterpret_cast<uint4 *>(q_to + h * D) = raw;
+        continue;
+      }
+      const __half2 *h2 = reinterpret_cast<const __half2 *>(&raw);
+      float v[8], lo = 0.0f, hi = 0.0f;
+      bool odd = false;
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
-    }
-    uint32_t code = 0, meta = 0x7FFFu;
-    if (!__any_sync(mask, odd)) {
-      const W4Params p = w4_params(lo, hi);
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(h2[j]);
+        v[2 * j] = f.x, v[2 * j + 1] = f.y;
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) code |= static_cast<uint32_t>(w4_code(x[j], p)) << (4 * j);
-      meta = static_cast<uint32_t>(__half_as_ushort(p.sh)) | static_cast<uint32_t>(p.z) << 16;
+      for (int j = 0; j < 8; ++j) {
+        lo = fminf(lo, v[j]), hi = fmaxf(hi, v[j]);
+        odd |= !(fabsf(v[j]) <= 65504.0f);
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
+      }
+      uint32_t code = 0, meta = 0x7FFFu;
+      if (!__any_sync(mask, odd)) {
+        const W4Params p = w4_params(lo, hi);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) code |= static_cast<uint32_t>(w4_code(v[j], p)) << (4 * j);
+        meta = static_cast<uint32_t>(__half_as_ushort(p.sh)) | static_cast<uint32_t>(p.z) << 16;
+      }
+      const bool value = h >= a.Hq + a.cache.H;
+      const int64_t row = first_row + (value ? to_value : 0) +
+                          (static_cast<int64_t>(h - a.Hq - (value ? a.cache.H : 0)) << a.cache.page_log2);
+      *reinterpret_cast<uint32_t *>(a.cache.codes + row * (D / 2) + sub * 4) = code;
+      if (sub == 0) a.cache.meta[row] = meta;
     }
-    const int64_t row = kv4_row(a.cache, slot, kind - 1, head);
-    *reinterpret_cast<uint32_t *>(a.cache.codes + row * (D / 2) + sub * 4) = code;
-    if (sub == 0) a.cache.meta[row] = meta;
   }
 }
 
@@ -244,30 +279,30 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Append
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) kv4_read_kernel(const Kv4Cache c, const int64_t *__restrict__ slots,
                                                                   int64_t T, __half *__restrict__ k,
-                                                                  __half *__restrict__ v) {
+                                                                  __half *__restrict__ v, int per) {
   constexpr int kLanes = D / 8;
   const int sub = threadIdx.x % kLanes;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kAppendThreads / kLanes);
-  const int rows = 2 * c.H;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / kLanes) + threadIdx.x / kLanes; i < T * rows;
-       i += stride) {
-    const int64_t t = i / rows;
-    const int h = static_cast<int>(i - t * rows);
-    const int64_t slot = slots[t];
-    if (slot < 0) continue;
-    if (slot >= c.pages << c.page_log2) {
-      if (sub == 0) record_status(kStatusBounds);
-      continue;
-    }
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / kLanes) + threadIdx.x / kLanes;
+  if (t >= T) return;
+  const int64_t slot = slots[t];
+  if (slot < 0) return;
+  if (slot >= c.pages << c.page_log2) {
+    if (sub == 0) record_status(kStatusBounds);
+    return;
+  }
+  const int h_end = min(2 * c.H, static_cast<int>(blockIdx.y + 1) * per);
+#pragma unroll 4
+  for (int h = blockIdx.y * per; h < h_end; ++h) {
     const int kv = h >= c.H, head = kv ? h - c.H : h;
     const int64_t row = kv4_row(c, slot, kv, head);
     const uint32_t code = *reinterpret_cast<const uint32_t *>(c.codes + row * (D / 2) + sub * 4), meta = c.meta[row];
     const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(meta & 0xFFFFu)));
-    const int z = static_cast<int>(meta >> 16 & 15u);
+    // code + 2^23 as a float, less z + 2^23: the difference, exactly
+    const float z = __uint_as_float(0x4B000000u | (meta >> 16 & 15u));
     float f[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float x = static_cast<float>(static_cast<int>(code >> (4 * j) & 15u) - z) * s;
+      const float x = (__uint_as_float(0x4B000000u | (code >> (4 * j) & 15u)) - z) * s;
       f[j] = x > 65504.0f ? 65504.0f : (x < -65504.0f ? -65504.0f : x);  // a NaN stays one
     }
     *reinterpret_cast<uint4 *>((kv ? v : k) + (t * c.H + head) * D + sub * 8) = pack8(f);
@@ -310,24 +345,34 @@ cudaError_t launch_kv4_assign(const AssignArgs &a, cudaStream_t stream, const ch
   return e;
 }
 
-static unsigned append_grid(int64_t rows, int D) {
-  const int64_t blocks = (rows + kAppendThreads / (D / 8) - 1) / (kAppendThreads / (D / 8));
-  return static_cast<unsigned>(blocks < 148 * 64 ? blocks : 148 * 64);
+// Heads of one lane: eight where the call fills the GPU all the same, one where
+// it is latency that counts.
+static int heads_per_lane(int64_t T, int rows, int D) {
+  const int64_t lanes = T * rows * (D / 8);
+  int per = lanes >= 8ll * 148 * 2048 ? 8 : 1;
+  while ((rows + per - 1) / per > 65535) ++per;
+  return per;
+}
+static dim3 append_grid(int64_t T, int rows, int D, int per) {
+  const int tokens = kAppendThreads / (D / 8);
+  return dim3(static_cast<unsigned>((T + tokens - 1) / tokens), static_cast<unsigned>((rows + per - 1) / per));
 }
 
 cudaError_t launch_kv4_append(const AppendArgs &a, cudaStream_t stream) {
-  const unsigned grid = append_grid(a.T * (a.Hq + 2 * a.cache.H), a.cache.D);
-  if (a.cache.D == 128) kv4_append_kernel<128><<<grid, kAppendThreads, 0, stream>>>(a);
-  else kv4_append_kernel<64><<<grid, kAppendThreads, 0, stream>>>(a);
+  const int rows = a.Hq + 2 * a.cache.H, per = heads_per_lane(a.T, rows, a.cache.D);
+  const dim3 grid = append_grid(a.T, rows, a.cache.D, per);
+  if (a.cache.D == 128) kv4_append_kernel<128><<<grid, kAppendThreads, 0, stream>>>(a, per);
+  else kv4_append_kernel<64><<<grid, kAppendThreads, 0, stream>>>(a, per);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_read(const Kv4Cache &c, const int64_t *slots, int64_t T, void *k, void *v,
                             cudaStream_t stream) {
-  const unsigned grid = append_grid(T * 2 * c.H, c.D);
+  const int per = heads_per_lane(T, 2 * c.H, c.D);
+  const dim3 grid = append_grid(T, 2 * c.H, c.D, per);
   __half *kh = static_cast<__half *>(k), *vh = static_cast<__half *>(v);
-  if (c.D == 128) kv4_read_kernel<128><<<grid, kAppendThreads, 0, stream>>>(c, slots, T, kh, vh);
-  else kv4_read_kernel<64><<<grid, kAppendThreads, 0, stream>>>(c, slots, T, kh, vh);
+  if (c.D == 128) kv4_read_kernel<128><<<grid, kAppendThreads, 0, stream>>>(c, slots, T, kh, vh, per);
+  else kv4_read_kernel<64><<<grid, kAppendThreads, 0, stream>>>(c, slots, T, kh, vh, per);
   return cudaGetLastError();
 }
 

@@ -79,57 +79,74 @@ __device__ __forceinline__ void store8_rounded(float *p, float (&f)[8]) {
 // The sums of squares are held in fp32: a thread adds at most 8 V squares and
 // the block adds the threads' sums as a tree.  Without x, r' = r.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void widen8(const uint4 raw, float (&f)[8]) {
+  const __half2 *h = reinterpret_cast<const __half2 *>(&raw);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(h[i]);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+
 template <typename R, int V>
-__global__ void __launch_bounds__(1024) residual_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(V == 1 ? 512 : 1024) residual_norm_kernel(const NormArgs a) {
   __shared__ float part[2][32];
   const int64_t m = blockIdx.x;
   const int K = static_cast<int>(a.K);
   const int step = blockDim.x * 8;
+  // every load of the row is issued before the first sum, as far as the registers go
+  constexpr bool kAhead = V < 4;
   float r[V][8];
+  uint4 x[V], gate[V], w_post[V], w[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int k = threadIdx.x * 8 + v * step;
     if (k < K) {
+      if (a.x) x[v] = *reinterpret_cast<const uint4 *>(a.x + m * a.x_stride + k);
       load8(static_cast<const R *>(a.r) + m * a.r_stride + k, r[v]);
+      if constexpr (kAhead) {
+        if (a.gate) gate[v] = *reinterpret_cast<const uint4 *>(a.gate + m * a.gate_stride + k);
+        if (a.w_post) w_post[v] = *reinterpret_cast<const uint4 *>(a.w_post + k);
+        w[v] = *reinterpret_cast<const uint4 *>(a.w + k);
+      }
     } else {
+      x[v] = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) r[v][i] = 0.0f;
     }
   }
   if (a.x) {
-    float u[V][8];
-    float ss = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int k = threadIdx.x * 8 + v * step;
-      if (k < K) {
-        load8(a.x + m * a.x_stride + k, u[v]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[v][i] = 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(u[v][i], u[v][i], ss);
-    }
     float inv = 1.0f;
-    if (a.w_post) inv = rsqrtf(block_sum(ss, part[0]) / static_cast<float>(K) + a.eps);
+    if (a.w_post) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float u[8];
+        widen8(x[v], u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(u[i], u[i], ss);
+      }
+      inv = rsqrtf(block_sum(ss, part[0]) / static_cast<float>(K) + a.eps);
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int k = threadIdx.x * 8 + v * step;
       if (k >= K) continue;
-      float f[8];
+      float u[8], f[8];
+      widen8(x[v], u);
       if (a.w_post) {
-        load8(a.w_post + k, f);
+        widen8(kAhead ? w_post[v] : *reinterpret_cast<const uint4 *>(a.w_post + k), f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[v][i] = u[v][i] * inv * f[i];
+        for (int i = 0; i < 8; ++i) u[i] = u[i] * inv * f[i];
       }
       if (a.gate) {
-        load8(a.gate + m * a.gate_stride + k, f);
+        widen8(kAhead ? gate[v] : *reinterpret_cast<const uint4 *>(a.gate + m * a.gate_stride + k), f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[v][i] *= f[i];
+        for (int i = 0; i < 8; ++i) u[i] *= f[i];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[v][i] = fmaf(a.scale, u[v][i], r[v][i]);
+      for (int i = 0; i < 8; ++i) r[v][i] = fmaf(a.scale, u[i], r[v][i]);
       store8_rounded(a.r_out ? static_cast<R *>(a.r_out) + m * a.r_out_stride + k : static_cast<R *>(nullptr), r[v]);
     }
   }
@@ -145,7 +162,7 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormArgs a) {
     const int k = threadIdx.x * 8 + v * step;
     if (k >= K) continue;  // 16 lanes together: K and the runs of 16 lanes are multiples of 128 channels
     float f[8];
-    load8(a.w + k, f);
+    widen8(kAhead ? w[v] : *reinterpret_cast<const uint4 *>(a.w + k), f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = r[v][i] * inv * f[i];
     const uint4 y = pack8(f);
@@ -181,7 +198,7 @@ static void launch_residual_norm_type(const NormArgs &a, cudaStream_t stream) {
   const int64_t runs = a.K / 8;
   const unsigned M = static_cast<unsigned>(a.M);
   auto threads = [&](int v) { return static_cast<unsigned>(((runs + v - 1) / v + 31) / 32 * 32); };
-  if (runs <= 1024) residual_norm_kernel<R, 1><<<M, threads(1), 0, stream>>>(a);
+  if (runs <= 512) residual_norm_kernel<R, 1><<<M, threads(1), 0, stream>>>(a);
   else if (runs <= 2048) residual_norm_kernel<R, 2><<<M, threads(2), 0, stream>>>(a);
   else residual_norm_kernel<R, 4><<<M, threads(4), 0, stream>>>(a);
 }
