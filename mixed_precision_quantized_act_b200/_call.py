@@ -1,53 +1,62 @@
 """What the bindings of the operators between the linears share: checks of
-tensors, and the device and stream a call goes to."""
+tensors, and the device and stream a call goes to.  A decode step makes a few
+such calls per layer, so they are kept short."""
 from __future__ import annotations
-
-import ctypes
 
 import torch
 
 from . import _lib
 
+_functions = {}
 
-def need(t, name: str, dtype, shape, device, contiguous: bool = True):
-    """Raises ValueError unless t is a tensor of this type, shape and device
-    (and contiguous)."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or (contiguous and not t.is_contiguous()):
-        raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}{dtype} {list(shape)} on {device}, "
+
+def need(t, name: str, dtype, shape, device: int):
+    """Raises ValueError unless t is a contiguous tensor of this type and shape
+    on this CUDA device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} on cuda:{device}, "
                          f"not {t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def rows(t, name: str, dtype, shape, device) -> int:
-    """need() for a tensor whose dimensions after the first are contiguous;
-    returns the first one's stride in elements."""
-    need(t, name, dtype, shape, device, False)
+def rows(t, name: str, dtype, shape, device: int) -> int:
+    """need() for a tensor whose first dimension may have any stride; returns
+    that stride in elements."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{name} must be a {dtype} {list(shape)} on cuda:{device}, "
+                         f"not {t.dtype} {list(t.shape)} on {t.device}")
+    strides = t.stride()
     inner = 1
-    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and s != inner and t.numel() > 0:
-            raise ValueError(f"every row of {name} must be contiguous (strides {t.stride()})")
-        inner *= n
-    return t.stride(0) if shape[0] > 1 else inner
+    for i in range(len(shape) - 1, 0, -1):
+        if strides[i] != inner and shape[i] != 1 and t.numel() > 0:
+            raise ValueError(f"every row of {name} must be contiguous (strides {strides})")
+        inner *= shape[i]
+    return strides[0] if shape[0] > 1 else inner
 
 
-def on_cuda(t, name: str):
+def on_cuda(t, name: str) -> int:
+    """The index of the CUDA device that t is on."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-def call(fn: str, device, stream, *args):
-    """Calls the library's `fn` on `device` and its stream (the device's
-    current stream when None), whatever the current device is."""
+def call(fn: str, device: int, stream, *args):
+    """Calls the library's `fn` on the CUDA device and its stream (the device's
+    current one when None), whatever the current device is."""
+    f = _functions.get(fn)
+    if f is None:
+        f = _functions[fn] = getattr(_lib.load(), fn)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"the tensors are on {device}, the stream on {stream.device}")
-    f = getattr(_lib.load(), fn)
-    if torch.cuda.current_device() == device.index:
-        status = f(*args, ctypes.c_void_p(stream.cuda_stream))
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device.index != device:
+        raise ValueError(f"the tensors are on cuda:{device}, the stream on {stream.device}")
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device:
+        status = f(*args, handle)
     else:
         with torch.cuda.device(device):
-            status = f(*args, ctypes.c_void_p(stream.cuda_stream))
+            status = f(*args, handle)
     if status != _lib.OK:
         _lib._check(status, fn)
 

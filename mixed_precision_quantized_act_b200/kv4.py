@@ -25,9 +25,10 @@ class KV4Cache:
     def __post_init__(self):
         if self.codes.dim() != 5 or self.codes.shape[1] != 2:
             raise ValueError("codes must be a uint8 [pages, 2, kv_heads, page_size, head_dim / 2]")
-        self.device = on_cuda(self.codes, "codes")
-        need(self.codes, "codes", torch.uint8, self.codes.shape, self.device)
-        need(self.meta, "meta", _I32, self.codes.shape[:4], self.device)
+        self.index = on_cuda(self.codes, "codes")
+        need(self.codes, "codes", torch.uint8, self.codes.shape, self.index)
+        need(self.meta, "meta", _I32, self.codes.shape[:4], self.index)
+        self.device = self.codes.device
         self.pages, _, self.kv_heads, self.page_size, half = self.codes.shape
         self.head_dim = 2 * half
         self._args = (self.codes.data_ptr(), self.meta.data_ptr(), self.pages, self.kv_heads, self.head_dim,
@@ -83,7 +84,7 @@ def kv4_append_into(k, v, slots, cache: KV4Cache, q=None, q_out=None, positions=
     [T] (negative: skipped); with rope fp32 [max_pos, rotary] and positions
     int32 [T], rotates the keys and q fp16 [T, q_heads, head_dim] (into q_out,
     which may be q) first.  Rows may be strided: slices of one qkv output serve."""
-    dev = cache.device
+    dev = cache.index
     T = slots.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
     need(slots, "slots", _I64, (T,), dev)
@@ -104,7 +105,7 @@ def kv4_append_into(k, v, slots, cache: KV4Cache, q=None, q_out=None, positions=
 def kv4_read_into(slots, cache: KV4Cache, k_out, v_out, stream=None):
     """The cached keys and values of slots int64 [T] into fp16
     [T, kv_heads, head_dim] tensors (mixllm_kv4_read)."""
-    dev = cache.device
+    dev = cache.index
     T = slots.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
     need(slots, "slots", _I64, (T,), dev)
@@ -137,7 +138,7 @@ def kv4_attention_into(q, cache: KV4Cache, block_table, seq_lens, cu_q, max_q: i
     cu_q[b]:cu_q[b+1] of q fp16 [T, q_heads, head_dim] (at most max_q of them)
     against the seq_lens[b] tokens in the pages of block_table's row b.  scale:
     1 / sqrt(head_dim) when None.  lse: fp32 [T, q_heads] or None."""
-    dev = cache.device
+    dev = cache.index
     T, q_heads = q.shape[0], q.shape[1]
     B = seq_lens.shape[0]
     shape = (T, q_heads, cache.head_dim)
