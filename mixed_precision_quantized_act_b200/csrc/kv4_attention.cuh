@@ -324,8 +324,6 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
   constexpr int kRows = C::kRows, kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int first_b[kWarps], join_blocks[2][2];
-  __shared__ uint64_t pace;
-  __shared__ volatile int abort_flag;
   __shared__ KvSeg part_at[kWarps][2], cut_at[2];
   // part_first: the segment (its first unit) of a part that a warp left, or -1:
   // [0] in the workspace (behind its first segment), [1] in shared memory (its last one)
@@ -333,11 +331,6 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.Hq / a.cache.H;
-  if (tid == 0) {
-    mbar_init(&pace, kWarps);
-    fence_mbar_init();
-    abort_flag = 0;
-  }
   if (tid < 2) cut_first[tid] = -1;
   if (tid < kWarps) {
     first_b[tid] = a.B;
@@ -452,17 +445,6 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
         if (g == 0) *reinterpret_cast<float2 *>(part + kRows * D + 2 * r) = make_float2(m[ni][j], l[ni][j]);
       }
   };
-  // Warps keep in step: none begins its step s + 1 before all have begun step s.
-  // The scheduler prefers the older of two ready warps; left alone, half of an
-  // SM's warps end at 0.8 of the time and the rest run on with too few to hide
-  // their latencies.  (A wait that gives up costs speed only.)
-  int step = 0;
-  const int steps = static_cast<int>(warp_start(kWarps) - warp_start(kWarps - 1));  // the last warp has the most
-  const auto keep_pace = [&] {
-    if (step > 0) warp_wait(&pace, (step - 1) & 1, &abort_flag);
-    if (lane == 0) mbar_arrive(&pace);
-    ++step;
-  };
   bool in_registers = false;  // the last segment's part, cut at one of the warp's ends
   for (KvWalk w = w0; w.left > 0; w.next(a, kRows)) {
     const int rows = w.r.n * group;
@@ -521,7 +503,6 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
 
     for (int i = 0; i < w.count; ++i) {
       const int base = (w.tile + i) * kKvTile;
-      keep_pace();
       cp_async_wait<C::kStages - 2>();
       __syncwarp();  // every lane's copies of this stage are here, and every lane is done with the stage before
       const uint32_t have = fetch.present >> 2 * stage & 3u;
@@ -722,7 +703,6 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
       }
     }
   }
-  while (step < steps) keep_pace();
   float *last_parts = reinterpret_cast<float *>(smem);
   __threadfence_block();
   __syncthreads();  // no warp needs its ring any more
