@@ -71,12 +71,11 @@ namespace mixllm {
 // so the result does not depend on timing.
 // ---------------------------------------------------------------------------
 constexpr int kKvTile = 32;  // tokens per unit
-constexpr int kKvJoinThreads = 256;
 constexpr float kKvNoMax = -3.0e38f;
 
 template <int D, int NT>
 struct KvCfg {
-  static constexpr int kWarps = NT == 1 ? 16 : 8;  // by registers: 128 and 255 a thread
+  static constexpr int kWarps = D * NT <= 128 ? 16 : 8;  // by registers: 128 and 255 a thread
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NT;
   static constexpr int kRowBytes = D / 2;
@@ -84,7 +83,8 @@ struct KvCfg {
   static constexpr int kStage = 2 * (kCodes + 32 * 4);
   static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kRing = kStages * kStage;  // of one warp
-  static constexpr int kPart = kRows * (D + 2);   // floats of one part: sums, then (m, l) per row
+  static constexpr int kPitch = D + 8;            // floats of a part's row: two rows further, 16 banks further
+  static constexpr int kPart = kRows * (kPitch + 2);  // floats of one part: sums, then (m, l) per row
   static constexpr int kSmem = kWarps * kRing;
   static_assert(kWarps * kPart * 4 <= kSmem, "the warps' last parts take the ring's place");
   static_assert(kSmem + 4096 <= 227 * 1024, "shared memory of a block");
@@ -113,31 +113,26 @@ __device__ __forceinline__ KvReq kv_req(const AttendArgs &a, int b, int rows_per
   return r;
 }
 
-// Walks a warp's units as segments: runs of units of one (request, row tile,
-// key head).
+// Walks a warp's units as segments: runs of units of one request and key head.
 struct KvWalk {
-  int b, rt, h, tile, count;  // the segment: its first unit's tile and its units in this warp
-  int64_t left;               // units of the warp from the segment's first on
-  int64_t seg_first;          // unit index of the whole segment's first tile
+  int b, h, tile, count;  // the segment: its first unit's tile and its units in this warp
+  int left;               // units of the warp from the segment's first on
+  int seg_first;          // unit index of the whole segment's first tile
   KvReq r;
 
-  __device__ __forceinline__ void settle(const AttendArgs &a, int rows_per_tile) {
-    while (left > 0 && r.tiles == 0 && ++b < a.B) r = kv_req(a, b, rows_per_tile);
-    if (b >= a.B) left = 0;
-    count = static_cast<int>(left < r.tiles - tile ? left : r.tiles - tile);
-  }
   __device__ __forceinline__ void next(const AttendArgs &a, int rows_per_tile) {
     left -= count;
     seg_first += r.tiles;
     tile = 0;
     if (++h == a.cache.H) {
       h = 0;
-      if (++rt == r.row_tiles) {
-        rt = 0;
-        if (++b < a.B && left > 0) r = kv_req(a, b, rows_per_tile);
+      while (left > 0 && ++b < a.B) {
+        r = kv_req(a, b, rows_per_tile);
+        if (r.tiles > 0) break;
       }
+      if (b >= a.B) left = 0;
     }
-    settle(a, rows_per_tile);
+    count = min(left, r.tiles);
   }
 };
 
@@ -149,15 +144,14 @@ struct KvFetch {
   uint32_t ring;     // shared address of this lane's first bytes in stage 0
   uint32_t present;  // bits 2s, 2s + 1: the halves of stage s are tokens of a page that exists
   int stage;
-  int b, rt, h, tile, batch, id;
-  int64_t left;
+  int b, h, tile, batch, id, left;
   KvReq r;
 
   __device__ __forceinline__ void start(const KvWalk &w, int lane, const uint8_t *to) {
     ring = smem_u32(to) + (lane >> 4) * (16 * C::kRowBytes) + (lane & 15) * 16;
     present = 0;
     stage = 0;
-    b = w.b, rt = w.rt, h = w.h, tile = w.tile, r = w.r;
+    b = w.b, h = w.h, tile = w.tile, r = w.r;
     left = w.left;
     batch = -1;
   }
@@ -206,14 +200,11 @@ struct KvFetch {
         batch = -1;
         if (++h == a.cache.H) {
           h = 0;
-          if (++rt == r.row_tiles) {
-            rt = 0;
-            while (left > 0 && ++b < a.B) {
-              r = kv_req(a, b, C::kRows);
-              if (r.tiles > 0) break;
-            }
-            if (b >= a.B) left = 0;
+          while (left > 0 && ++b < a.B) {
+            r = kv_req(a, b, C::kRows);
+            if (r.tiles > 0) break;
           }
+          if (b >= a.B) left = 0;
         }
       }
     }
@@ -256,21 +247,19 @@ constexpr float kHighToLow = 0x1p10f;
 
 // A segment's place, for who joins its parts.
 struct KvSeg {
-  int rt, h, tiles, q0, n;
+  int h, tiles, q0, n;
 };
 
-// Joining parts: a thread holds kCh channels of one row.  The 32 or 16
-// neighbouring lanes that share a row hold the weights of as many parts.
-template <int D, int NT>
+// Joining parts: a warp takes a row, a lane four (or two) of its channels, and
+// lane i holds the weight of part i.  A part's row holds channel D/8 g + 2k + e
+// at 16k + 2g + e: the order in which the lanes of an accumulator can write it
+// without conflicts of shared-memory banks.
+template <int D>
 struct KvRow {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kThreadsPerRow = kKvJoinThreads / kRows;  // 32 or 16
-  static constexpr int kCh = D / kThreadsPerRow;             // 2, 4 or 8
-  int r, d0;
+  static constexpr int kCh = D / 32;
   float top, sum, acc[kCh];
 
   __device__ __forceinline__ void clear() {
-    r = threadIdx.x / kThreadsPerRow, d0 = threadIdx.x % kThreadsPerRow * kCh;
     top = kKvNoMax;
     sum = 0.0f;
 #pragma unroll
@@ -278,39 +267,45 @@ struct KvRow {
   }
   static __device__ __forceinline__ float max_lanes(float v) {
 #pragma unroll
-    for (int x = kThreadsPerRow / 2; x > 0; x >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, x));
+    for (int x = 16; x > 0; x >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, x));
     return v;
   }
   static __device__ __forceinline__ float sum_lanes(float v) {
 #pragma unroll
-    for (int x = kThreadsPerRow / 2; x > 0; x >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, x);
+    for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, x);
     return v;
   }
+  // `from`: this lane's channels of the row in a part
   template <bool kGlobal>
-  __device__ __forceinline__ void add(const float *part, float f) {
-#pragma unroll
-    for (int k = 0; k < kCh; k += 2) {
-      const float2 *from = reinterpret_cast<const float2 *>(part + r * D + d0 + k);
-      const float2 v = kGlobal ? __ldcg(from) : *from;
-      acc[k] = fmaf(v.x, f, acc[k]), acc[k + 1] = fmaf(v.y, f, acc[k + 1]);
+  static __device__ __forceinline__ void load(const float *from, float (&v)[kCh]) {
+    if constexpr (kCh == 4) {
+      const float4 *f = reinterpret_cast<const float4 *>(from);
+      const float4 u = kGlobal ? __ldcg(f) : *f;
+      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+    } else {
+      const float2 *f = reinterpret_cast<const float2 *>(from);
+      const float2 u = kGlobal ? __ldcg(f) : *f;
+      v[0] = u.x, v[1] = u.y;
     }
   }
-  __device__ __forceinline__ void leave(float *part) {
+  __device__ __forceinline__ void add(const float (&v)[kCh], float f) {
 #pragma unroll
-    for (int k = 0; k < kCh; k += 2) *reinterpret_cast<float2 *>(part + r * D + d0 + k) = make_float2(acc[k], acc[k + 1]);
-    if (d0 == 0) *reinterpret_cast<float2 *>(part + kRows * D + 2 * r) = make_float2(top, sum);
+    for (int k = 0; k < kCh; ++k) acc[k] = fmaf(v[k], f, acc[k]);
   }
-  __device__ __forceinline__ void write(const AttendArgs &a, const KvSeg &g) {
-    const int group = a.Hq / a.cache.H, row = g.rt * kRows + r;
-    if (row >= g.n * group) return;
-    const int tok = row / group, head = g.h * group + row - tok * group;
-    const int64_t token = static_cast<int64_t>(g.q0) + tok;
+  __device__ __forceinline__ void write(const AttendArgs &a, const KvSeg &s, int row, int lane) {
+    const int group = a.Hq / a.cache.H;
+    if (row >= s.n * group) return;
+    const int tok = row / group, head = s.h * group + row - tok * group;
+    const int64_t token = static_cast<int64_t>(s.q0) + tok;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row that saw no key is zero
-    __half *dst = a.out + token * a.out_stride + static_cast<int64_t>(head) * D + d0;
+    __half *dst = a.out + token * a.out_stride + static_cast<int64_t>(head) * D;
 #pragma unroll
-    for (int k = 0; k < kCh; k += 2)
-      *reinterpret_cast<__half2 *>(dst + k) = __floats2half2_rn(acc[k] * inv, acc[k + 1] * inv);
-    if (a.lse && d0 == 0)
+    for (int j = 0; j < kCh; j += 2) {
+      const int at = lane * kCh + j;  // 16k + 2g
+      *reinterpret_cast<__half2 *>(dst + (at % 16 / 2) * (D / 8) + at / 16 * 2) =
+          __floats2half2_rn(acc[j] * inv, acc[j + 1] * inv);
+    }
+    if (a.lse && lane == 0)
       a.lse[token * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   }
 };
@@ -323,90 +318,100 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
   using C = KvCfg<D, NT>;
   constexpr int kRows = C::kRows, kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int first_b[kWarps], join_blocks[2][2];
-  __shared__ KvSeg part_at[kWarps][2], cut_at[2];
   // part_first: the segment (its first unit) of a part that a warp left, or -1:
   // [0] in the workspace (behind its first segment), [1] in shared memory (its last one)
-  __shared__ long long first_rem[kWarps], warp_units[kWarps], part_first[kWarps][2], cut_first[2];
+  __shared__ int part_first[kWarps][2], cut_first[2], join_blocks[2][2], warp_units[kWarps];
+  __shared__ KvSeg part_at[kWarps][2], cut_at[2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.Hq / a.cache.H;
+  pdl_launch_dependents();
   if (tid < 2) cut_first[tid] = -1;
-  if (tid < kWarps) {
-    first_b[tid] = a.B;
-    part_first[tid][0] = part_first[tid][1] = -1;
-  }
+  if (lane < 2) part_first[warp][lane] = -1;
+  pdl_wait();
 
-  // ---- this block's units: a prefix sum over the requests, in chunks of one per thread
+  // ---- this warp's units, by a prefix sum of the requests' units
   int P = gridDim.x;
   const int c = blockIdx.x;
-  int64_t U = 0;
-  const int chunks = (a.B + kThreads - 1) / kThreads;
-  long long u = 0, incl = 0;
-  auto scan_chunk = [&](int chunk, int64_t base) {  // u, incl of request chunk * threads + tid; returns base + the chunk's sum
-    const int b = chunk * kThreads + tid;
-    u = 0;
-    if (b < a.B) {
-      const KvReq r = kv_req(a, b, kRows);
-      u = static_cast<long long>(r.tiles) * r.row_tiles * a.cache.H;
-    }
-    incl = u;
+  const auto units_of = [&](int b) {
+    const KvReq r = kv_req(a, b, kRows);
+    return r.tiles * a.cache.H;
+  };
+  const auto scan = [&](int v) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += v;
+      const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
     }
-    if (lane == 31) warp_units[warp] = incl;
-    __syncthreads();
-    incl += base;
-#pragma unroll
-    for (int x = 0; x < kWarps; ++x) {
-      if (x < warp) incl += warp_units[x];
-      base += warp_units[x];
-    }
-    __syncthreads();
-    return base;
+    return v;
   };
-  for (int k = 0; k < chunks; ++k) U = scan_chunk(k, U);
-  if (U < static_cast<int64_t>(P) * kWarps) P = static_cast<int>(U + kWarps - 1) / kWarps;
-  if (c >= P) return;  // every other block has a unit
-  const int64_t share = U < 1ll << 32 ? static_cast<uint32_t>(U) / static_cast<uint32_t>(P) : U / P;
-  const int rest = static_cast<int>(U - share * P);
-  const auto block_start = [&](int b) { return share * b + rest * b / P; };  // rest, b < 2^10
-  const int64_t start = block_start(c);
-  const int64_t mine = block_start(c + 1) - start;
-  const auto warp_start = [&](int x) { return start + mine * x / kWarps; };
-  int64_t base = 0;
-  for (int k = 0; k < chunks && base <= warp_start(kWarps - 1); ++k) {
-    if (chunks > 1) base = scan_chunk(k, base);
-    else base = U;
+  constexpr int kFew = 4;  // requests per lane that a warp scans for itself, with no barrier
+  const bool few = a.B <= 32 * kFew;
+  int incl[kFew], U = 0;  // of requests 32 i + lane
+  if (few) {
+    int u[kFew];
 #pragma unroll
-    for (int x = 0; x < kWarps; ++x) {
-      const int64_t at = warp_start(x);
-      if (at >= incl - u && at < incl) {
-        first_b[x] = k * kThreads + tid;
-        first_rem[x] = at - (incl - u);
+    for (int i = 0; i < kFew; ++i) u[i] = 32 * i + lane < a.B ? units_of(32 * i + lane) : 0;
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+      incl[i] = scan(u[i]) + U;
+      U = __shfl_sync(0xFFFFFFFFu, incl[i], 31);
+    }
+  } else {
+    for (int b = tid; b < a.B; b += kThreads) U += units_of(b);
+    U = __reduce_add_sync(0xFFFFFFFFu, U);
+    if (lane == 0) warp_units[warp] = U;
+    __syncthreads();
+    U = 0;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) U += warp_units[x];
+  }
+  // at least two units a warp: fewer blocks share a short context, whose joining would cost more than a unit
+  if (U < P * kWarps * 2) P = (U + kWarps * 2 - 1) / (kWarps * 2);
+  if (c >= P) return;  // every other block has a unit
+  const int share = U / P, rest = U - share * P;
+  const auto block_start = [&](int b) { return share * b + rest * b / P; };  // rest, b < 2^8
+  const int start = block_start(c), mine = block_start(c + 1) - start;
+  const int my_start = start + mine * warp / kWarps, my_end = start + mine * (warp + 1) / kWarps;
+  KvWalk w0;
+  w0.left = my_end - my_start;
+  w0.b = a.B;
+  int before = 0;  // units before request w0.b
+  if (few) {
+#pragma unroll
+    for (int i = kFew - 1; i >= 0; --i) {
+      const uint32_t beyond = __ballot_sync(0xFFFFFFFFu, incl[i] > my_start);
+      if (beyond) w0.b = 32 * i + __ffs(beyond) - 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+      const int v = __shfl_sync(0xFFFFFFFFu, incl[i], (w0.b - 1) & 31);
+      if (w0.b > 0 && (w0.b - 1) / 32 == i) before = v;
+    }
+  } else {
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int end = scan(b0 + lane < a.B ? units_of(b0 + lane) : 0) + before;
+      const uint32_t beyond = __ballot_sync(0xFFFFFFFFu, end > my_start);
+      if (beyond) {
+        const int i = __ffs(beyond) - 1;
+        const int v = __shfl_sync(0xFFFFFFFFu, end, i > 0 ? i - 1 : 0);
+        if (i > 0) before = v;
+        w0.b = b0 + i;
+        break;
       }
+      before = __shfl_sync(0xFFFFFFFFu, end, 31);
     }
   }
-  __syncthreads();
-  const int64_t my_start = warp_start(warp), my_end = warp_start(warp + 1);
-  KvWalk w0;
-  w0.b = first_b[warp];
-  w0.left = w0.b < a.B ? my_end - my_start : 0;
-  w0.rt = w0.h = w0.tile = 0;
   w0.r = KvReq{0, 0, 0, 0, 0};
+  w0.h = w0.tile = 0;
+  if (w0.b >= a.B) w0.left = 0;
   if (w0.left > 0) {
     w0.r = kv_req(a, w0.b, kRows);
-    const int64_t seg = first_rem[warp] < 1ll << 32
-                            ? static_cast<uint32_t>(first_rem[warp]) / static_cast<uint32_t>(w0.r.tiles)
-                            : first_rem[warp] / w0.r.tiles;
-    w0.tile = static_cast<int>(first_rem[warp] - seg * w0.r.tiles);
-    w0.rt = static_cast<int>(seg / a.cache.H);
-    w0.h = static_cast<int>(seg - static_cast<int64_t>(w0.rt) * a.cache.H);
+    w0.h = (my_start - before) / w0.r.tiles;
+    w0.tile = my_start - before - w0.h * w0.r.tiles;
   }
   w0.seg_first = my_start - w0.tile;
-  w0.settle(a, kRows);
+  w0.count = min(w0.left, w0.r.tiles - w0.tile);
 
   KvFetch<C> fetch;
   fetch.start(w0, lane, smem + warp * C::kRing);
@@ -436,19 +441,18 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
       for (int j = 0; j < 2; ++j) {
         const int r = ni * 8 + 2 * t + j;
         const float back = S * 0x1p10f, z = oz[ni][j];
-        float *dst = part + r * D + g * (D / 8);
+        float *dst = part + r * C::kPitch + g * 2;
 #pragma unroll
-        for (int k = 0; k < kMTiles; k += 2)
-          *reinterpret_cast<float4 *>(dst + 2 * k) = make_float4(
-              (o[ni][k][j] - z) * back, fmaf(o[ni][k][2 + j], kHighToLow, -z) * back, (o[ni][k + 1][j] - z) * back,
-              fmaf(o[ni][k + 1][2 + j], kHighToLow, -z) * back);
-        if (g == 0) *reinterpret_cast<float2 *>(part + kRows * D + 2 * r) = make_float2(m[ni][j], l[ni][j]);
+        for (int k = 0; k < kMTiles; ++k)
+          *reinterpret_cast<float2 *>(dst + 16 * k) =
+              make_float2((o[ni][k][j] - z) * back, fmaf(o[ni][k][2 + j], kHighToLow, -z) * back);
+        if (g == 0) *reinterpret_cast<float2 *>(part + kRows * C::kPitch + 2 * r) = make_float2(m[ni][j], l[ni][j]);
       }
   };
   bool in_registers = false;  // the last segment's part, cut at one of the warp's ends
   for (KvWalk w = w0; w.left > 0; w.next(a, kRows)) {
     const int rows = w.r.n * group;
-    const int row0 = w.rt * kRows;
+    constexpr int row0 = 0;
     // ---- the query rows' B fragments, channels permuted as the keys' nibbles, and their sums
     uint32_t qf[NT][kWords * 4];
     float qs[NT][2];
@@ -699,7 +703,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
       if (!in_registers) leave(warp_parts + (c * kWarps + warp) * C::kPart);
       if (lane == 0) {
         part_first[warp][side] = w.seg_first;
-        part_at[warp][side] = KvSeg{w.rt, w.h, w.r.tiles, w.r.q0, w.r.n};
+        part_at[warp][side] = KvSeg{w.h, w.r.tiles, w.r.q0, w.r.n};
       }
     }
   }
@@ -709,96 +713,128 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
   if (in_registers) leave(last_parts + warp * C::kPart);
   __syncthreads();
 
-  // ---- the block's parts, segment by segment; lane i looks after part i.
-  // A segment's parts are neighbours among those that there are.
-  constexpr int kLanes = 2 * kWarps;  // and as many lanes share a row
-  static_assert(kLanes == KvRow<D, NT>::kThreadsPerRow, "one part per lane of a row");
-  if (warp >= kKvJoinThreads / 32) return;
-  const int me = lane & (kLanes - 1);
-  constexpr uint32_t kAll = kLanes == 32 ? 0xFFFFFFFFu : 0xFFFFu;
-  const int64_t part_seg = part_first[me >> 1][me & 1];
-  const uint32_t there = __ballot_sync(0xFFFFFFFFu, part_seg >= 0) & kAll;
-  const uint32_t before_me = there & ((1u << me) - 1u);
-  const int64_t seg_before = __shfl_sync(0xFFFFFFFFu, part_seg, before_me ? 31 - __clz(before_me) : 0);
-  uint32_t firsts = __ballot_sync(0xFFFFFFFFu, part_seg >= 0 && (!before_me || seg_before != part_seg)) & kAll;
-  const float *my_part = me & 1 ? last_parts + (me >> 1) * C::kPart : warp_parts + (c * kWarps + (me >> 1)) * C::kPart;
-  while (firsts) {
+  // ---- the block's parts, segment by segment; lane i looks after part i.  A
+  // segment's parts are neighbours among those that there are.  A warp takes
+  // one row of one segment at a time.
+  const int part_seg = lane < 2 * kWarps ? part_first[lane >> 1 & (kWarps - 1)][lane & 1] : -1;
+  const uint32_t there = __ballot_sync(0xFFFFFFFFu, part_seg >= 0);
+  const uint32_t before_me = there & ((1u << lane) - 1u);
+  const int seg_before = __shfl_sync(0xFFFFFFFFu, part_seg, before_me ? 31 - __clz(before_me) : 0);
+  uint32_t firsts = __ballot_sync(0xFFFFFFFFu, part_seg >= 0 && (!before_me || seg_before != part_seg));
+  const auto place_of = [&](int i) -> const float * {
+    return i & 1 ? last_parts + (i >> 1) * C::kPart : warp_parts + (c * kWarps + (i >> 1)) * C::kPart;
+  };
+  const float *my_part = place_of(lane & (2 * kWarps - 1));
+  KvRow<D> row;
+  for (int item = 0; firsts; firsts &= firsts - 1) {
     const int first = __ffs(firsts) - 1;
-    firsts &= firsts - 1;
+    const uint32_t rest_of = firsts & (firsts - 1);
     uint32_t these = there & ~((1u << first) - 1u);
-    if (firsts) these &= (firsts & -firsts) - 1u;
-    const int64_t seg_first = part_first[first >> 1][first & 1];
+    if (rest_of) these &= (rest_of & -rest_of) - 1u;
+    const int seg_first = part_first[first >> 1][first & 1];
     const KvSeg seg = part_at[first >> 1][first & 1];
-    KvRow<D, NT> row;
-    row.clear();
-    const bool in = these >> me & 1u;
-    const float2 ml = in ? *reinterpret_cast<const float2 *>(my_part + kRows * D + 2 * row.r) : make_float2(kKvNoMax, 0.0f);
-    row.top = row.max_lanes(ml.x);
-    const float f = in ? ex2(ml.x - row.top) : 0.0f;
-    row.sum = row.sum_lanes(ml.y * f);
-#pragma unroll 1
-    for (; these; these &= these - 1) {
-      const int i = __ffs(these) - 1;
-      row.template add<false>(i & 1 ? last_parts + (i >> 1) * C::kPart : warp_parts + (c * kWarps + (i >> 1)) * C::kPart,
-                              __shfl_sync(0xFFFFFFFFu, f, i, kLanes));
+    const bool whole = seg_first >= start && seg_first + seg.tiles <= start + mine;
+    const int side = start <= seg_first ? 1 : 0;  // the block's end cuts it, or its beginning
+    if (!whole && tid == 0) {
+      cut_first[side] = seg_first;
+      cut_at[side] = seg;
     }
-    if (seg_first >= start && seg_first + seg.tiles <= start + mine) {
-      row.write(a, seg);
-    } else {
-      const int side = start <= seg_first ? 1 : 0;  // the block's end cuts it, or its beginning
-      row.leave(block_parts + (c * 2 + side) * C::kPart);
-      if (tid == 0) {
-        cut_first[side] = seg_first;
-        cut_at[side] = seg;
+    for (int r = 0; r < kRows; ++r, ++item) {
+      if (item % kWarps != warp) continue;
+      row.clear();
+      const bool in = these >> lane & 1u;
+      const float2 ml = in ? *reinterpret_cast<const float2 *>(my_part + kRows * C::kPitch + 2 * r) : make_float2(kKvNoMax, 0.0f);
+      row.top = row.max_lanes(ml.x);
+      const float f = in ? ex2(ml.x - row.top) : 0.0f;
+      row.sum = row.sum_lanes(ml.y * f);
+      const int at = r * C::kPitch + lane * KvRow<D>::kCh;
+#pragma unroll 1
+      for (uint32_t some = these; some;) {  // four parts' loads together
+        int i[4];
+        float v[4][KvRow<D>::kCh];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          i[x] = some ? __ffs(some) - 1 : -1;
+          some &= some - 1;
+          if (i[x] >= 0) row.template load<false>(place_of(i[x]) + at, v[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (i[x] >= 0) row.add(v[x], __shfl_sync(0xFFFFFFFFu, f, i[x]));
+      }
+      if (whole) {
+        row.write(a, seg, r, lane);
+      } else {
+        float *part = block_parts + (c * 2 + side) * C::kPart;
+#pragma unroll
+        for (int k = 0; k < KvRow<D>::kCh; k += 2)
+          *reinterpret_cast<float2 *>(part + at + k) = make_float2(row.acc[k], row.acc[k + 1]);
+        if (lane == 0) *reinterpret_cast<float2 *>(part + kRows * C::kPitch + 2 * r) = make_float2(row.top, row.sum);
       }
     }
   }
 
   // ---- segments cut between blocks: the last block to get here joins the parts
-  named_bar_sync(1, kKvJoinThreads);
+  __syncthreads();
   if (tid < 2) {
     join_blocks[tid][1] = -1;
     if (cut_first[tid] >= 0) {
       // blocks that hold units of the segment: the one with unit x is ((x + 1) P - 1) / U
-      const int c0 = static_cast<int>(((cut_first[tid] + 1) * P - 1) / U);
-      const int c1 = static_cast<int>(((cut_first[tid] + cut_at[tid].tiles) * P - 1) / U);
-      // a block's end cuts one segment at most, so the first block of a segment names its counter
-      __threadfence();
-      const uint32_t before = atom_add_acq_rel_gpu_u32(counters + c0, 1u);
-      if (before == static_cast<uint32_t>(c1 - c0)) {
+      const int c0 = static_cast<int>((static_cast<int64_t>(cut_first[tid] + 1) * P - 1) / U);
+      const int c1 = static_cast<int>((static_cast<int64_t>(cut_first[tid] + cut_at[tid].tiles) * P - 1) / U);
+      // A block's end cuts one segment at most, so the first block of a segment names its counter.  The barrier
+      // before and after makes the release and the acquire the whole block's.
+      const uint32_t arrived = atom_add_acq_rel_gpu_u32(counters + c0, 1u);
+      if (arrived == static_cast<uint32_t>(c1 - c0)) {
         counters[c0] = 0;
         join_blocks[tid][0] = c0;
         join_blocks[tid][1] = c1;
       }
     }
   }
-  named_bar_sync(1, kKvJoinThreads);
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
+  __syncthreads();
+  for (int item = warp; item < 2 * kRows; item += kWarps) {
+    const int side = item / kRows, r = item % kRows;
     const int c0 = join_blocks[side][0], c1 = join_blocks[side][1];
     if (c1 < 0) continue;
-    __threadfence();
-    KvRow<D, NT> row;
-    row.clear();
     // the segment is the first block's last one and every other's first one
     const auto part_of = [&](int b) { return block_parts + (b * 2 + (b == c0 ? 1 : 0)) * C::kPart; };
-    float top = kKvNoMax;
-    for (int b = c0 + me; b <= c1; b += kLanes) top = fmaxf(top, __ldcg(part_of(b) + kRows * D + 2 * row.r));
+    const int at = r * C::kPitch + lane * KvRow<D>::kCh, n = c1 - c0 + 1;
+    const auto ml_of = [&](int i) {
+      return i < n ? __ldcg(reinterpret_cast<const float2 *>(part_of(c0 + i) + kRows * C::kPitch + 2 * r))
+                   : make_float2(kKvNoMax, 0.0f);
+    };
+    constexpr int kTogether = 4;  // the first parts' loads are under way with the weights'
+    float v[kTogether][KvRow<D>::kCh];
+    float2 ml = ml_of(lane);
+#pragma unroll
+    for (int x = 0; x < kTogether; ++x)
+      if (x < n) row.template load<true>(part_of(c0 + x) + at, v[x]);
+    row.clear();
+    float top = ml.x;
+    for (int i = 32; i < n; i += 32) top = fmaxf(top, ml_of(i + lane).x);
     row.top = row.max_lanes(top);
-    float sum = 0.0f;
-    for (int b0 = c0; b0 <= c1; b0 += kLanes) {
-      float f = 0.0f;
-      if (b0 + me <= c1) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_of(b0 + me) + kRows * D + 2 * row.r));
+    float f = ex2(ml.x - row.top), sum = ml.y * f;
+#pragma unroll
+    for (int x = 0; x < kTogether; ++x) {
+      const float fx = __shfl_sync(0xFFFFFFFFu, f, x);
+      if (x < n) row.add(v[x], fx);
+    }
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      if (i0 > 0) {
+        ml = ml_of(i0 + lane);
         f = ex2(ml.x - row.top);
         sum = fmaf(ml.y, f, sum);
       }
-      const int n = min(kLanes, c1 - b0 + 1);
 #pragma unroll 8
-      for (int i = 0; i < n; ++i) row.template add<true>(part_of(b0 + i), __shfl_sync(0xFFFFFFFFu, f, i, kLanes));
+      for (int i = i0 > 0 ? i0 : kTogether; i < min(n, i0 + 32); ++i) {
+        float u[KvRow<D>::kCh];
+        row.template load<true>(part_of(c0 + i) + at, u);
+        row.add(u, __shfl_sync(0xFFFFFFFFu, f, i & 31));
+      }
     }
     row.sum = row.sum_lanes(sum);
-    row.write(a, cut_at[side]);
+    row.write(a, cut_at[side], r, lane);
   }
 }
 
@@ -816,7 +852,7 @@ static_assert(kKvMaxGrid * sizeof(uint32_t) <= kKvCounterBytes, "one counter per
 
 static size_t kv4_decode_workspace_bytes(int max_q, int group, int D) {
   const int rows = 8 * kv4_decode_nt(max_q, group);
-  return kKvCounterBytes + static_cast<size_t>(kKvMaxGrid) * (2 + 16) * rows * (D + 2) * sizeof(float);
+  return kKvCounterBytes + static_cast<size_t>(kKvMaxGrid) * (2 + 16) * rows * (D + 8 + 2) * sizeof(float);
 }
 
 template <int D, int NT>
@@ -837,15 +873,27 @@ static cudaError_t launch_kv4_decode_type(const AttendArgs &a, void *ws, cudaStr
   }
   // one wave of blocks, fewer when even the longest contexts have fewer units
   const int64_t tiles = ((static_cast<int64_t>(a.W) << a.cache.page_log2) + kKvTile - 1) / kKvTile;
-  const int64_t row_tiles = (static_cast<int64_t>(a.max_q) * (a.Hq / a.cache.H) + C::kRows - 1) / C::kRows;
-  const int64_t units = a.B * row_tiles * a.cache.H * (tiles > 0 ? tiles : 1);
+  const int64_t units = static_cast<int64_t>(a.B) * a.cache.H * (tiles > 0 ? tiles : 1);
+  if (units > 0x7FFFFFFF) {
+    *msg = "requests x key heads x 32-token blocks of a table row pass 2^31";
+    return cudaErrorNotSupported;
+  }
   int64_t grid = device_sm_count();
   if (grid > kKvMaxGrid) grid = kKvMaxGrid;
   if (grid > (units + C::kWarps - 1) / C::kWarps) grid = (units + C::kWarps - 1) / C::kWarps;
   float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kKvCounterBytes);
-  kern<<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, stream>>>(a, static_cast<uint32_t *>(ws), parts,
-                                                                      parts + kKvMaxGrid * 2 * C::kPart);
-  cudaError_t e = cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // starts while the kernel before it ends
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, static_cast<uint32_t *>(ws), parts, parts + kKvMaxGrid * 2 * C::kPart);
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) *msg = "launch of the decode attention failed";
   return e;
 }

@@ -787,6 +787,7 @@ mixllm_status mixllm_kv4_attention(const void *q_f16, int64_t q_stride, int64_t 
                        lse};
   const char *msg = "";
   cudaError_t e = mixllm::launch_kv4_attention(a, workspace, static_cast<cudaStream_t>(stream), &msg);
+  if (e == cudaErrorNotSupported) return fail(MIXLLM_ERR_UNSUPPORTED, "%s", msg);
   if (e != cudaSuccess) return fail(MIXLLM_ERR_CUDA, "%s: %s", msg, cudaGetErrorString(e));
   return ok();
 }

@@ -400,16 +400,20 @@ def test_attention_reports_pages_and_lengths_out_of_range(dev):
         want, _, tol = ref.attention(q, cache.codes.cpu(), cache.meta.cpu(), bad, kv, cu.tolist(), D ** -0.5, True)
         assert ((out - want).abs() <= tol).all()
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
-    good = mx.kv4_attention(q.to(dev), cache, table.to(dev), lens, cu, 2).cpu().double()
-    mx.sync_status()
+    # A request with such lengths gets nothing; the others get theirs.  (Compared with the reference and not
+    # bit by bit with a call without it: where the units of a batch fall on blocks, and so the order of the
+    # sums, depends on all of its requests.)
+    want, _, tol = ref.attention(q, cache.codes.cpu(), cache.meta.cpu(), table, kv, cu.tolist(), D ** -0.5, True)
+
+    def first_only(out):
+        return ((out[0] - want[0]).abs() <= tol[0]).all() and (out[1:] == 77).all()
+
     for l, c in ((i32([300, table.shape[1] * page + 1]), cu), (i32([300, -1]), cu), (lens, i32([0, 1, 4])),
                  (lens, i32([0, 1, 0])), (lens, i32([0, 1, 2 ** 31 - 1]))):
-        out = run(table, l, c)
-        assert torch.equal(out[0], good[0]) and (out[1:] == 77).all()
+        assert first_only(run(table, l, c))
     out = run(table, lens, i32([-1, 1, 3]))
-    assert (out[0] == 77).all() and torch.equal(out[1:], good[1:])
-    out = run(table, lens, cu, max_q=1)  # the second request brings two
-    assert torch.equal(out[0], good[0]) and (out[1:] == 77).all()
+    assert (out[0] == 77).all() and ((out[1:] - want[1:]).abs() <= tol[1:]).all()
+    assert first_only(run(table, lens, cu, max_q=1))  # the second request brings two
 
 
 def test_attention_in_a_graph_with_lengths_that_grow(dev):
