@@ -1,11 +1,13 @@
-"""The linears of one decoder layer as a single CUDA graph.
+"""The linears of one decoder layer as a single CUDA graph, and the layer's
+attention half around two of them.
 
 A Llama decoder layer runs four W4.4A8 linears -- fused qkv, o_proj, fused
 gate_up and down -- each as activation quantization followed by the fused
 GEMM (MLSys 2026 talk notes on MixLLM, notes.yuuk.io, §探索の特性: the
 per-layer view of the method's kernels).  The attention core, the norms and
-the SwiGLU between them are not part of the method and are not run here: each
-linear reads its own input buffer.
+the SwiGLU between them are not part of the method and are not run by
+`LinearChain`: each linear reads its own input buffer.  `AttentionBlock` runs
+what a served model needs between and around the first two linears.
 
 `LinearChain` holds the packed weights and every intermediate buffer of such
 a chain, runs it eagerly, and captures it once into a CUDA graph so that a
@@ -20,7 +22,7 @@ from typing import List, Optional
 
 import torch
 
-from . import _lib
+from . import _lib, kv4, norm
 
 
 @dataclass
@@ -108,3 +110,61 @@ class LinearChain:
 
     def release(self):
         self.graph = None
+
+
+class AttentionBlock:
+    """The attention half of one decoder layer over a 4-bit paged cache:
+
+        r <- r + x;  y = norm(r);  q, k, v = qkv(y);  q, k <- rotated;
+        cache <- k, v in 4 bits;  out = o_proj(attention(q, cache))
+
+    for up to `tokens` tokens of up to `requests` requests at a time.  x is the
+    output of the block before (the residual update and its norm are one kernel
+    with the quantization for the qkv linear); `out` is this one's, for the block
+    after to add.  Buffers are allocated once; `run` allocates nothing and can be
+    captured into a graph, lengths and slots being device tensors
+    (kv4_assign_into).
+    """
+
+    def __init__(self, w_norm: torch.Tensor, qkv: _lib.PackedLinear, o_proj: _lib.PackedLinear, q_heads: int,
+                 cache: kv4.KV4Cache, rope: Optional[torch.Tensor], tokens: int, requests: int, max_q: int,
+                 table_width: int, eps: float = 1e-5):
+        H, D = cache.kv_heads, cache.head_dim
+        _lib._require(qkv.N == (q_heads + 2 * H) * D, "qkv must have (q_heads + 2 kv_heads) x head_dim channels")
+        _lib._require(o_proj.K == q_heads * D and o_proj.N == qkv.K, "o_proj must lead from the heads to qkv's inputs")
+        _lib._require(tokens > 0, "need room for at least one token")
+        dev = cache.device
+        self.w_norm, self.qkv, self.o_proj, self.cache, self.rope, self.eps = w_norm, qkv, o_proj, cache, rope, eps
+        self.q_heads, self.tokens, self.max_q = q_heads, tokens, max_q
+        self.A_q = torch.empty((tokens, qkv.K), dtype=torch.int8, device=dev)
+        self.s_a = torch.empty((tokens, qkv.K // _lib.GROUP), dtype=torch.float32, device=dev)
+        self.heads = torch.empty((tokens, q_heads + 2 * H, D), dtype=torch.float16, device=dev)
+        self.q = torch.zeros((tokens, q_heads, D), dtype=torch.float16, device=dev)
+        self.att = torch.zeros((tokens, q_heads, D), dtype=torch.float16, device=dev)
+        self.out = torch.empty((tokens, o_proj.N), dtype=torch.float16, device=dev)
+        self.few = tokens <= _lib.SMALL_M_MAX
+        self.ws_qkv = _lib.small_m_workspace(tokens, qkv, dev) if self.few else None
+        self.ws_o = _lib.linear_workspace(tokens, o_proj, dev)
+        self.ws_att = kv4.kv4_attention_workspace(requests, max_q, q_heads, cache, table_width)
+
+    def run(self, r: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, cu_q: torch.Tensor,
+            slots: torch.Tensor, positions: torch.Tensor, x: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """One pass: r fp16 or fp32 [tokens, K] is updated in place when x is
+        given; returns the output buffer fp16 [tokens, K].  seq_lens counts the
+        new tokens (behind those cached); rows behind cu_q's last entry are padding
+        and their outputs of no meaning."""
+        H = self.cache.kv_heads
+        norm.residual_norm_quantize_into(r, self.w_norm, self.A_q, self.s_a, x=x, r_out=None if x is None else r,
+                                         eps=self.eps, stream=stream)
+        Y = self.heads.view(self.tokens, -1)
+        if self.few:
+            _lib.gemm_w4w8a8_small_m_into(self.A_q, self.s_a, self.qkv, Y, self.ws_qkv, stream)
+        else:
+            _lib.gemm_w4w8a8_into(self.A_q, self.s_a, self.qkv, Y, stream)
+        q, k, v = self.heads.split((self.q_heads, H, H), 1)
+        kv4.kv4_append_into(k, v, slots, self.cache, q=q, q_out=self.q, positions=positions, rope=self.rope,
+                            stream=stream)
+        kv4.kv4_attention_into(self.q, self.cache, block_table, seq_lens, cu_q, self.max_q, self.att, self.ws_att,
+                               stream=stream)
+        _lib.linear_into(self.att.view(self.tokens, -1), self.o_proj, self.out, self.ws_o, stream)
+        return self.out
