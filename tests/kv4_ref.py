@@ -58,6 +58,9 @@ def attention(q, codes, meta, table, kv_lens, cu_q, scale, causal, bad_pages=())
         (2^-11 A), or, where the scaled weight p s / max s is below fp16's
         smallest normal 2^-14, an absolute 2^-25 max s per term, times |code - z|
         <= 15;
+      * the denominator sums p as rounded where the value's scale is at least an
+        eighth of the largest: 2^-11 |o| for its terms of normal weights, and
+        2^-25 * 8 |o| / sum p for each of a smaller one;
       * the result is rounded once to fp16: 2^-11 |o| (2^-25 below 2^-14);
       * the score's products are exact; their fp32 sum over D channels, the
         scale factors, the subtraction of the maximum and the exponential leave a
@@ -111,7 +114,8 @@ def attention(q, codes, meta, table, kv_lens, cu_q, scale, causal, bad_pages=())
                 big = sv.max() if sv.numel() else torch.zeros(())
                 small = (p * sv < 2.0 ** -14 * big).sum()
                 e = (D + 16) * 2.0 ** -24 * float(((k.abs() @ x.abs()) * abs(scale)).max()) + 2.0 ** -20
-                tol[first + i, h] = (2.0 ** -11 * (A + o.abs()) + 2.0 ** -25 + small * 2.0 ** -25 * 15 * big / p.sum()
+                tol[first + i, h] = (2.0 ** -11 * (A + 2 * o.abs()) + 2.0 ** -25
+                                     + small * 2.0 ** -25 * (15 * big + 8 * o.abs()) / p.sum()
                                      + e * (A + o.abs()) + (see / 16 + 64) * 2.0 ** -24 * A
                                      + 2 * (2.0 ** -17 + (see / 16 + 1) * 15 * 2.0 ** -23) * (w @ sv))
     return out, lse, tol

@@ -116,9 +116,9 @@ def test_attention_workspace(L):
     # up to 16 rows (queries x heads of a group) a request: counters and the parts of 148 blocks (two each, and one
     # per warp), whatever the batch
     for B in (1, 2, 16384):
-        assert ws(B) == (OK, 4096 + 148 * 18 * 8 * (128 + 10) * 4)
-    assert ws(max_q=4) == (OK, 4096 + 148 * 18 * 16 * (128 + 10) * 4)
-    assert ws(max_q=2, D=64) == (OK, 4096 + 148 * 18 * 8 * (64 + 10) * 4)
+        assert ws(B) == (OK, 4096 + 148 * 18 * 8 * (128 + 12) * 4)
+    assert ws(max_q=4) == (OK, 4096 + 148 * 18 * 16 * (128 + 12) * 4)
+    assert ws(max_q=2, D=64) == (OK, 4096 + 148 * 18 * 8 * (64 + 12) * 4)
     # more rows: counters, the list of 256-row tile pairs, and two parts of 256 rows per block
     for B, max_q in ((1, 5), (3, 1000)):
         pairs = B * -(-max_q * 4 // 256)
