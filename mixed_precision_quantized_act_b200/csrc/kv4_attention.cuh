@@ -13,28 +13,33 @@
 
 #include "gemm_w4w8a8.cuh"  // device_sm_count
 #include "kv4_cache.cuh"
+#include "kv4_ptx.cuh"
 #include "launch.h"
 #include "ptx_sm100.cuh"
 
 namespace mixllm {
 
 // ---------------------------------------------------------------------------
-// Few queries per request (decode).  HBM-bound: 2 * (D/2 + 4) bytes per cached
-// token and head.
+// Few queries per request (decode: up to 16 rows of query token and query head
+// per key head).  HBM-bound: 2 * (D/2 + 4) bytes per cached token and head.
 //
-// Work is cut into units of 32 tokens of one (request, row tile, key head);
-// block c takes the units [c U / P, (c + 1) U / P) of their concatenation and
-// its eight warps an eighth of them each, so requests of any lengths load every
-// SM alike, and the lengths stay on the device.  A row tile is 8 NT rows (query
-// token, query head of the group).  A warp fetches its tokens itself, by
-// cp.async into stages of its own, and meets the others only when all of the
+// Work is cut into units of 32 tokens of one (request, key head); block c takes
+// the units [c U / P, (c + 1) U / P) of their concatenation and its warps an
+// even share of them each, so requests of any lengths load every SM alike, and
+// the lengths stay on the device.  A warp fetches its tokens itself, by
+// cp.async into stages of its own (bulk copies of 2 KB, with less address
+// arithmetic, took 7 % longer), and meets the others only when all of the
 // block's units are done: the latencies where one request or head ends and the
-// next begins are then one warp's in sixteen, and few (with 256-token units
-// shared by the block's warps, every such step was a barrier for all of them:
-// 97 us instead of 66 for 64 requests of about 4100 tokens).  Tokens are the
-// 16-row side of m16n8k16 and the query rows its 8-column side, so that a group
+// next begins are then one warp's in sixteen.  Tokens are the 16-row side of
+// m16n8k16 and the query rows its 8-column side (NT such tiles), so that a group
 // of 8 heads fills the instruction and smaller ones waste only tensor work:
 // S^T = K Q^T with K as the A operand, then O^T = V^T P^T with V^T as A.
+//
+// Measured on B200 (as a CUDA graph): 64 requests of 100 to 8100 tokens, 32 query
+// and 8 key heads of 128: 83.7 us, 3.4 TB/s; 4 requests of 100000 to 131071
+// tokens, 64 and 8 heads: 119.5 us, 4.3 TB/s (66 % of the measured copy rate);
+// one request of 1003 tokens: 12.8 us.  With the products left out the second
+// takes 96 us, with the loads left out 114: neither hides the other wholly.
 //
 // What bounds the loop on the way to HBM speed is the unpacking: integer
 // instructions issue at half rate.  So one AND per pair of codes makes fp16
@@ -69,7 +74,7 @@ namespace mixllm {
 // times that of rounding the result alone, with it 1.4; it costs 3 to 6 % of the
 // time.  Sums stay in fp32.
 //
-// A segment (the units of one request, row tile and head) that one warp holds
+// A segment (the units of one request and head) that one warp holds
 // whole is written by it.  Parts of one that is cut between warps are joined by
 // the block at its end, and those cut between blocks left in the workspace,
 // where the last block to arrive adds them; always in the order of the tokens,
@@ -218,26 +223,9 @@ struct KvFetch {
   }
 };
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
 }
 // A row's scale, and its zero point as the subnormal z 2^-24.
 __device__ __forceinline__ float2 meta_pair(uint32_t m) { return __half22float2(*reinterpret_cast<const __half2 *>(&m)); }

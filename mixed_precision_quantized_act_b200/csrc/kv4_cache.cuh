@@ -42,7 +42,8 @@ __device__ __forceinline__ int owner_of(const int *start, int n, int i) {
 // the tokens and the new pages, each found by a binary search in the sums.
 // The cluster barrier between the scan and the first write lets seq_lens be
 // ctx_lens and left be count.  Latency-bound: one load round trip, the scan,
-// the search and a second trip for the page's number.
+// the search and a second trip for the page's number; 5.7 us for 64 requests of
+// one token on B200, 13.7 us for 256 prompts in 130304 slots.
 // ---------------------------------------------------------------------------
 constexpr int kAssignThreads = 1024;
 constexpr int kAssignCluster = 8;
@@ -160,7 +161,9 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const Assign
 // finite.  HBM-bound: reads 2 bytes and writes 0.5 (keys, values) or 2
 // (queries) a channel.  A lane takes `per` heads of its token, so that the
 // table's 8 bytes a channel are read once for all of them, and loads four heads
-// ahead (one head at a time: 62 us for 4099 tokens of 64 + 16 heads of 128).
+// ahead: with the read-back below, 4099 tokens of 64 + 16 heads of 128 took
+// 54 us on B200 (one head at a time 78 us).  Its integer and conversion
+// instructions, not HBM, bound it there (27 us of traffic).
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 

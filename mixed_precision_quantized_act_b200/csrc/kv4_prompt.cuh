@@ -9,6 +9,7 @@
 
 #include "gemm_w4w8a8.cuh"  // device_sm_count
 #include "kv4_attention.cuh"
+#include "kv4_ptx.cuh"
 #include "launch.h"
 #include "ptx_sm100.cuh"
 
@@ -55,6 +56,11 @@ namespace mixllm {
 // work stood behind everything).  The sequence depends on lengths that only the
 // device knows: a small kernel before this one lists the pairs and the running
 // sum of their tiles.
+//
+// Measured on B200: 1024 and 866 new tokens behind contexts of 8192 and 6354, 32
+// query and 8 key heads of 128: 254 us for the three kernels, 829 TFLOP/s (49 %
+// of the measured bf16 burst rate).  A pair's tile takes some 5000 clocks; the
+// softmax of its two halves is busy for 3900 of them (exponentials 2048).
 // ---------------------------------------------------------------------------
 constexpr int kPmThreads = 512;
 constexpr int kPmTile = 128;
@@ -171,49 +177,6 @@ struct PmWalk {
   __device__ __forceinline__ int rows(int group) const { return min(kPmRows, n * group - pair * kPmRows); }
 };
 
-// Instruction descriptor of tcgen05.mma kind::f16: fp16 operands, fp32
-// accumulator; A K-major, B K-major or MN-major.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
-  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-// D[tmem] (+)= A[smem] . B[smem], and with A in tensor memory (two fp16 per
-// 32-bit column).
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Descriptor of an MN-major operand in the 128-byte swizzle: rows (along K) of
-// 128 bytes (64 elements along MN), 8-row atoms `stride` apart along K
-// (1024 bytes), the next 64 elements along MN one panel further.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t panel) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(panel >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-// True on one lane of the (converged) warp, always the same one.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
 __device__ __forceinline__ ulonglong2 lds_2x2f(const float *p) { return *reinterpret_cast<const ulonglong2 *>(p); }
 
 // Codes minus zero point of eight channels (order 0 4 1 5 2 6 3 7), exact.
@@ -262,7 +225,6 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
     fence_mbar_init();
     abort_flag = 0;
   }
-  pdl_launch_dependents();
   pdl_wait();  // the plan, and with it all that came before it
   const int E = *plan.entries;
   const int64_t U = plan.cum[E] * H;
@@ -291,6 +253,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_launch_dependents();  // only now: a dependent may take tensor memory as it starts
   const uint32_t tmem = tmem_slot;
   PmWalk w;
   w.e = first_e;

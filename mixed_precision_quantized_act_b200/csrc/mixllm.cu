@@ -156,7 +156,7 @@ mixllm_status check_kv4_heads(int64_t requests, int64_t max_q, int32_t q_heads, 
 
 extern "C" {
 
-int mixllm_version(void) { return 100; }
+int mixllm_version(void) { return 200; }
 
 const char *mixllm_last_error(void) { return g_last_error; }
 
@@ -804,7 +804,9 @@ mixllm_status mixllm_sync_status(void *stream) {
     if (e != cudaSuccess) return cuda_fail(e, "status clear");
     if (status == mixllm::kStatusTimeout) return fail(MIXLLM_ERR_TIMEOUT, "a device-side wait gave up");
     if (status == mixllm::kStatusBounds)
-      return fail(MIXLLM_ERR_BOUNDS, "a range check of the checked build failed (the access was skipped)");
+      return fail(MIXLLM_ERR_BOUNDS,
+                  "a KV-cache kernel met a page, slot, position or length out of range, or a range check of the "
+                  "checked build failed (the access was skipped)");
     return fail(MIXLLM_ERR_INVALID_ARG, "device reported status %d", status);
   }
   return ok();

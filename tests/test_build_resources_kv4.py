@@ -8,7 +8,7 @@ BUDGETS = [
     ("_ZN6mixllm17kv4_decode_kernelILi128ELi1E", 64),
     ("_ZN6mixllm17kv4_decode_kernelILi128ELi2E", 64),
     ("_ZN6mixllm17kv4_decode_kernelILi64ELi1E", 0),
-    ("_ZN6mixllm17kv4_decode_kernelILi64ELi2E", 256),
+    ("_ZN6mixllm17kv4_decode_kernelILi64ELi2E", 320),
     ("_ZN6mixllm17kv4_prompt_kernel", 256),  # outside the softmax's loop
     ("_ZN6mixllm22kv4_prompt_join_kernel", 0),
     ("_ZN6mixllm22kv4_prompt_plan_kernel", 0),
