@@ -315,7 +315,7 @@ def test_attention_of_single_tokens(dev, kv, Hq, H, D, page):
 
 @pytest.mark.parametrize("kv,qs", [([3, 0, 40, 129], [3, 0, 2, 5]), ([2, 1], [5, 1]), ([200, 17], [8, 8]),
                                    ([1000], [2]), ([0, 0], [3, 1])], ids=str)
-@pytest.mark.parametrize("Hq,H,D,page", [(4, 2, 128, 16), (10, 1, 64, 64), (24, 1, 128, 64), (3, 3, 64, 128)])
+@pytest.mark.parametrize("Hq,H,D,page", [(4, 2, 128, 16), (10, 1, 64, 64), (20, 1, 128, 64), (3, 3, 64, 128)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_attention_of_few_tokens(dev, kv, qs, Hq, H, D, page, causal):
     _check(dev, kv, qs, Hq, H, D, page, causal, seed=sum(kv), tail=3)
@@ -473,3 +473,95 @@ def test_two_streams_with_their_own_workspaces(dev):
     mx.sync_status()
     for h, want in zip(held, alone):
         assert torch.equal(h[6], want)
+
+
+def _within(dev, out, case, causal=True):
+    q, cache, table, lens, cu = case
+    D = q.shape[2]
+    want, _, tol = ref.attention(q, cache.codes.cpu(), cache.meta.cpu(), table, lens.tolist(), cu.tolist(), D ** -0.5, causal)
+    n = int(cu[-1])
+    return bool(((out[:n].cpu().double() - want[:n]).abs() <= tol[:n]).all())
+
+
+def test_one_workspace_serves_calls_of_all_sizes(dev):
+    cases = [_case(dev, kv, qs, Hq, H, D, 64, seed=i) for i, (kv, qs, Hq, H, D) in enumerate([
+        ([3000, 10], [1, 1], 8, 2, 128), ([400, 300], [100, 33], 4, 1, 128), ([900], [1], 4, 4, 64),
+        ([700, 5, 90], [4, 2, 1], 6, 2, 64), ([2000], [9], 8, 2, 64)])]
+    need = [mx.kv4_attention_workspace(len(c[3]), int(c[4].diff().max()), c[0].shape[1], c[1], c[2].shape[1]).numel()
+            for c in cases]
+    ws = torch.zeros(max(need), dtype=torch.uint8, device=dev)
+    for _ in range(3):
+        for c in cases:
+            out = mx.kv4_attention(c[0].to(dev), c[1], c[2].to(dev), c[3], c[4], int(c[4].diff().max()), workspace=ws)
+            assert _within(dev, out, c)
+            assert not ws[:4096].any()
+    mx.sync_status()
+
+
+def test_prompts_in_a_graph_with_other_lengths(dev):
+    """One captured call, replayed for lengths from nothing to the most it was captured for."""
+    Hq, H, D, page = 4, 2, 128, 64
+    full = _case(dev, [600, 500, 300], [200, 90, 300], Hq, H, D, page, seed=3)
+    q, cache, table, lens, cu = full
+    qd, td = q.to(dev), table.to(dev)
+    out = torch.zeros_like(qd)
+    ws = mx.kv4_attention_workspace(3, 300, Hq, cache, table.shape[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    mx.kv4_attention_into(qd, cache, td, lens, cu, 300, out, ws, stream=side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mx.kv4_attention_into(qd, cache, td, lens, cu, 300, out, ws)
+    for kv, qs in (([600, 500, 300], [200, 90, 300]), ([600, 1, 300], [1, 1, 17]), ([0, 0, 0], [0, 0, 0]),
+                   ([128, 129, 0], [128, 0, 2]), ([600, 500, 300], [300, 300, 300])):
+        lens.copy_(torch.tensor(kv, dtype=torch.int32))
+        cu.copy_(torch.tensor([0, qs[0], qs[0] + qs[1], sum(qs)], dtype=torch.int32) if sum(qs) <= q.shape[0]
+                 else torch.tensor([0, 290, 590, 590], dtype=torch.int32))
+        out.fill_(77)
+        graph.replay()
+        mx.sync_status()
+        assert _within(dev, out, (q, cache, table, lens, cu))
+        assert (out[int(cu[-1]):] == 77).all()
+
+
+def test_attention_of_nothing(dev):
+    cache = mx.kv4_cache(2, 2, 64, 16, dev)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    q = torch.zeros((0, 4, 64), dtype=torch.float16, device=dev)
+    assert mx.kv4_attention(q, cache, torch.zeros((0, 3), dtype=torch.int32, device=dev), i32([]), i32([0]), 0).numel() == 0
+    assert mx.kv4_attention(q, cache, torch.zeros((2, 3), dtype=torch.int32, device=dev), i32([5, 0]), i32([0, 0, 0]), 1).numel() == 0
+    q = torch.full((3, 4, 64), 1.0, dtype=torch.float16, device=dev)  # rows of no request
+    out = mx.kv4_attention(q, cache, torch.zeros((1, 3), dtype=torch.int32, device=dev), i32([0]), i32([0, 0]), 3)
+    assert not out.any()
+    z = torch.zeros(0, dtype=torch.int64, device=dev)
+    kv = torch.zeros((0, 2, 64), dtype=torch.float16, device=dev)
+    mx.kv4_append_into(kv, kv, z, cache)
+    mx.kv4_read_into(z, cache, kv, kv.clone())
+    mx.sync_status()
+
+
+def test_everything_on_a_stream_of_its_own(dev):
+    """The given stream orders the calls, whatever the current one does."""
+    H, D, page, T = 2, 64, 16, 40
+    cache = mx.kv4_cache(8, H, D, page, dev)
+    x = torch.randn((T, 3 * H, D), device=dev).half()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    ctx, new, table = i32([0]), i32([T]), torch.full((1, 4), -1, dtype=torch.int32, device=dev)
+    free, count, seq, cu = i32(list(range(8))), i32([8]), i32([0]), i32([0, 0])
+    slots, pos = torch.zeros(T, dtype=torch.int64, device=dev), torch.zeros(T, dtype=torch.int32, device=dev)
+    left, status, rope = i32([0]), i32([-1]), mx.rope_table(64, D, device=dev)
+    q, out = torch.zeros((T, H, D), dtype=torch.float16, device=dev), torch.zeros((T, H, D), dtype=torch.float16, device=dev)
+    ws = mx.kv4_attention_workspace(1, T, H, cache, 4)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    big = torch.zeros(1 << 28, device=dev)
+    big.add_(1)  # the current stream is busy
+    for _ in range(3):
+        mx.kv4_assign_into(ctx, new, table, free, count, page, seq, cu, slots, pos, left, status, stream=s)
+        mx.kv4_append_into(x[:, H:2 * H], x[:, 2 * H:], slots, cache, q=x[:, :H], q_out=q, positions=pos, rope=rope, stream=s)
+        mx.kv4_attention_into(q, cache, table, seq, cu, T, out, ws, stream=s)
+    s.synchronize()
+    mx.sync_status(s)
+    assert int(status) == 0
+    assert _within(dev, out, (q.cpu(), cache, table.cpu(), seq, cu))
