@@ -727,10 +727,8 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
   const uint32_t before_me = there & ((1u << lane) - 1u);
   const int seg_before = __shfl_sync(0xFFFFFFFFu, part_seg, before_me ? 31 - __clz(before_me) : 0);
   uint32_t firsts = __ballot_sync(0xFFFFFFFFu, part_seg >= 0 && (!before_me || seg_before != part_seg));
-  const auto place_of = [&](int i) -> const float * {
-    return i & 1 ? last_parts + (i >> 1) * C::kPart : warp_parts + (c * kWarps + (i >> 1)) * C::kPart;
-  };
-  const float *my_part = place_of(lane & (2 * kWarps - 1));
+  const int my_warp = lane >> 1 & (kWarps - 1);
+  const float *my_part = lane & 1 ? last_parts + my_warp * C::kPart : warp_parts + (c * kWarps + my_warp) * C::kPart;
   KvRow<D> row;
   for (int item = 0; firsts; firsts &= firsts - 1) {
     const int first = __ffs(firsts) - 1;
@@ -756,19 +754,27 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
       row.sum = row.sum_lanes(ml.y * f);
       row.plain = row.sum_lanes(ml.z * f);
       const int at = r * C::kPitch + lane * KvRow<D>::kCh;
-#pragma unroll 1
-      for (uint32_t some = these; some;) {  // four parts' loads together
-        int i[4];
-        float v[4][KvRow<D>::kCh];
+      // the warps' last parts, in shared memory, then the few that a warp left behind before going on (any fixed
+      // order will do: a sum's terms are the same whoever was first)
+      constexpr int kTogether = 8;
+      for (uint32_t some = these & 0xAAAAAAAAu; some;) {
+        float v[kTogether][KvRow<D>::kCh], fx[kTogether];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          i[x] = some ? __ffs(some) - 1 : -1;
+        for (int x = 0; x < kTogether; ++x) {
+          const int i = some ? __ffs(some) - 1 : 0;
+          fx[x] = some ? __shfl_sync(0xFFFFFFFFu, f, i) : 0.0f;
+          row.template load<false>(last_parts + (some ? (i >> 1) * C::kPart : 0) + at, v[x]);
           some &= some - 1;
-          if (i[x] >= 0) row.template load<false>(place_of(i[x]) + at, v[x]);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (i[x] >= 0) row.add(v[x], __shfl_sync(0xFFFFFFFFu, f, i[x]));
+        for (int x = 0; x < kTogether; ++x)
+          if (fx[x] != 0.0f) row.add(v[x], fx[x]);
+      }
+      for (uint32_t some = these & 0x55555555u; some; some &= some - 1) {
+        const int i = __ffs(some) - 1;
+        float v[KvRow<D>::kCh];
+        row.template load<true>(warp_parts + (c * kWarps + (i >> 1)) * C::kPart + at, v);
+        row.add(v, __shfl_sync(0xFFFFFFFFu, f, i));
       }
       if (whole) {
         row.write(a, seg, r, lane);
