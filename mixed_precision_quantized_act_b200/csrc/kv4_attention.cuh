@@ -37,8 +37,8 @@ namespace mixllm {
 //
 // Measured on B200 (as a CUDA graph): 64 requests of 100 to 8100 tokens, 32 query
 // and 8 key heads of 128: 83.7 us, 3.4 TB/s; 4 requests of 100000 to 131071
-// tokens, 64 and 8 heads: 119.5 us, 4.3 TB/s (66 % of the measured copy rate);
-// one request of 1003 tokens: 12.8 us.  With the products left out the second
+// tokens, 64 and 8 heads: 119 us, 4.3 TB/s (66 % of the measured copy rate);
+// one request of 1003 tokens: 11.6 us.  With the products left out the second
 // takes 96 us, with the loads left out 114: neither hides the other wholly.
 //
 // What bounds the loop on the way to HBM speed is the unpacking: integer
