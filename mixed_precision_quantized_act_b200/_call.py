@@ -3,6 +3,8 @@ tensors, and the device and stream a call goes to.  A decode step makes a few
 such calls per layer, so they are kept short."""
 from __future__ import annotations
 
+from contextlib import nullcontext
+
 import torch
 
 from . import _lib
@@ -59,6 +61,13 @@ def call(fn: str, device: int, stream, *args):
             status = f(*args, handle)
     if status != _lib.OK:
         _lib._check(status, fn)
+
+
+def allocating(stream):
+    """A context in which new tensors belong to `stream` (the current one when
+    None): what fills them comes before the call's kernels there, and their
+    memory goes to others only behind them."""
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def ptr(t):

@@ -9,7 +9,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._call import call, need, on_cuda, ptr, rows
+from ._call import allocating, call, need, on_cuda, ptr, rows
 
 _F16, _F32, _I32, _I64 = torch.float16, torch.float32, torch.int32, torch.int64
 
@@ -161,9 +161,11 @@ def kv4_attention_into(q, cache: KV4Cache, block_table, seq_lens, cu_q, max_q: i
 def kv4_attention(q, cache: KV4Cache, block_table, seq_lens, cu_q, max_q: int, scale=None, causal: bool = True,
                   workspace=None, stream=None) -> torch.Tensor:
     """kv4_attention_into with a fresh output and, unless given, workspace.
-    Rows of q outside every request come back as zeros."""
-    out = torch.zeros_like(q, memory_format=torch.contiguous_format)
-    if workspace is None:
-        workspace = kv4_attention_workspace(seq_lens.shape[0], max_q, q.shape[1], cache, block_table.shape[1])
+    Rows of q outside every request come back as zeros.  With a stream, both
+    are allocated on it."""
+    with allocating(stream):
+        out = torch.zeros_like(q, memory_format=torch.contiguous_format)
+        if workspace is None:
+            workspace = kv4_attention_workspace(seq_lens.shape[0], max_q, q.shape[1], cache, block_table.shape[1])
     kv4_attention_into(q, cache, block_table, seq_lens, cu_q, max_q, out, workspace, scale, causal, None, stream)
     return out

@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._call import call, need, on_cuda, ptr, rows
+from ._call import allocating, call, need, on_cuda, ptr, rows
 
 _F16, _F32 = torch.float16, torch.float32
 
@@ -66,6 +66,7 @@ def dequantize_act_into(A_q, s_a, X, stream=None):
 
 def dequantize_act(A_q, s_a, stream=None) -> torch.Tensor:
     """A_q int8 [M, K], s_a fp32 [M, K/128] -> fp16 [M, K]."""
-    X = torch.empty(A_q.shape, dtype=_F16, device=A_q.device)
+    with allocating(stream):
+        X = torch.empty(A_q.shape, dtype=_F16, device=A_q.device)
     dequantize_act_into(A_q, s_a, X, stream)
     return X

@@ -541,6 +541,35 @@ def test_attention_of_nothing(dev):
     mx.sync_status()
 
 
+def test_fresh_tensors_belong_to_the_given_stream(dev):
+    """What kv4_attention and dequantize_act allocate is filled and reused in
+    the given stream's order, however far behind the current one is."""
+    H, D, page, T = 2, 64, 16, 1000
+    cache = mx.kv4_cache(64, H, D, page, dev)
+    kv = torch.randn((T, 2 * H, D), device=dev).half()
+    mx.kv4_append_into(kv[:, :H], kv[:, H:], torch.arange(T, device=dev), cache)
+    table = torch.arange(64, dtype=torch.int32, device=dev).reshape(1, 64)
+    seq = torch.tensor([T], dtype=torch.int32, device=dev)
+    A_q, s_a = mx.quantize_act(torch.randn((64, 256), device=dev).half())
+    back = mx.dequantize_act(A_q, s_a)
+    s, big = torch.cuda.Stream(), torch.zeros(1 << 28, device=dev)
+    for n in (1, 100):  # either kernel
+        q = torch.randn((n, H, D), device=dev).half()
+        cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+        torch.full((1 << 22,), 255, dtype=torch.uint8, device=dev)  # freed: fresh memory need not be zero
+        torch.cuda.synchronize()
+        for _ in range(10):
+            big.add_(1)  # the current stream is busy
+        out = mx.kv4_attention(q, cache, table, seq, cu, n, stream=s)
+        X = mx.dequantize_act(A_q, s_a, stream=s)
+        for _ in range(10):
+            big.add_(1)
+        torch.cuda.synchronize()
+        mx.sync_status()
+        assert _within(dev, out, (q.cpu(), cache, table.cpu(), seq, cu))
+        assert torch.equal(X, back)
+
+
 def test_everything_on_a_stream_of_its_own(dev):
     """The given stream orders the calls, whatever the current one does."""
     H, D, page, T = 2, 64, 16, 40
