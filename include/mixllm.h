@@ -632,8 +632,10 @@ MIXLLM_API mixllm_status mixllm_kv4_attention_workspace_bytes(int64_t requests, 
  *            at the same time must not share one.  After MIXLLM_ERR_TIMEOUT
  *            zero it again.
  * The lengths stay on the device: a captured graph serves any lengths within
- * requests, max_q and table_width.  At most 16384 requests.  The result does
- * not depend on timing.  Asynchronous on `stream`.
+ * requests, max_q and table_width.  At most 16384 requests and, where max_q *
+ * g <= 16, requests * kv_heads * ceil(table_width * page_size / 32) below 2^31
+ * (MIXLLM_ERR_UNSUPPORTED otherwise).  The result does not depend on timing.
+ * Asynchronous on `stream`.
  */
 MIXLLM_API mixllm_status mixllm_kv4_attention(const void *q_f16, int64_t q_stride, int64_t n_tokens, int32_t q_heads,
                                               const uint8_t *codes, const uint32_t *meta, int64_t pages,

@@ -88,6 +88,8 @@ def kv4_append_into(k, v, slots, cache: KV4Cache, q=None, q_out=None, positions=
     dev = cache.index
     T = slots.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
+    if (q is not None and q_out is None) or (rope is not None and positions is None):
+        raise ValueError("q needs q_out, and rope positions")
     need(slots, "slots", _I64, (T,), dev)
     k_stride, v_stride = rows(k, "k", _F16, shape, dev), rows(v, "v", _F16, shape, dev)
     q_heads = q_stride = out_stride = max_pos = rotary = 0

@@ -541,6 +541,15 @@ def test_attention_of_nothing(dev):
     mx.sync_status()
 
 
+def test_append_needs_what_goes_together(dev):
+    cache = mx.kv4_cache(1, 1, 64, 16, dev)
+    kv, slots = torch.zeros((2, 1, 64), dtype=torch.float16, device=dev), torch.arange(2, device=dev)
+    with pytest.raises(ValueError, match="q_out"):
+        mx.kv4_append_into(kv, kv, slots, cache, q=kv)
+    with pytest.raises(ValueError, match="positions"):
+        mx.kv4_append_into(kv, kv, slots, cache, rope=mx.rope_table(4, 64, device=dev))
+
+
 def test_fresh_tensors_belong_to_the_given_stream(dev):
     """What kv4_attention and dequantize_act allocate is filled and reused in
     the given stream's order, however far behind the current one is."""
