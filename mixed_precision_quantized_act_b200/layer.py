@@ -153,18 +153,19 @@ class AttentionBlock:
         given; returns the output buffer fp16 [tokens, K].  seq_lens counts the
         new tokens (behind those cached); rows behind cu_q's last entry are padding
         and their outputs of no meaning."""
-        H = self.cache.kv_heads
-        norm.residual_norm_quantize_into(r, self.w_norm, self.A_q, self.s_a, x=x, r_out=None if x is None else r,
-                                         eps=self.eps, stream=stream)
-        Y = self.heads.view(self.tokens, -1)
-        if self.few:
-            _lib.gemm_w4w8a8_small_m_into(self.A_q, self.s_a, self.qkv, Y, self.ws_qkv, stream)
-        else:
-            _lib.gemm_w4w8a8_into(self.A_q, self.s_a, self.qkv, Y, stream)
-        q, k, v = self.heads.split((self.q_heads, H, H), 1)
-        kv4.kv4_append_into(k, v, slots, self.cache, q=q, q_out=self.q, positions=positions, rope=self.rope,
-                            stream=stream)
-        kv4.kv4_attention_into(self.q, self.cache, block_table, seq_lens, cu_q, self.max_q, self.att, self.ws_att,
-                               stream=stream)
-        _lib.linear_into(self.att.view(self.tokens, -1), self.o_proj, self.out, self.ws_o, stream)
+        with torch.cuda.device(self.cache.device):  # whatever the current device is
+            H = self.cache.kv_heads
+            norm.residual_norm_quantize_into(r, self.w_norm, self.A_q, self.s_a, x=x, r_out=None if x is None else r,
+                                             eps=self.eps, stream=stream)
+            Y = self.heads.view(self.tokens, -1)
+            if self.few:
+                _lib.gemm_w4w8a8_small_m_into(self.A_q, self.s_a, self.qkv, Y, self.ws_qkv, stream)
+            else:
+                _lib.gemm_w4w8a8_into(self.A_q, self.s_a, self.qkv, Y, stream)
+            q, k, v = self.heads.split((self.q_heads, H, H), 1)
+            kv4.kv4_append_into(k, v, slots, self.cache, q=q, q_out=self.q, positions=positions, rope=self.rope,
+                                stream=stream)
+            kv4.kv4_attention_into(self.q, self.cache, block_table, seq_lens, cu_q, self.max_q, self.att, self.ws_att,
+                                   stream=stream)
+            _lib.linear_into(self.att.view(self.tokens, -1), self.o_proj, self.out, self.ws_o, stream)
         return self.out
