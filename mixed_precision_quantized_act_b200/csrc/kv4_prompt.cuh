@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
   float *k_scale = reinterpret_cast<float *>(smem + 6 * kOperand);  // [ring][128], to log2 units
   float *v_scale = k_scale + kPmScaleRing * kPmTile;
   __shared__ uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2];  // s, p: [tile][half]
-  __shared__ uint32_t seen[kPmScaleRing][4];   // bit t: token t's page exists
-  __shared__ float v_top[kPmScaleRing][4];     // largest value scales of 32 tokens each
+  __shared__ __align__(16) uint32_t seen[kPmScaleRing][4];  // bit t: token t's page exists; read in pairs
+  __shared__ __align__(16) float v_top[kPmScaleRing][4];    // largest value scales of 32 tokens each; read as one
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ int first_e;
