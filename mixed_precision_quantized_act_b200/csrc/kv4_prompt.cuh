@@ -42,10 +42,11 @@ namespace mixllm {
 //
 // Scales: a key's scale multiplies its column of S in the softmax, a value's
 // scale its column of P before the rounding to fp16 (the one rounding of the
-// weights).  The exponent's reference R is the running maximum plus the
-// logarithm of the largest value scale, both moved only when passed by 8 and 2
-// (in log2 units), so p s_v stays within 2^10; O is then rescaled in tensor
-// memory, which is rare.
+// weights).  The exponent's reference R is the row's own, 7 (in log2 units)
+// below its largest weight p s_v so far among the columns that it sees, and moved
+// only when a weight passes 2^15: what a row does not see, or gives no weight,
+// costs it no bits, and weights down to 2^-21 of the largest are normal numbers.
+// Where R moves, O is rescaled in tensor memory, which is rare.
 //
 // Bound by the tensor core (4 D flops per row and token) and, close behind, by
 // the exponentials: 16 a clock and SM make a 128 x 128 tile 1024 clocks, its two
@@ -58,21 +59,25 @@ namespace mixllm {
 // sum of their tiles.
 //
 // Measured on B200: 1024 and 866 new tokens behind contexts of 8192 and 6354, 32
-// query and 8 key heads of 128: 254 us for the three kernels, 829 TFLOP/s (49 %
-// of the measured bf16 burst rate).  A pair's tile takes some 5000 clocks; the
-// softmax of its two halves is busy for 3900 of them (exponentials 2048).
+// query and 8 key heads of 128: 248 us for the three kernels, 850 TFLOP/s (51 %
+// of the measured bf16 burst rate); 16 and 4 heads of 64: 122 us, 431 TFLOP/s.  A
+// pair's tile takes some 4900 clocks at heads of 128, of which the exponentials
+// need 2048.
 // ---------------------------------------------------------------------------
 constexpr int kPmThreads = 512;
 constexpr int kPmTile = 128;
 constexpr int kPmRows = 256;
 constexpr int kPmMaxGrid = 148;
 constexpr int kPmScaleRing = 4;
+constexpr float kPmLift = 7.0f;        // log2 of a row's largest weight where its reference is set
+constexpr float kPmTopWeight = 0x1p15f;  // and the largest before it is moved
+constexpr float kPmTopSum = 0x1p80f;   // sum of p: larger ones are zero-valued tokens' alone, and move it too
 
 template <int D>
 struct PmCfg {
   static constexpr int kPanel = 128 * 128;  // bytes of 128 rows of 64 channels
   static constexpr int kOperand = D / 64 * kPanel;
-  static constexpr int kSmem = 6 * kOperand + kPmScaleRing * 2 * kPmTile * 4 + 1024;
+  static constexpr int kSmem = 6 * kOperand + kPmScaleRing * 3 * kPmTile * 4 + 1024;
   static constexpr int64_t kPart = static_cast<int64_t>(kPmRows) * (D + 2);  // floats
   static_assert(kSmem + 1024 <= 227 * 1024, "shared memory of a block");
 };
@@ -200,9 +205,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
   uint8_t *q_s = smem, *k_s = smem + 2 * kOperand, *v_s = smem + 4 * kOperand;
   float *k_scale = reinterpret_cast<float *>(smem + 6 * kOperand);  // [ring][128], to log2 units
   float *v_scale = k_scale + kPmScaleRing * kPmTile;
+  float *v_log = v_scale + kPmScaleRing * kPmTile;  // log2 of it, of 2^-24 at least
   __shared__ uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2];  // s, p: [tile][half]
   __shared__ __align__(16) uint32_t seen[kPmScaleRing][4];  // bit t: token t's page exists; read in pairs
-  __shared__ __align__(16) float v_top[kPmScaleRing][4];    // largest value scales of 32 tokens each; read as one
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ int first_e;
@@ -425,14 +430,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
         const float2 vs = __half22float2(*reinterpret_cast<const __half2 *>(&vm));
         k_scale[at * kPmTile + tk] = ks.x * scale2;
         v_scale[at * kPmTile + tk] = vs.x;
-        float top = vs.x;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        v_log[at * kPmTile + tk] = __log2f(fmaxf(vs.x, 0x1p-24f));
         const uint32_t bits = __ballot_sync(0xFFFFFFFFu, ok_now);
-        if (lane == 0) {
-          v_top[at][warp - 4] = top;
-          seen[at][warp - 4] = bits;
-        }
+        if (lane == 0) seen[at][warp - 4] = bits;
       }
       store(k_s + s * kOperand, kr, km);
       mbar_arrive(&k_full[s]);
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       // keys this row sees; rows behind the last one see what the request has
       const int lim = valid && a.causal ? w.kv - w.n + tok + 1 : w.kv;
       const int lim_min = __shfl_sync(0xFFFFFFFFu, lim, 0);
-      float m = kKvNoMax, log_s = -24.0f;  // the reference is m + log_s
+      float ref = kKvNoMax;  // of the exponents; the first column that the row sees sets it
       uint64_t sum2 = 0;
       for (int jh = 0; jh < 2 * w.count; ++jh) {
         const int h = jh & 1, at = (it + (jh >> 1)) & (kPmScaleRing - 1);
@@ -497,7 +497,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           break;
         }
         tc_fence_after();
-        const float *ks = k_scale + at * kPmTile + 64 * h, *vs = v_scale + at * kPmTile + 64 * h;
+        const float *ks = k_scale + at * kPmTile + 64 * h, *vs = v_scale + at * kPmTile + 64 * h,
+                    *vl = v_log + at * kPmTile + 64 * h;
         const uint2 there = *reinterpret_cast<const uint2 *>(&seen[at][2 * h]);
         const bool whole = base + 64 <= lim_min && (there.x & there.y) == 0xFFFFFFFFu;
         // bit k: column 32 b + k is seen by this row
@@ -506,9 +507,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           return (b == 0 ? there.x : there.y) &
                  (n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u));
         };
-        // the row's largest score
-        const auto maximum = [&](auto all) {
-          constexpr bool kAll = decltype(all)::value;  // every column is seen by every row of the warp
+        // the logarithm of the row's largest weight; a value scale of zero counts as 2^-24, so that the sum of
+        // p stays finite, too
+        const auto maximum = [&] {
           float top = -INFINITY;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
@@ -516,24 +517,22 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
             tmem_ld_32x32b_x32(sh_at + 32 * b, c);
             tmem_ld_wait();
             reg_fence(c);
-            const uint32_t see = kAll ? 0xFFFFFFFFu : visible(b);
+            const uint32_t see = visible(b);
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const float v = __uint_as_float(c[k]) * ks[32 * b + k];
-              top = fmaxf(top, kAll || (see >> k & 1u) ? v : -INFINITY);
+              const float v = fmaf(__uint_as_float(c[k]), ks[32 * b + k], vl[32 * b + k]);
+              top = fmaxf(top, see >> k & 1u ? v : -INFINITY);
             }
           }
           return top;
         };
-        // the row's weights p s_v, relative to the reference; adds sum p to sum2 and returns the largest score
-        // above the reference
+        // the row's weights p s_v, relative to the reference; adds sum p to sum2 and returns the largest weight
         uint32_t p[32];
         const auto weights = [&](auto all) {
           constexpr bool kAll = decltype(all)::value;
-          const float ref = -(m + log_s);
-          const uint64_t ref2 = pack_f2(ref, ref);
+          const uint64_t ref2 = pack_f2(-ref, -ref);
           uint32_t x[2][32];
-          float hi[2] = {-INFINITY, -INFINITY};
+          float hi[2] = {0.0f, 0.0f};
           tmem_ld_32x32b_x32(sh_at, x[0]);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
@@ -551,22 +550,22 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
                 float2 v = unpack_f2(
                     fma_f2(pack_f2(__uint_as_float(c[at2]), __uint_as_float(c[at2 + 1])), q ? f.y : f.x, ref2));
                 if constexpr (!kAll) v.x = see >> at2 & 1u ? v.x : -INFINITY, v.y = see >> (at2 + 1) & 1u ? v.y : -INFINITY;
-                hi[q] = fmaxf(fmaxf(hi[q], v.x), v.y);
                 const uint64_t e2 = pack_f2(ex2(v.x), ex2(v.y));
                 sum2 = add_f2(sum2, e2);
                 float2 pv = unpack_f2(mul_f2(e2, q ? g.y : g.x));
                 // a value's scale may be NaN: select, not multiply
                 if constexpr (!kAll) pv.x = see >> at2 & 1u ? pv.x : 0.0f, pv.y = see >> (at2 + 1) & 1u ? pv.y : 0.0f;
+                hi[q] = fmaxf(fmaxf(hi[q], pv.x), pv.y);
                 p[16 * b + 2 * k + q] = half2_bits(pv.x, pv.y);
               }
             }
           }
           return fmaxf(hi[0], hi[1]);
         };
-        // moves the reference to these, and takes the sums along
-        const auto move_to = [&](float m_new, float ls_new) {
-          const float keep = ex2((m - m_new) + (log_s - ls_new));
-          m = m_new, log_s = ls_new;
+        // moves the reference there, and takes the sums along
+        const auto move_to = [&](float to) {
+          const float keep = ex2(ref - to);
+          ref = to;
           sum2 = mul_f2(sum2, pack_f2(keep, keep));
           if (jh > 0) {
             // no product into O may be under way: this half's last one came before its s_full, the other
@@ -585,24 +584,20 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
             }
           }
         };
-        const float4 st = *reinterpret_cast<const float4 *>(v_top[at]);
-        const float log_top = __log2f(fmaxf(fmaxf(st.x, st.y), fmaxf(fmaxf(st.z, st.w), 0x1p-24f)));
         // A row's first scores set its reference before they are used.  Later ones are used with the reference
-        // that there is, and once more where they pass it by too much, which is rare.
-        const bool first = __any_sync(0xFFFFFFFFu, m == kKvNoMax);
-        float ls_new = log_top > log_s + 2.0f ? log_top : log_s;
-        float m_new = m;
-        if (first) {
-          const float top = whole ? maximum(std::true_type{}) : maximum(std::false_type{});
-          if (top > m + 8.0f) m_new = top;
-        }
-        if (__any_sync(0xFFFFFFFFu, m_new != m || ls_new != log_s)) move_to(m_new, ls_new);
-        const uint64_t sum_before = sum2;
-        for (int again = 0; again < 2; ++again) {
-          const float over = (whole ? weights(std::true_type{}) : weights(std::false_type{})) + log_s;
-          if (first || !__any_sync(0xFFFFFFFFu, over > 8.0f)) break;
+        // that there is, and once more where a weight passes it by too much, which is rare.
+        for (bool set = __any_sync(0xFFFFFFFFu, ref == kKvNoMax);; set = true) {
+          if (set) {
+            const float to = maximum() - kPmLift;
+            const bool move = to > ref + 8.0f;
+            if (__any_sync(0xFFFFFFFFu, move)) move_to(move ? to : ref);
+          }
+          const uint64_t sum_before = sum2;
+          const float top = whole ? weights(std::true_type{}) : weights(std::false_type{});
+          const float2 s2 = unpack_f2(sum2);
+          const bool over = top > kPmTopWeight || s2.x + s2.y > kPmTopSum;
+          if (set || !__any_sync(0xFFFFFFFFu, over)) break;
           sum2 = sum_before;
-          move_to(over > 8.0f ? m + over : m, log_s);
         }
         tmem_st_32x32b_x32(sh_at, p);  // over the half's first columns
         tmem_st_wait();
@@ -616,7 +611,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       if (!ok) break;
       tc_fence_after();
       const float2 both = unpack_f2(sum2);
-      const float sum = both.x + both.y, ref = m + log_s;
+      const float sum = both.x + both.y;
       const bool cut = w.count < w.tiles;
       const int side = start <= w.seg_first ? 1 : 0;  // the block's end cuts it, or its beginning
       float *part = parts + (static_cast<int64_t>(c) * 2 + side) * C::kPart;
