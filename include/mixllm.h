@@ -616,7 +616,10 @@ MIXLLM_API mixllm_status mixllm_kv4_attention_workspace_bytes(int64_t requests, 
  *   out[i, h] = sum_t softmax_t(scale * q[i, h] . k[t, h / g]) v[t, h / g],
  * g = q_heads / kv_heads.  Scores, softmax statistics and sums are fp32; the
  * probabilities, times the values' scales, are rounded once to fp16 for the
- * tensor cores.  A query that sees no token gets zeros (and lse -infinity).
+ * tensor cores: to 11 bits, or where such a weight is below 2^-21 of the
+ * largest of its row, by at most 2^-32 of that.  Tokens that a query does not
+ * see have no part in it.  A query that sees no token gets zeros (and lse
+ * -infinity).
  * Only the first ceil(seq_lens[b] / page_size) entries of a request's row of
  * the table are read.  Rows of q and out outside every request are neither read
  * nor written.

@@ -63,14 +63,18 @@ namespace mixllm {
 // is lost than in the sums themselves.  P^T goes from accumulator to B layout
 // by movmatrix.
 //
-// Softmax per warp with lazy rescaling: the running maximum m moves only when
-// a score passes it by more than 8 (in log2 units), so p <= 2^8.  The values'
-// scales pass through fp16 together with p, as p * s_v / S with S the running
-// maximum of s_v (moved when passed by a factor of 4); the accumulators hold
-// O / S.  p s_v is rounded once, to fp16's 11 bits, and O is divided by the sum
-// of p as that rounding leaves it (the logarithm of the denominator is that of
-// the unrounded sum): where one token has nearly all the weight, its error
-// cancels.  Without it a single request's error against 64 bits was up to 1.6
+// Softmax per warp with lazy rescaling.  The values' scales pass through fp16
+// together with p, as weights p s_v.  The exponents' reference m of a row is 7
+// (in log2 units) below its largest weight so far among the keys that it sees (a
+// scale of zero counting as 2^-24, so that the sum of p stays finite), and moves
+// only when a weight passes 2^15: what a row does not see, or gives no weight,
+// costs it no bits, and weights down to 2^-21 of the largest are normal numbers.
+// A weight is rounded once, to fp16's 11 bits, and O is divided by the sum of p as
+// that rounding leaves it (the logarithm of the denominator is that of the
+// unrounded sum): where one token has nearly all the weight, its error cancels.
+// The correction is left out for values much smaller than the largest, S, that
+// the warp has met: a weight that is an fp16 subnormal, or zero, says little
+// about p.  Without it a single request's error against 64 bits was up to 1.6
 // times that of rounding the result alone, with it 1.4; it costs 3 to 6 % of the
 // time.  Sums stay in fp32.
 //
@@ -82,6 +86,7 @@ namespace mixllm {
 // ---------------------------------------------------------------------------
 constexpr int kKvTile = 32;  // tokens per unit
 constexpr float kKvNoMax = -3.0e38f;
+constexpr float kKvLift = 7.0f;  // log2 of a row's largest weight where its reference is set: 2^15, 8 more, is in range
 
 template <int D, int NT>
 struct KvCfg {
@@ -425,20 +430,20 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
 
   float o[NT][kMTiles][4], oz[NT][4];  // oz: sums of p z, the same in every row
   float m[NT][2], l[NT][2], off[NT][2];  // off: by how much rounding the weights moved l
-  float S, inv_S;
-  // this warp's part of a segment: S O, and (m, l) per row
+  float S;  // largest scale of a value met, within a factor of 4
+  // this warp's part of a segment: O, and (m, l) per row
   const auto leave = [&](float *part) {
 #pragma unroll
     for (int ni = 0; ni < NT; ++ni)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int r = ni * 8 + 2 * t + j;
-        const float back = S * 0x1p10f, z = oz[ni][j];
+        const float z = oz[ni][j];
         float *dst = part + r * C::kPitch + g * 2;
 #pragma unroll
         for (int k = 0; k < kMTiles; ++k)
           *reinterpret_cast<float2 *>(dst + 16 * k) =
-              make_float2((o[ni][k][j] - z) * back, fmaf(o[ni][k][2 + j], kHighToLow, -z) * back);
+              make_float2((o[ni][k][j] - z) * 0x1p10f, fmaf(o[ni][k][2 + j], kHighToLow, -z) * 0x1p10f);
         if (g == 0)
           *reinterpret_cast<float4 *>(part + kRows * C::kPitch + 4 * r) = make_float4(m[ni][j], l[ni][j] + off[ni][j], l[ni][j], 0.0f);
       }
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
     const int last_row = min(rows, row0 + kRows) - 1;
     const int lim_max = a.causal ? w.r.kv - w.r.n + last_row / group + 1 : w.r.kv;
 
-    S = 0x1p-24f, inv_S = 0x1p24f;
+    S = 0x1p-24f;
 #pragma unroll
     for (int ni = 0; ni < NT; ++ni) {
       m[ni][0] = m[ni][1] = kKvNoMax;
@@ -566,7 +571,12 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
           if (tb >= lim_max) sv[x][1] = 0.0f;
         }
       }
-      // ---- running maximum
+      // ---- running maximum of the weights
+      float ls[2][2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) ls[x][i] = lg2(sv[x][i] + 0x1p-24f);
       const float sv_max = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
       bool move = sv_max > 4.0f * S;
       float top[NT][2];
@@ -574,41 +584,38 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
       for (int ni = 0; ni < NT; ++ni)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          top[ni][j] = fmaxf(fmaxf(sc[0][ni][j], sc[0][ni][2 + j]), fmaxf(sc[1][ni][j], sc[1][ni][2 + j]));
-          move |= top[ni][j] > m[ni][j] + 8.0f;
+          top[ni][j] = fmaxf(fmaxf(sc[0][ni][j] + ls[0][0], sc[0][ni][2 + j] + ls[0][1]),
+                             fmaxf(sc[1][ni][j] + ls[1][0], sc[1][ni][2 + j] + ls[1][1]));
+          move |= top[ni][j] > m[ni][j] + (kKvLift + 8.0f);
         }
       if (__any_sync(0xFFFFFFFFu, move)) {
-        float s_new = fmaxf(S, sv_max);
+        S = fmaxf(S, sv_max);
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) s_new = fmaxf(s_new, __shfl_xor_sync(0xFFFFFFFFu, s_new, x));
-        const float down = __fdividef(S, s_new);
-        S = s_new;
-        inv_S = __fdividef(1.0f, S);
+        for (int x = 4; x < 32; x <<= 1) S = fmaxf(S, __shfl_xor_sync(0xFFFFFFFFu, S, x));
 #pragma unroll
         for (int ni = 0; ni < NT; ++ni)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float mx = fmaxf(m[ni][j], top[ni][j]);
+            float mx = top[ni][j] - kKvLift;
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+            mx = fmaxf(mx, m[ni][j]);
             const float keep = ex2(m[ni][j] - mx);
             m[ni][j] = mx;
             l[ni][j] *= keep, off[ni][j] *= keep;
-            oz[ni][j] *= keep * down;
+            oz[ni][j] *= keep;
 #pragma unroll
             for (int k = 0; k < kMTiles; ++k) {
-              o[ni][k][j] *= keep * down;
-              o[ni][k][2 + j] *= keep * down;
+              o[ni][k][j] *= keep;
+              o[ni][k][2 + j] *= keep;
             }
           }
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         // ---- probabilities
-        const float wa = sv[x][0] * inv_S, wb = sv[x][1] * inv_S;
-        // for values of a size with the largest: smaller ones' weights may be fp16 subnormals, whose rounding says
-        // nothing about p
-        const float ra = wa >= 0.125f ? __fdividef(1.0f, wa) : 0.0f, rb = wb >= 0.125f ? __fdividef(1.0f, wb) : 0.0f;
+        const float wa = sv[x][0], wb = sv[x][1];
+        const float ra = wa >= 0.125f * S ? __fdividef(1.0f, wa) : 0.0f, rb = wb >= 0.125f * S ? __fdividef(1.0f, wb) : 0.0f;
         uint32_t pf[NT][2];
 #pragma unroll
         for (int ni = 0; ni < NT; ++ni) {
@@ -691,7 +698,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
           if (r >= rows) continue;
           const int tok = r / group, head = w.h * group + r - tok * group;
           const int64_t token = static_cast<int64_t>(w.r.q0) + tok;
-          const float inv = l[ni][j] == 0.0f ? 0.0f : S * 0x1p10f / (l[ni][j] + off[ni][j]);  // a row that saw no key is zero
+          const float inv = l[ni][j] == 0.0f ? 0.0f : 0x1p10f / (l[ni][j] + off[ni][j]);  // a row that saw no key is zero
           const float z = oz[ni][j];
           uint32_t packed[kMTiles];
 #pragma unroll

@@ -1,6 +1,6 @@
 // kv4_ptx.cuh -- inline-PTX wrappers of the attention kernels: the warp's matrix
 // product and transpose, tcgen05.mma kind::f16 with its descriptors, pairs of
-// floats, the base-2 exponential and a copy to a 32-bit shared address.
+// floats, the base-2 exponential and logarithm and a copy to a 32-bit shared address.
 #pragma once
 
 #include <cstdint>
@@ -25,6 +25,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 

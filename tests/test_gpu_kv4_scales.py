@@ -56,7 +56,8 @@ def _run(dev, q, cache, table, kv, qs, causal=True, scale=None):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("Hq,Hkv,n,context", [(4, 1, 70, 0), (2, 2, 150, 0), (3, 1, 100, 200)])
+@pytest.mark.parametrize("Hq,Hkv,n,context", [(2, 1, 2, 0), (4, 2, 4, 0), (8, 1, 2, 300),          # few rows
+                                              (4, 1, 70, 0), (2, 2, 150, 0), (3, 1, 100, 200)])   # prompts
 @pytest.mark.parametrize("power", [12, 4])
 def test_tokens_that_are_not_seen_yet_have_no_say(dev, D, Hq, Hkv, n, context, power):
     """The newest tokens' values are 2^17 or 2^25 times as large as those before:
@@ -71,7 +72,7 @@ def test_tokens_that_are_not_seen_yet_have_no_say(dev, D, Hq, Hkv, n, context, p
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("Hq,Hkv,n", [(4, 1, 90)])
+@pytest.mark.parametrize("Hq,Hkv,n", [(2, 1, 1), (4, 1, 4), (4, 1, 90)])
 @pytest.mark.parametrize("where", [0, 40, 399])
 def test_tokens_without_weight_have_no_say(dev, D, Hq, Hkv, n, where):
     """One token has values 2^25 times as large as the others' and a score at
@@ -90,7 +91,7 @@ def test_tokens_without_weight_have_no_say(dev, D, Hq, Hkv, n, where):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("Hq,Hkv,n", [(4, 1, 90)])
+@pytest.mark.parametrize("Hq,Hkv,n", [(2, 1, 1), (4, 1, 4), (4, 1, 90)])
 def test_value_rows_of_zeros_take_their_share(dev, D, Hq, Hkv, n):
     """A token whose values are all zero (a scale of zero) has nearly all the
     weight: the others' share of the result is what the denominator leaves."""
@@ -109,7 +110,7 @@ def test_value_rows_of_zeros_take_their_share(dev, D, Hq, Hkv, n):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("n", [90])
+@pytest.mark.parametrize("n", [1, 4, 90])
 @pytest.mark.parametrize("causal", [True, False])
 def test_value_scales_of_all_sizes_in_any_order(dev, D, n, causal):
     kv, qs, page, Hq, Hkv = [700, 130], [n, min(n, 3)], 64, 4, 2
