@@ -129,7 +129,8 @@ def kv4_attention_workspace_bytes(requests: int, max_q: int, q_heads: int, kv_he
 def kv4_attention_workspace(requests: int, max_q: int, q_heads: int, cache: KV4Cache,
                             table_width: int) -> torch.Tensor:
     """A zero-filled workspace for kv4_attention_into with these sizes (calls
-    leave its counters at zero; calls that overlap in time must not share one)."""
+    leave its counters at zero; calls that overlap in time must not share one).
+    Filled on the current stream: a first call on another has to wait for it."""
     n = kv4_attention_workspace_bytes(requests, max_q, q_heads, cache.kv_heads, cache.head_dim, cache.page_size,
                                       table_width)
     return torch.zeros(max(256, n), dtype=torch.uint8, device=cache.device)

@@ -121,9 +121,9 @@ class AttentionBlock:
     for up to `tokens` tokens of up to `requests` requests at a time.  x is the
     output of the block before (the residual update and its norm are one kernel
     with the quantization for the qkv linear); `out` is this one's, for the block
-    after to add.  Buffers are allocated once; `run` allocates nothing and can be
-    captured into a graph, lengths and slots being device tensors
-    (kv4_assign_into).
+    after to add.  Buffers are allocated once, and ready for any stream when the
+    constructor returns; `run` allocates nothing and can be captured into a graph,
+    lengths and slots being device tensors (kv4_assign_into).
     """
 
     def __init__(self, w_norm: torch.Tensor, qkv: _lib.PackedLinear, o_proj: _lib.PackedLinear, q_heads: int,
@@ -146,6 +146,9 @@ class AttentionBlock:
         self.ws_qkv = _lib.small_m_workspace(tokens, qkv, dev) if self.few else None
         self.ws_o = _lib.linear_workspace(tokens, o_proj, dev)
         self.ws_att = kv4.kv4_attention_workspace(requests, max_q, q_heads, cache, table_width)
+        # the fills above went to the current stream, and `run` may be given any: its kernels' counters start at zero
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()
 
     def run(self, r: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, cu_q: torch.Tensor,
             slots: torch.Tensor, positions: torch.Tensor, x: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
