@@ -186,15 +186,15 @@ class PackedLinear:
     s_w8: torch.Tensor  # fp16 [G, N8p]
     idx8: torch.Tensor  # int32 [N8]
 
+    def buffers(self):
+        return self.W4, self.z4, self.s_w4, self.idx4, self.W8, self.s_w8, self.idx8
+
     def nbytes(self) -> int:
-        return sum(t.numel() * t.element_size() for t in
-                   (self.W4, self.z4, self.s_w4, self.idx4, self.W8, self.s_w8, self.idx8))
+        return sum(t.numel() * t.element_size() for t in self.buffers())
 
     def to(self, device) -> "PackedLinear":
         """The same packed layer with every buffer on `device` (a copy)."""
-        return PackedLinear(self.N, self.K, self.N4, self.N8,
-                            *(t.to(device).contiguous() for t in
-                              (self.W4, self.z4, self.s_w4, self.idx4, self.W8, self.s_w8, self.idx8)))
+        return PackedLinear(self.N, self.K, self.N4, self.N8, *(t.to(device).contiguous() for t in self.buffers()))
 
 
 def padded(n: int) -> int:

@@ -134,6 +134,8 @@ class AttentionBlock:
         _lib._require(o_proj.K == q_heads * D and o_proj.N == qkv.K, "o_proj must lead from the heads to qkv's inputs")
         _lib._require(tokens > 0, "need room for at least one token")
         dev = cache.device
+        _lib._require(all(t.device == dev for p in (qkv, o_proj) for t in p.buffers()),
+                      f"the packed linears must be on the cache's device, {dev}")
         self.w_norm, self.qkv, self.o_proj, self.cache, self.rope, self.eps = w_norm, qkv, o_proj, cache, rope, eps
         self.q_heads, self.tokens, self.max_q = q_heads, tokens, max_q
         self.A_q = torch.empty((tokens, qkv.K), dtype=torch.int8, device=dev)
