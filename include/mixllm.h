@@ -517,7 +517,7 @@ MIXLLM_API mixllm_status mixllm_residual_norm(const void *r, int64_t r_stride, i
  *   codes  uint8  [pages, 2, H, page_size, D/2]  keys then values; byte i of a
  *          row holds the code of channel 2i (low nibble) and 2i + 1 (high)
  *   meta   uint32 [pages, 2, H, page_size]       low half: the row's fp16 scale
- *          s; bits 16..19: its zero point z
+ *          s; bits 16..19: its zero point z; the bits above are not read
  * both 16-byte aligned; a row's values are s * (code - z).  A row (one token,
  * head, key or value) is quantized like the weights' 4-bit set:
  *   lo = min(0, min x), hi = max(0, max x), s = fp16((hi - lo) / 15),

@@ -232,7 +232,8 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-// A row's scale, and its zero point as the subnormal z 2^-24.
+// A row's scale, and its zero point as the subnormal z 2^-24 (the bits above it left out).
+constexpr uint32_t kKvMetaBits = 0x000FFFFFu;
 __device__ __forceinline__ float2 meta_pair(uint32_t m) { return __half22float2(*reinterpret_cast<const __half2 *>(&m)); }
 // Pairs of codes as fp16: low nibbles as n 2^-10, high ones as n 2^-20.
 __device__ __forceinline__ uint32_t low_codes(uint32_t w) {
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
           *reinterpret_cast<uint2 *>(kb) = *reinterpret_cast<const uint2 *>(kr + 8 * C::kRowBytes);
         }
         const uint32_t *km = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes) + 16 * x + row_a;
-        const float2 ma = meta_pair(km[0]), mb = meta_pair(km[8]);
+        const float2 ma = meta_pair(km[0] & kKvMetaBits), mb = meta_pair(km[8] & kKvMetaBits);
         sv[x][0] = meta_pair(km[32]).x;
         sv[x][1] = meta_pair(km[40]).x;
         float lo[NT][4], hi[NT][4];
