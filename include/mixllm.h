@@ -614,12 +614,15 @@ MIXLLM_API mixllm_status mixllm_kv4_attention_workspace_bytes(int64_t requests, 
  * cu_q[b+1] - cu_q[b]) stands at position seq_lens[b] - n + i and sees the
  * tokens up to its own position (causal != 0) or all seq_lens[b] of them:
  *   out[i, h] = sum_t softmax_t(scale * q[i, h] . k[t, h / g]) v[t, h / g],
- * g = q_heads / kv_heads.  Scores, softmax statistics and sums are fp32; the
- * probabilities, times the values' scales, are rounded once to fp16 for the
- * tensor cores: to 11 bits, or where such a weight is below 2^-21 of the
- * largest of its row, by at most 2^-32 of that.  Tokens that a query does not
- * see have no part in it.  A query that sees no token gets zeros (and lse
- * -infinity).
+ * g = q_heads / kv_heads.  Scores, softmax statistics and sums are fp32.  With
+ * at most 16 rows (max_q * g) per key head a score is taken as
+ * s (sum q code - z sum q): its error goes by those sums' terms, of up to 15 |q|
+ * (in all at most s |scale| (D 2^-18 max |q| + (D + 16) 2^-19 sum |q|)), and not by
+ * the score, which may be far smaller.  The probabilities, times the values'
+ * scales, are rounded once to fp16 for the tensor cores: to 11 bits, or where
+ * such a weight is below 2^-21 of the largest of its row, by at most 2^-32 of
+ * that.  Tokens that a query does not see have no part in it.  A query that sees
+ * no token gets zeros (and lse -infinity).
  * Only the first ceil(seq_lens[b] / page_size) entries of a request's row of
  * the table are read.  Rows of q and out outside every request are neither read
  * nor written.
