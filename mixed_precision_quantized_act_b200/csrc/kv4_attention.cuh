@@ -452,14 +452,13 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
   bool in_registers = false;  // the last segment's part, cut at one of the warp's ends
   for (KvWalk w = w0; w.left > 0; w.next(a, kRows)) {
     const int rows = w.r.n * group;
-    constexpr int row0 = 0;
     // ---- the query rows' B fragments, channels permuted as the keys' nibbles, and their sums
     uint32_t qf[NT][kWords * 4];
     float qs[NT][2];
     int lim[NT][2];  // keys seen by columns 2t and 2t + 1
 #pragma unroll
     for (int ni = 0; ni < NT; ++ni) {
-      const int r = row0 + ni * 8 + g;
+      const int r = ni * 8 + g;
       const __half *src = nullptr;
       if (r < rows) {
         const int tok = r / group;
@@ -486,13 +485,13 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         qs[ni][j] = __shfl_sync(0xFFFFFFFFu, sum, (2 * t + j) * 4) * 0x1p14f;  // meets z 2^-24
-        const int rj = row0 + ni * 8 + 2 * t + j;
+        const int rj = ni * 8 + 2 * t + j;
         lim[ni][j] = a.causal && rj < rows ? w.r.kv - w.r.n + rj / group + 1 : w.r.kv;
       }
     }
-    // keys seen by the tile's first row (the fewest) and last row (the most)
-    const int lim_min = a.causal ? w.r.kv - w.r.n + row0 / group + 1 : w.r.kv;
-    const int last_row = min(rows, row0 + kRows) - 1;
+    // keys seen by the first row (the fewest) and the last one (the most)
+    const int lim_min = a.causal ? w.r.kv - w.r.n + 1 : w.r.kv;
+    const int last_row = min(rows, kRows) - 1;
     const int lim_max = a.causal ? w.r.kv - w.r.n + last_row / group + 1 : w.r.kv;
 
     S = 0x1p-24f;
@@ -695,7 +694,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::kThreads, 1) kv4_decode_kernel(c
       for (int ni = 0; ni < NT; ++ni)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int r = row0 + ni * 8 + 2 * t + j;
+          const int r = ni * 8 + 2 * t + j;
           if (r >= rows) continue;
           const int tok = r / group, head = w.h * group + r - tok * group;
           const int64_t token = static_cast<int64_t>(w.r.q0) + tok;

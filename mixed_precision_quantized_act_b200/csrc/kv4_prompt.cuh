@@ -795,7 +795,7 @@ static cudaError_t launch_kv4_prompt(const AttendArgs &a, void *ws, cudaStream_t
 // ---------------------------------------------------------------------------
 static bool kv4_is_decode(int max_q, int group) { return static_cast<int64_t>(max_q) * group <= 16; }
 
-size_t kv4_attention_workspace_bytes(int B, int max_q, int Hq, int H, int D, int, int) {
+size_t kv4_attention_workspace_bytes(int B, int max_q, int Hq, int H, int D) {
   return kv4_is_decode(max_q, Hq / H) ? kv4_decode_workspace_bytes(max_q, Hq / H, D)
                                       : kv4_prompt_workspace_bytes(B, max_q, Hq / H, D);
 }

@@ -179,7 +179,7 @@ struct AttendArgs {
   int64_t out_stride;
   float *lse;  // [T][Hq], or null
 };
-size_t kv4_attention_workspace_bytes(int B, int max_q, int Hq, int H, int D, int page_log2, int W);
+size_t kv4_attention_workspace_bytes(int B, int max_q, int Hq, int H, int D);
 cudaError_t launch_kv4_attention(const AttendArgs &a, void *ws, cudaStream_t stream, const char **msg);
 
 int64_t padded_channels(int64_t n);  // n rounded up to a multiple of 256

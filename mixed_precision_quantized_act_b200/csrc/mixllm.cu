@@ -730,7 +730,7 @@ mixllm_status mixllm_kv4_attention_workspace_bytes(int64_t requests, int64_t max
   if (st == MIXLLM_OK) st = check_kv4_heads(requests, max_q, q_heads, table_width, cache);
   if (st != MIXLLM_OK) return st;
   *bytes = mixllm::kv4_attention_workspace_bytes(static_cast<int>(requests), static_cast<int>(max_q), q_heads,
-                                                 kv_heads, head_dim, cache.page_log2, static_cast<int>(table_width));
+                                                 kv_heads, head_dim);
   return ok();
 }
 
@@ -759,8 +759,7 @@ mixllm_status mixllm_kv4_attention(const void *q_f16, int64_t q_stride, int64_t 
   if (n_tokens > 1 && out_stride < static_cast<int64_t>(q_heads) * head_dim)
     return fail(MIXLLM_ERR_INVALID_ARG, "rows of out overlap");
   const size_t need = mixllm::kv4_attention_workspace_bytes(static_cast<int>(requests), static_cast<int>(max_q),
-                                                            q_heads, kv_heads, head_dim, cache.page_log2,
-                                                            static_cast<int>(table_width));
+                                                            q_heads, kv_heads, head_dim);
   if (workspace_bytes < need)
     return fail(MIXLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu this shape needs",
                 workspace_bytes, need);
