@@ -36,10 +36,13 @@ namespace mixllm {
 // S^T = K Q^T with K as the A operand, then O^T = V^T P^T with V^T as A.
 //
 // Measured on B200 (as a CUDA graph): 64 requests of 100 to 8100 tokens, 32 query
-// and 8 key heads of 128: 83.7 us, 3.4 TB/s; 4 requests of 100000 to 131071
-// tokens, 64 and 8 heads: 119 us, 4.3 TB/s (66 % of the measured copy rate);
+// and 8 key heads of 128: 84.0 us, 3.4 TB/s; 4 requests of 100000 to 131071
+// tokens, 64 and 8 heads: 120 us, 4.3 TB/s (65 % of the measured copy rate);
 // one request of 1003 tokens: 11.6 us.  With the products left out the second
-// takes 96 us, with the loads left out 114: neither hides the other wholly.
+// took 96 us, with the loads left out 114: neither hides the other wholly.
+// Above 128 requests a warp no longer holds all their lengths, and the walk to its
+// first unit is a chain of loads: 262144 tokens as 128 requests take 83 us, as 256
+// 92, as 1024 105.
 //
 // What bounds the loop on the way to HBM speed is the unpacking: integer
 // instructions issue at half rate.  So one AND per pair of codes makes fp16

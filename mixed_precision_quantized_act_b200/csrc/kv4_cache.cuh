@@ -161,9 +161,10 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const Assign
 // finite.  HBM-bound: reads 2 bytes and writes 0.5 (keys, values) or 2
 // (queries) a channel.  A lane takes `per` heads of its token, so that the
 // table's 8 bytes a channel are read once for all of them, and loads four heads
-// ahead: with the read-back below, 4099 tokens of 64 + 16 heads of 128 took
-// 54 us on B200 (one head at a time 78 us).  Its integer and conversion
-// instructions, not HBM, bound it there (27 us of traffic).
+// ahead: 4099 tokens of 64 + 16 heads of 128 took 44 us on B200, and 8 us to read
+// back (both with one head at a time 78 us), for 27 us of traffic.  No unit is
+// full there (issue slots 61 %, DRAM 34 %): 64 registers leave 32 warps an SM, which
+// wait for their loads and, row by row, for a chain of shuffles and divisions.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 

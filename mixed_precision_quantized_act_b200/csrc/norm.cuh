@@ -80,7 +80,9 @@ __device__ __forceinline__ void store8_rounded(float *p, float (&f)[8]) {
 // the block adds the threads' sums as a tree.  Without x, r' = r.
 // HBM-bound: 2 + 2 |r| bytes a channel and 2 (y), 1 (codes) or both out; with an
 // fp32 residual, a gate and both norms, 1024 x 8192 took 20.6 us, 4.9 TB/s on
-// B200 (75 % of the measured copy rate).  Threads hold one run up to 4096
+// B200 (75 % of the measured copy rate): two blocks of 512 threads fit an SM, and a
+// row's loads, its two block-wide sums and its stores come one after the other.
+// Threads hold one run up to 4096
 // channels and two up to 16384, which keeps every load of a row in registers.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void widen8(const uint4 raw, float (&f)[8]) {
