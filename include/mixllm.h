@@ -653,6 +653,165 @@ MIXLLM_API mixllm_status mixllm_kv4_attention(const void *q_f16, int64_t q_strid
                                               size_t workspace_bytes, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The 8-bit operators of a decoder layer: linears in 8-bit integers, the norms
+ * of query and key heads, and a paged KV cache in 8 bits.  They stand beside
+ * the 4-bit ones above and take and give the same fp16 activations, slots,
+ * positions and block tables.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * One scale per row: s = amax / 127 (fp32, IEEE division), codes
+ * clamp(rne(x / s), -127, 127) with x / s the IEEE fp32 quotient; a row of
+ * zeros gets s = 0 and codes 0, a row with a NaN or an infinity s = NaN and codes
+ * 0 (its outputs are NaN).
+ *   mixllm_w8a8_pack      W fp32 [N, K] -> codes int8 [N, K], s_w fp32 [N]
+ *   mixllm_w8a8_quantize  X fp16 [M, K], rows x_stride elements apart -> A_q
+ *                         int8 [M, K], s_a fp32 [M]
+ * Device buffers, 16-byte aligned (scales 4); K a positive multiple of 16 up to
+ * 131056 (a row of products of any codes then fits int32), x_stride a multiple
+ * of 8.
+ * No rows is a no-op.  Asynchronous on `stream`.
+ */
+MIXLLM_API mixllm_status mixllm_w8a8_pack(const float *W, int64_t N, int64_t K, int8_t *codes, float *s_w,
+                                          void *stream);
+MIXLLM_API mixllm_status mixllm_w8a8_quantize(const void *X_f16, int64_t x_stride, int64_t M, int64_t K, int8_t *A_q,
+                                              float *s_a, void *stream);
+
+/*
+ * Bytes of workspace that mixllm_w8a8_gemm (from_f16 = 0) or mixllm_w8a8_linear
+ * (from_f16 = 1) need, in *bytes (0 for an empty product).  Pure host function.
+ */
+MIXLLM_API mixllm_status mixllm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t from_f16, size_t *bytes);
+
+/*
+ * The linear layer in 8-bit integers:
+ *   P[m, n] = sum_k A_q[m, k] W[n, k]                   (int32, exact)
+ *   Y[m, n] = fp16(float(P) * s_a[m] * s_w[n] + bias[n])  (fp32, in this order;
+ *             the last product and the sum are one FMA)
+ * mixllm_w8a8_linear quantizes X first, like mixllm_w8a8_quantize (two launches,
+ * the product's prologue and first weight copies overlapping the quantizer).
+ *   A_q, s_a   device, int8 [M, K] and fp32 [M]
+ *   X_f16      device, fp16 [M, K], rows x_stride apart (a multiple of 8)
+ *   W, s_w     device, int8 [N, K] and fp32 [N], as of mixllm_w8a8_pack; codes of
+ *              -128 are allowed
+ *   bias_f16   device, fp16 [N], or NULL
+ *   Y_f16      device, fp16 [M, N] contiguous; overlaps no input
+ *   workspace  device, at least mixllm_w8a8_workspace_bytes() bytes, 256-byte
+ *              aligned, zero-filled before its first use; calls leave its
+ *              counters (the first 4096 bytes) at zero, so it stays ready for
+ *              calls of any sizes it is large enough for.  Two calls that run at
+ *              the same time must not share one.  After MIXLLM_ERR_TIMEOUT zero
+ *              it again.
+ * A_q, X and W 16-byte aligned, s_a and s_w 4, bias and Y 2.  Any M and N; K as
+ * above.  The result does not depend on timing.  Asynchronous on `stream`.
+ */
+MIXLLM_API mixllm_status mixllm_w8a8_gemm(const int8_t *A_q, const float *s_a, int64_t M, int64_t K, const int8_t *W,
+                                          const float *s_w, int64_t N, const void *bias_f16, void *Y_f16,
+                                          void *workspace, size_t workspace_bytes, void *stream);
+MIXLLM_API mixllm_status mixllm_w8a8_linear(const void *X_f16, int64_t x_stride, int64_t M, int64_t K,
+                                            const int8_t *W, const float *s_w, int64_t N, const void *bias_f16,
+                                            void *Y_f16, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * RMS norms of query and key heads, each over its own head_dim channels, and the
+ * rotation by position, in one pass:
+ *   y = x * rsqrt(mean(x^2) + eps) * w     (w NULL: y = x)
+ *   y_i cos_i - y_j sin_i,  y_j cos_i + y_i sin_i   for j = i + rotary/2 < rotary
+ * in fp32, rounded to fp16 once.  Without a norm the rotation is
+ * mixllm_kv4_append's, bit for bit.
+ *   q, q_out   device fp16, token t's heads contiguous at t * stride
+ *              ([n_tokens, q_heads, head_dim]); q_out may be q; q_heads may be 0
+ *   k, k_out   the same for the kv_heads key heads, which may be 0
+ *   w_q, w_k   device fp16 [head_dim], or NULL
+ *   positions, rope, max_pos, rotary   as of mixllm_kv4_append (rotary = 0: no
+ *              rotation).  A token with a negative position is left alone, one
+ *              beyond the table too and recorded (MIXLLM_ERR_BOUNDS).
+ * head_dim 64, 128 or 256.  q, k, outputs, weights and rope 16-byte aligned,
+ * strides (in elements) multiples of 8.  Asynchronous on `stream`.
+ */
+MIXLLM_API mixllm_status mixllm_head_norm_rope(const void *q_f16, int64_t q_stride, int32_t q_heads, void *q_out_f16,
+                                               int64_t q_out_stride, const void *w_q_f16, const void *k_f16,
+                                               int64_t k_stride, int32_t kv_heads, void *k_out_f16,
+                                               int64_t k_out_stride, const void *w_k_f16, int64_t n_tokens,
+                                               int32_t head_dim, float eps, const int32_t *positions,
+                                               const float *rope, int64_t max_pos, int32_t rotary, void *stream);
+
+/*
+ * The paged 8-bit KV cache.  Two buffers of `pages` pages of page_size tokens
+ * (16, 32, 64, 128 or 256), H = kv_heads, D = head_dim (64 or 128):
+ *   codes   uint8 [pages, 2, H, page_size, D]        keys then values
+ *   scales  fp32  [pages, 2, H, page_size / 16]      one for each block of 16
+ *           tokens of a head, keys and values apart
+ * both 16-byte aligned; a block's values are s * (code - 128).  Slots are those
+ * of the 4-bit cache (page * page_size + row), assigned by mixllm_kv4_assign.
+ * Page numbers, slots, positions and lengths out of range are skipped and
+ * recorded as there.
+ */
+
+/*
+ * Writes the keys and values of n_slots tokens into their slots and, on the way,
+ * normalizes and rotates keys and queries like mixllm_head_norm_rope (one
+ * kernel).  For every block of 16 tokens, head and kind that gets new rows:
+ *   s     = max(s before, amax / 127) over the new rows, where s before is 0 if
+ *           the block's first row is among them, else the block's scale
+ *   code  = 128 + clamp(rne(x / s), -127, 127)   (128 where s = 0)
+ * and where s has grown, the block's other rows are re-coded:
+ *   code' = 128 + clamp(rne((code - 128) * (s before / s)), -127, 127)
+ * (fp32, IEEE).  Older rows are those of a sequence that is written in order:
+ * a block's first row starts it anew.  A NaN or an infinity in a row makes its
+ * block's scale NaN, and with it all of the block's tokens, until the block's
+ * first row is written again.
+ *   slots     device int64 [n_slots], distinct; a negative one skips the token
+ *             (its q_out row too).  The tokens of one block stand one behind
+ *             the other (as mixllm_kv4_assign lists them).
+ *   k, v      device fp16 [n_slots, kv_heads, head_dim], tokens stride apart
+ *   q, q_out  device fp16 [n_slots, q_heads, head_dim] likewise; q_heads = 0:
+ *             none.  q_out may be q.
+ *   w_q, w_k  device fp16 [head_dim], or NULL: no norm
+ *   positions, rope, max_pos, rotary   as of mixllm_kv4_append; a token whose
+ *             position is out of range is skipped and recorded
+ * Alignment and strides as there.  n_slots = 0 is a no-op.  Asynchronous.
+ */
+MIXLLM_API mixllm_status mixllm_kv8_append(uint8_t *codes, float *scales, int64_t pages, int32_t kv_heads,
+                                           int32_t head_dim, int32_t page_size, const int64_t *slots,
+                                           int64_t n_slots, const void *k_f16, int64_t k_stride, const void *v_f16,
+                                           int64_t v_stride, const void *q_f16, int64_t q_stride, int32_t q_heads,
+                                           void *q_out_f16, int64_t q_out_stride, const void *w_q_f16,
+                                           const void *w_k_f16, float eps, const int32_t *positions,
+                                           const float *rope, int64_t max_pos, int32_t rotary, void *stream);
+
+/*
+ * The cached keys and values of n_slots slots as fp16 [n_slots, kv_heads,
+ * head_dim] each, contiguous and 16-byte aligned: s * (code - 128) rounded once,
+ * within +-65504.  A negative slot leaves its rows as they were.  Asynchronous.
+ */
+MIXLLM_API mixllm_status mixllm_kv8_read(const uint8_t *codes, const float *scales, int64_t pages, int32_t kv_heads,
+                                         int32_t head_dim, int32_t page_size, const int64_t *slots, int64_t n_slots,
+                                         void *k_f16, void *v_f16, void *stream);
+
+/*
+ * Attention of ragged queries over the 8-bit cache: mixllm_kv4_attention's
+ * definition, arguments, workspace rules and limits, with this cache's values.
+ * Scores, softmax statistics and sums are fp32.  The probabilities, times the
+ * values' scales, are rounded once to fp16 for the tensor cores: to 11 bits, or
+ * where such a weight is below 2^-21 of the largest of its row, by at most 2^-32
+ * of that.
+ */
+MIXLLM_API mixllm_status mixllm_kv8_attention_workspace_bytes(int64_t requests, int64_t max_q, int32_t q_heads,
+                                                              int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                                                              int64_t table_width, size_t *bytes);
+MIXLLM_API mixllm_status mixllm_kv8_attention(const void *q_f16, int64_t q_stride, int64_t n_tokens, int32_t q_heads,
+                                              const uint8_t *codes, const float *scales, int64_t pages,
+                                              int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                                              const int32_t *block_table, int64_t table_stride, int64_t table_width,
+                                              const int32_t *seq_lens, const int32_t *cu_q, int64_t requests,
+                                              int64_t max_q, float scale, int32_t causal, void *out_f16,
+                                              int64_t out_stride, float *lse, void *workspace,
+                                              size_t workspace_bytes, void *stream);
+
+/*
  * Waits for `stream`, then reads and clears the device status word of the
  * current device.  Returns MIXLLM_ERR_TIMEOUT if a kernel of this library
  * gave up a wait since the last call, MIXLLM_ERR_BOUNDS if a KV-cache kernel

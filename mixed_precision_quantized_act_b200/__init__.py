@@ -55,10 +55,32 @@ from .kv4 import (  # noqa: F401
     kv4_read_into,
     rope_table,
 )
+from .kv8 import (  # noqa: F401
+    KV8Cache,
+    kv8_append_into,
+    kv8_attention,
+    kv8_attention_into,
+    kv8_attention_workspace,
+    kv8_attention_workspace_bytes,
+    kv8_cache,
+    kv8_read_into,
+)
 from .norm import (  # noqa: F401
     dequantize_act,
     dequantize_act_into,
+    head_norm_rope_into,
     residual_norm_into,
     residual_norm_quantize_into,
 )
 from .packfile import load_packed, save_packed  # noqa: F401
+from .w8a8 import (  # noqa: F401
+    W8Weights,
+    w8a8_gemm_into,
+    w8a8_linear,
+    w8a8_linear_into,
+    w8a8_linear_workspace,
+    w8a8_pack,
+    w8a8_quantize,
+    w8a8_quantize_into,
+    w8a8_workspace_bytes,
+)

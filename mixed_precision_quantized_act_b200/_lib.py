@@ -73,6 +73,21 @@ SIGNATURES = {
     "mixllm_kv4_attention": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _i64,
                                             _vp, _vp, _i64, _i64, _f32, _i32, _vp, _i64, _vp, _vp, ctypes.c_size_t,
                                             _vp]),
+    "mixllm_w8a8_pack": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "mixllm_w8a8_quantize": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "mixllm_w8a8_workspace_bytes": (ctypes.c_int, [_i64, _i64, _i64, _i32, ctypes.POINTER(ctypes.c_size_t)]),
+    "mixllm_w8a8_gemm": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "mixllm_w8a8_linear": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "mixllm_head_norm_rope": (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64,
+                                             _i32, _f32, _vp, _vp, _i64, _i32, _vp]),
+    "mixllm_kv8_append": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                         _i32, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _i64, _i32, _vp]),
+    "mixllm_kv8_read": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp]),
+    "mixllm_kv8_attention_workspace_bytes": (ctypes.c_int, [_i64, _i64, _i32, _i32, _i32, _i32, _i64,
+                                                            ctypes.POINTER(ctypes.c_size_t)]),
+    "mixllm_kv8_attention": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _i64,
+                                            _vp, _vp, _i64, _i64, _f32, _i32, _vp, _i64, _vp, _vp, ctypes.c_size_t,
+                                            _vp]),
     "mixllm_sync_status": (ctypes.c_int, [_vp]),
     "mixllm_selftest_wait_timeout": (ctypes.c_int, [_u32, _vp]),
     "mixllm_checked_build": (ctypes.c_int, []),

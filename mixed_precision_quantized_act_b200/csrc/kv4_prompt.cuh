@@ -99,7 +99,8 @@ struct PmPlan {
 
 constexpr int kPmPlanThreads = 1024;
 
-__global__ void __launch_bounds__(kPmPlanThreads) kv4_prompt_plan_kernel(const AttendArgs a, const PmPlan plan) {
+template <typename A>
+__global__ void __launch_bounds__(kPmPlanThreads) kv4_prompt_plan_kernel(const A a, const PmPlan plan) {
   extern __shared__ int pair_base[];  // pairs before each request
   pdl_launch_dependents();
   __shared__ long long warp_sum[32];
@@ -160,7 +161,8 @@ struct PmWalk {
   int64_t seg_first;  // unit index of the whole segment's first tile
   int q0, n, kv;
 
-  __device__ __forceinline__ void load(const AttendArgs &a, const PmPlan &plan) {
+  template <typename A>
+  __device__ __forceinline__ void load(const A &a, const PmPlan &plan) {
     const int2 v = plan.ent[e];
     b = v.x, pair = v.y;
     tiles = static_cast<int>(plan.cum[e + 1] - plan.cum[e]);
@@ -168,7 +170,8 @@ struct PmWalk {
     n = a.cu_q[b + 1] - q0;
     kv = a.kv_lens[b];
   }
-  __device__ __forceinline__ void next(const AttendArgs &a, const PmPlan &plan) {
+  template <typename A>
+  __device__ __forceinline__ void next(const A &a, const PmPlan &plan) {
     left -= count;
     seg_first += tiles;
     tile = 0;
@@ -195,8 +198,47 @@ __device__ __forceinline__ uint4 unpack_codes(uint32_t w, uint32_t zlo, uint32_t
   return r;
 }
 
+// What the prompt kernel knows of the 4-bit format: a row's codes and word of
+// metadata, the scale in it, and its codes as fp16 rows of an operand (128 bytes
+// a panel, swizzled), in an order of each eight channels that Q's copy and the
+// output's undo share (order(), place()).
 template <int D>
-__global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendArgs a, const PmPlan plan,
+struct Pm4 {
+  using Args = AttendArgs;
+  static constexpr int kVec = D / 32;  // 16-byte loads of a row's codes
+  static constexpr int kIssueRegs = 64, kUnpackRegs = 96;  // of a thread; with 2 x 176 of the softmax, 4 x 128
+  static __device__ __forceinline__ uint32_t load(const Kv4Cache &c, int64_t r, uint4 (&codes)[kVec]) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(c.codes + r * (D / 2));
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) codes[i] = src[i];
+    return c.meta[r];
+  }
+  static __device__ __forceinline__ float scale(uint32_t meta) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&meta)).x;
+  }
+  // chunk k (eight channels) of the row goes to put(k, eight fp16 values)
+  template <typename Put>
+  static __device__ __forceinline__ void unpack(const uint4 (&codes)[kVec], uint32_t meta, const Put &put) {
+    const uint32_t z = meta >> 16 & 15u;
+    const uint32_t zlo = 0xE400E400u | z * 0x00010001u, zhi = 0xD400D400u | z * 0x00100010u;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const uint32_t words[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) put(4 * i + j, unpack_codes(words[j], zlo, zhi));
+    }
+  }
+  // eight channels in order -> 0 4 1 5 2 6 3 7
+  static __device__ __forceinline__ uint4 order(const uint4 v) {
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                      __byte_perm(v.y, v.w, 0x7632));
+  }
+  // where channel x of eight stands
+  static __host__ __device__ constexpr int place(int x) { return x < 4 ? 2 * x : 2 * x - 7; }
+};
+
+template <typename F, int D>
+__global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typename F::Args a, const PmPlan plan,
                                                                  float *parts) {
   using C = PmCfg<D>;
   constexpr int kPanel = C::kPanel, kOperand = C::kOperand;
@@ -274,7 +316,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
 
   if (warp < 4) {
     // ------------------------------------------------------------ products
-    regs_dec<64>();
+    regs_dec<F::kIssueRegs>();
     if (warp == 0) {
       // The whole warp walks and waits; one elected lane issues.  (With the
       // walk itself inside a one-lane branch a product cost about 300 clocks to
@@ -351,12 +393,12 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
     __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------ unpacking: thread = token of the tile
-    regs_dec<96>();
+    regs_dec<F::kUnpackRegs>();
     const int tk = tid - 128;
     const float scale2 = a.scale * 1.4426950408889634f;
     const int page_log2 = a.cache.page_log2;
     const int64_t to_value = static_cast<int64_t>(H) << page_log2;
-    constexpr int kVec = D / 32;  // 16-byte loads of a row's codes
+    constexpr int kVec = F::kVec;  // 16-byte loads of a row's codes
     PmWalk n = w;  // one unit ahead of w
     int left = w.left;
     uint4 kr[kVec], vr[kVec];
@@ -380,27 +422,13 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       meta = 0;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) codes[i] = make_uint4(0, 0, 0, 0);
-      if (r >= 0) {
-        meta = a.cache.meta[r];
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.cache.codes + r * (D / 2));
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) codes[i] = src[i];
-      }
+      if (r >= 0) meta = F::load(a.cache, r, codes);
     };
     const auto store = [&](uint8_t *to, const uint4 (&codes)[kVec], uint32_t meta) {
-      const uint32_t z = meta >> 16 & 15u;
-      const uint32_t zlo = 0xE400E400u | z * 0x00010001u, zhi = 0xD400D400u | z * 0x00100010u;
       uint8_t *line = to + tk * 128;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const uint32_t words[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int chunk = 4 * i + j;
-          *reinterpret_cast<uint4 *>(line + (chunk >> 3) * kPanel + (((chunk & 7) ^ (tk & 7)) << 4)) =
-              unpack_codes(words[j], zlo, zhi);
-        }
-      }
+      F::unpack(codes, meta, [&](int chunk, const uint4 v) {
+        *reinterpret_cast<uint4 *>(line + (chunk >> 3) * kPanel + (((chunk & 7) ^ (tk & 7)) << 4)) = v;
+      });
       fence_proxy_async_smem();
     };
     look_up();
@@ -426,11 +454,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
       if (!mbar_wait(&k_empty[s], phase ^ 1, &abort_flag)) break;
       const int at = it & (kPmScaleRing - 1);
       {
-        const float2 ks = __half22float2(*reinterpret_cast<const __half2 *>(&km));
-        const float2 vs = __half22float2(*reinterpret_cast<const __half2 *>(&vm));
-        k_scale[at * kPmTile + tk] = ks.x * scale2;
-        v_scale[at * kPmTile + tk] = vs.x;
-        v_log[at * kPmTile + tk] = __log2f(fmaxf(vs.x, 0x1p-24f));
+        const float vs = F::scale(vm);
+        k_scale[at * kPmTile + tk] = F::scale(km) * scale2;
+        v_scale[at * kPmTile + tk] = vs;
+        v_log[at * kPmTile + tk] = __log2f(fmaxf(vs, 0x1p-24f));
         const uint32_t bits = __ballot_sync(0xFFFFFFFFu, ok_now);
         if (lane == 0) seen[at][warp - 4] = bits;
       }
@@ -476,8 +503,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
           v = *reinterpret_cast<const uint4 *>(a.q + (static_cast<int64_t>(w.q0) + tok2) * a.q_stride +
                                                static_cast<int64_t>(w.h * group + head2) * D + chunk * 8);
         *reinterpret_cast<uint4 *>(tile_s + rr * 128 + (chunk >> 3) * kPanel + (((chunk & 7) ^ (rr & 7)) << 4)) =
-            make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                       __byte_perm(v.y, v.w, 0x7632));
+            F::order(v);
       }
       fence_proxy_async_smem();
       mbar_arrive(&q_full[i]);
@@ -623,10 +649,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
         tmem_ld_wait();
         reg_fence(o);
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {  // columns 0 4 1 5 2 6 3 7 back in order
+        for (int k = 0; k < 32; k += 8) {  // the format's columns back in order
           float v[8];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(o[k + (x < 4 ? 2 * x : 2 * x - 7)]);
+          for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(o[k + F::place(x)]);
           const int ch = 4 * b + k / 8;
           if (cut) {  // four channels of all rows together: neighbouring rows are neighbouring lanes
             float4 *dst = reinterpret_cast<float4 *>(part) + 2 * ch * kPmRows + i * 128 + r;
@@ -669,8 +695,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const AttendA
 // Joins a cut segment's parts, 32 rows a block: lane = row, a warp an eighth of
 // the channels.  Block x's parts are those of the segment that block x of the
 // kernel before was the first to hold.
-template <int D>
-__global__ void __launch_bounds__(256) kv4_prompt_join_kernel(const AttendArgs a, const PmPlan plan,
+template <int D, typename A>
+__global__ void __launch_bounds__(256) kv4_prompt_join_kernel(const A a, const PmPlan plan,
                                                               const float *__restrict__ parts) {
   pdl_wait();
   using C = PmCfg<D>;
@@ -733,17 +759,18 @@ static size_t kv4_prompt_workspace_bytes(int B, int max_q, int group, int D) {
          static_cast<size_t>(kPmMaxGrid) * 2 * kPmRows * (D + 2) * sizeof(float);
 }
 
-template <int D>
-static cudaError_t launch_kv4_prompt(const AttendArgs &a, void *ws, cudaStream_t stream, const char **msg) {
+template <typename F, int D>
+static cudaError_t launch_kv4_prompt(const typename F::Args &a, void *ws, cudaStream_t stream, const char **msg) {
   using C = PmCfg<D>;
-  auto kern = kv4_prompt_kernel<D>;
+  using A = typename F::Args;
+  auto kern = kv4_prompt_kernel<F, D>;
   static std::atomic<unsigned long long> configured{0};  // one bit per device ordinal
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !(configured.load() & (1ull << dev))) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kv4_prompt_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(kv4_prompt_plan_kernel<A>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                kKv4MaxRequests * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) {
       *msg = "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed";
@@ -765,7 +792,7 @@ static cudaError_t launch_kv4_prompt(const AttendArgs &a, void *ws, cudaStream_t
   int64_t grid = device_sm_count();
   if (grid > kPmMaxGrid) grid = kPmMaxGrid;
   if (grid > units) grid = units;
-  kv4_prompt_plan_kernel<<<1, kPmPlanThreads, a.B * sizeof(int), stream>>>(a, plan);
+  kv4_prompt_plan_kernel<A><<<1, kPmPlanThreads, a.B * sizeof(int), stream>>>(a, plan);
   cudaError_t e = cudaGetLastError();
   // the other two start while the one before them ends, and wait for its results themselves
   cudaLaunchAttribute attr[1];
@@ -782,7 +809,7 @@ static cudaError_t launch_kv4_prompt(const AttendArgs &a, void *ws, cudaStream_t
   cfg.gridDim = dim3(static_cast<unsigned>(grid), kPmRows / 32);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kv4_prompt_join_kernel<D>, a, plan, static_cast<const float *>(parts));
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kv4_prompt_join_kernel<D, A>, a, plan, static_cast<const float *>(parts));
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) *msg = "launch of the prompt attention failed";
   return e;
@@ -802,7 +829,8 @@ size_t kv4_attention_workspace_bytes(int B, int max_q, int Hq, int H, int D) {
 
 cudaError_t launch_kv4_attention(const AttendArgs &a, void *ws, cudaStream_t stream, const char **msg) {
   if (kv4_is_decode(a.max_q, a.Hq / a.cache.H)) return launch_kv4_decode(a, ws, stream, msg);
-  return a.cache.D == 128 ? launch_kv4_prompt<128>(a, ws, stream, msg) : launch_kv4_prompt<64>(a, ws, stream, msg);
+  return a.cache.D == 128 ? launch_kv4_prompt<Pm4<128>, 128>(a, ws, stream, msg)
+                          : launch_kv4_prompt<Pm4<64>, 64>(a, ws, stream, msg);
 }
 
 }  // namespace mixllm

@@ -1,6 +1,6 @@
 // kv4_ptx.cuh -- inline-PTX wrappers of the attention kernels: the warp's matrix
 // product and transpose, tcgen05.mma kind::f16 with its descriptors, pairs of
-// floats, the base-2 exponential and logarithm and a copy to a 32-bit shared address.
+// floats, the base-2 exponential and logarithm and copies to a 32-bit shared address.
 #pragma once
 
 #include <cstdint>
@@ -37,6 +37,10 @@ __device__ __forceinline__ float lg2(float x) {
 // 16-byte asynchronous copy global -> shared through L2 only, to a 32-bit shared address.
 __device__ __forceinline__ void cp_async_16_u32(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_4_u32(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
 }
 
 // ----------------------------------------------------------------- pairs of floats

@@ -117,6 +117,26 @@ cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t stream);
 cudaError_t launch_dequantize_act(const int8_t *A_q, const float *s_a, int64_t M, int64_t K, void *X,
                                   cudaStream_t stream);
 
+// The linear layer in 8-bit integers, a scale per token and per channel (w8a8.cuh).
+struct W8A8Args {
+  const int8_t *A_q;
+  const float *s_a;
+  const int8_t *W;
+  const float *s_w;
+  const __half *bias;  // or null
+  __half *Y;
+  int64_t M, N, K;
+  void *ws;
+};
+size_t w8a8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t w8a8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_w8a8_pack(const float *W, int64_t N, int64_t K, int8_t *codes, float *s_w, cudaStream_t stream);
+cudaError_t launch_w8a8_quantize(const __half *X, int64_t stride, int64_t M, int64_t K, int8_t *A_q, float *s_a,
+                                 cudaStream_t stream);
+cudaError_t launch_w8a8_gemm(const W8A8Args &a, cudaStream_t stream, const char **msg);
+// a.A_q and a.s_a are in the workspace
+cudaError_t launch_w8a8_linear(const __half *X, int64_t stride, W8A8Args a, cudaStream_t stream, const char **msg);
+
 // The paged 4-bit KV cache (kv4_cache.cuh) and the attention over it
 // (kv4_attention.cuh).
 constexpr int kKv4MaxRequests = 16384;
@@ -164,8 +184,9 @@ cudaError_t launch_kv4_append(const AppendArgs &a, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4Cache &c, const int64_t *slots, int64_t T, void *k, void *v,
                             cudaStream_t stream);
 
-struct AttendArgs {
-  Kv4Cache cache;
+template <typename Cache>
+struct AttendArgsOf {
+  Cache cache;
   const __half *q;
   int64_t q_stride, T;
   int Hq, B, max_q;
@@ -179,8 +200,43 @@ struct AttendArgs {
   int64_t out_stride;
   float *lse;  // [T][Hq], or null
 };
+using AttendArgs = AttendArgsOf<Kv4Cache>;
 size_t kv4_attention_workspace_bytes(int B, int max_q, int Hq, int H, int D);
 cudaError_t launch_kv4_attention(const AttendArgs &a, void *ws, cudaStream_t stream, const char **msg);
+
+// Norms of query and key heads with the rotation (head_norm.cuh), and the paged
+// 8-bit KV cache (kv8_cache.cuh) with the attention over it (kv8_attention.cuh).
+struct HeadArgs {
+  int64_t T;
+  const __half *q, *k, *v;  // v: the cache's append only
+  int64_t q_stride, k_stride, v_stride;
+  int Hq, H;
+  __half *q_out, *k_out;
+  int64_t q_out_stride, k_out_stride;
+  const __half *w_q, *w_k;  // fp16 [D], or null: no norm
+  const int32_t *positions;
+  const float *rope;  // [max_pos][rotary]: cosines, then sines; or null
+  int64_t max_pos;
+  int rotary;
+  float eps;
+};
+cudaError_t launch_head_norm_rope(const HeadArgs &a, int D, cudaStream_t stream);
+
+struct Kv8Cache {
+  uint8_t *codes;
+  float *scales;
+  int64_t pages;
+  int H, D, page_log2;
+};
+struct Kv8AppendArgs {
+  Kv8Cache cache;
+  const int64_t *slots;
+};
+cudaError_t launch_kv8_append(const Kv8AppendArgs &a, const HeadArgs &heads, cudaStream_t stream);
+cudaError_t launch_kv8_read(const Kv8Cache &c, const int64_t *slots, int64_t T, void *k, void *v, cudaStream_t stream);
+using Attend8Args = AttendArgsOf<Kv8Cache>;
+size_t kv8_attention_workspace_bytes(int B, int max_q, int Hq, int H, int D);
+cudaError_t launch_kv8_attention(const Attend8Args &a, void *ws, cudaStream_t stream, const char **msg);
 
 int64_t padded_channels(int64_t n);  // n rounded up to a multiple of 256
 

@@ -17,10 +17,14 @@
 #include "kv4_attention.cuh"
 #include "kv4_cache.cuh"
 #include "kv4_prompt.cuh"
+#include "head_norm.cuh"
+#include "kv8_attention.cuh"
+#include "kv8_cache.cuh"
 #include "launch.h"
 #include "norm.cuh"
 #include "pack_host.cuh"
 #include "quant.cuh"
+#include "w8a8.cuh"
 
 namespace {
 
@@ -124,8 +128,9 @@ int page_log2_of(int32_t page_size) {
 }
 
 // The cache's shape and buffers (a cache of no pages may have null buffers).
-mixllm_status check_kv4(uint8_t *codes, uint32_t *meta, int64_t pages, int32_t kv_heads, int32_t head_dim,
-                        int32_t page_size, mixllm::Kv4Cache *cache) {
+template <typename Cache, typename Meta>
+mixllm_status check_cache(uint8_t *codes, Meta *meta, int64_t pages, int32_t kv_heads, int32_t head_dim,
+                          int32_t page_size, Cache *cache) {
   const int page_log2 = page_log2_of(page_size);
   if (page_log2 < 0) return fail(MIXLLM_ERR_UNSUPPORTED, "page size %d is not 16, 32, 64, 128 or 256", page_size);
   if (head_dim != 64 && head_dim != 128)
@@ -135,21 +140,139 @@ mixllm_status check_kv4(uint8_t *codes, uint32_t *meta, int64_t pages, int32_t k
   if (pages > 0 && (!codes || !meta)) return fail(MIXLLM_ERR_INVALID_ARG, "null cache buffer");
   if (!aligned(codes, 16) || !aligned(meta, 16))
     return fail(MIXLLM_ERR_INVALID_ARG, "the cache's buffers must be 16-byte aligned");
-  *cache = mixllm::Kv4Cache{codes, meta, pages, kv_heads, head_dim, page_log2};
+  *cache = Cache{codes, meta, pages, kv_heads, head_dim, page_log2};
   return MIXLLM_OK;
 }
 
-mixllm_status check_kv4_heads(int64_t requests, int64_t max_q, int32_t q_heads, int64_t table_width,
-                              const mixllm::Kv4Cache &cache) {
-  if (q_heads < cache.H || q_heads % cache.H != 0 || q_heads > 65536)
-    return fail(MIXLLM_ERR_INVALID_ARG, "%d query heads are no multiple of the %d key heads", q_heads, cache.H);
+mixllm_status check_kv4(uint8_t *codes, uint32_t *meta, int64_t pages, int32_t kv_heads, int32_t head_dim,
+                        int32_t page_size, mixllm::Kv4Cache *cache) {
+  return check_cache(codes, meta, pages, kv_heads, head_dim, page_size, cache);
+}
+
+mixllm_status check_kv_heads(int64_t requests, int64_t max_q, int32_t q_heads, int64_t table_width,
+                              int H, int page_log2) {
+  if (q_heads < H || q_heads % H != 0 || q_heads > 65536)
+    return fail(MIXLLM_ERR_INVALID_ARG, "%d query heads are no multiple of the %d key heads", q_heads, H);
   if (requests < 0 || max_q < 0 || table_width < 0) return fail(MIXLLM_ERR_INVALID_ARG, "negative size");
   if (requests > mixllm::kKv4MaxRequests)
     return fail(MIXLLM_ERR_UNSUPPORTED, "%lld requests are beyond %d", static_cast<long long>(requests),
                 mixllm::kKv4MaxRequests);
-  if (max_q > 0x7FFFFF00 / (q_heads / cache.H) || table_width > 0x7FFFFF00 >> cache.page_log2)
+  if (max_q > 0x7FFFFF00 / (q_heads / H) || table_width > 0x7FFFFF00 >> page_log2)
     return fail(MIXLLM_ERR_INVALID_ARG, "queries or cached tokens of a request beyond the supported 2^31 range");
   return MIXLLM_OK;
+}
+
+// The attention over either cache, whose shape and heads have been checked.
+template <typename Cache>
+mixllm_status attend(const Cache &cache, const void *q_f16, int64_t q_stride, int64_t n_tokens, int32_t q_heads,
+                     const int32_t *block_table, int64_t table_stride, int64_t table_width, const int32_t *seq_lens,
+                     const int32_t *cu_q, int64_t requests, int64_t max_q, float scale, int32_t causal, void *out_f16,
+                     int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes, size_t need,
+                     cudaError_t (*launch)(const mixllm::AttendArgsOf<Cache> &, void *, cudaStream_t, const char **),
+                     void *stream) {
+  if (n_tokens < 0 || n_tokens > 0x7FFFFFFF) return fail(MIXLLM_ERR_INVALID_ARG, "bad number of query tokens");
+  if (!std::isfinite(scale)) return fail(MIXLLM_ERR_INVALID_ARG, "scale must be finite");
+  if (n_tokens == 0 || requests == 0 || max_q == 0) return ok();
+  if (!q_f16 || !out_f16 || !seq_lens || !cu_q || (table_width > 0 && !block_table))
+    return fail(MIXLLM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(q_f16, 16) || !aligned(out_f16, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(cu_q, 4) || !aligned(lse, 4))
+    return fail(MIXLLM_ERR_INVALID_ARG, "q and out must be 16-byte aligned, the other buffers 4-byte aligned");
+  if (q_stride % 8 != 0 || out_stride % 8 != 0)
+    return fail(MIXLLM_ERR_INVALID_ARG, "token strides must be multiples of 8 elements");
+  if (n_tokens > 1 && out_stride < static_cast<int64_t>(q_heads) * cache.D)
+    return fail(MIXLLM_ERR_INVALID_ARG, "rows of out overlap");
+  if (workspace_bytes < need)
+    return fail(MIXLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu this shape needs",
+                workspace_bytes, need);
+  if (!workspace || !aligned(workspace, 256))
+    return fail(MIXLLM_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device buffer");
+  mixllm_status st = check_device();
+  if (st != MIXLLM_OK) return st;
+  mixllm::AttendArgsOf<Cache> a{cache,
+                       static_cast<const __half *>(q_f16),
+                       q_stride,
+                       n_tokens,
+                       q_heads,
+                       static_cast<int>(requests),
+                       static_cast<int>(max_q),
+                       block_table,
+                       table_stride,
+                       static_cast<int>(table_width),
+                       seq_lens,
+                       cu_q,
+                       scale,
+                       causal != 0,
+                       static_cast<__half *>(out_f16),
+                       out_stride,
+                       lse};
+  const char *msg = "";
+  cudaError_t e = launch(a, workspace, static_cast<cudaStream_t>(stream), &msg);
+  if (e == cudaErrorNotSupported) return fail(MIXLLM_ERR_UNSUPPORTED, "%s", msg);
+  if (e != cudaSuccess) return fail(MIXLLM_ERR_CUDA, "%s: %s", msg, cudaGetErrorString(e));
+  return ok();
+}
+
+// The tokens, rotation and norms of the entry points that write heads.
+mixllm_status check_turn(int64_t n_tokens, int32_t q_heads, int32_t head_dim, const void *w_q, const void *w_k, float eps,
+                         const int32_t *positions, const float *rope, int64_t max_pos, int32_t rotary) {
+  if (n_tokens < 0 || n_tokens > 0x7FFFFFFF || q_heads < 0 || q_heads > 65536)
+    return fail(MIXLLM_ERR_INVALID_ARG, "bad number of tokens or heads");
+  if (rotary < 0 || rotary > head_dim || rotary % 16 != 0)
+    return fail(MIXLLM_ERR_UNSUPPORTED, "%d rotated channels: need a multiple of 16 up to the head's %d", rotary, head_dim);
+  if (!(eps >= 0.0f)) return fail(MIXLLM_ERR_INVALID_ARG, "eps must not be negative");
+  if (n_tokens == 0) return MIXLLM_OK;
+  if (rotary > 0 && (!rope || !positions || max_pos <= 0))
+    return fail(MIXLLM_ERR_INVALID_ARG, "a rotation needs the table and the positions");
+  if (!aligned(w_q, 16) || !aligned(w_k, 16) || !aligned(rope, 16) || !aligned(positions, 4))
+    return fail(MIXLLM_ERR_INVALID_ARG, "weights and rope must be 16-byte aligned, positions 4");
+  return MIXLLM_OK;
+}
+
+// One tensor of heads that is read or written: token stride and alignment.
+mixllm_status check_heads(const char *name, const void *p, int64_t stride, int64_t n_tokens, int64_t row, bool written) {
+  if (!p) return fail(MIXLLM_ERR_INVALID_ARG, "null %s", name);
+  if (!aligned(p, 16)) return fail(MIXLLM_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (stride % 8 != 0) return fail(MIXLLM_ERR_INVALID_ARG, "the token stride of %s must be a multiple of 8", name);
+  if (written && n_tokens > 1 && stride < row) return fail(MIXLLM_ERR_INVALID_ARG, "rows of %s overlap", name);
+  return MIXLLM_OK;
+}
+
+mixllm_status check_w8a8(int64_t rows, int64_t K, const char *what) {
+  if (K <= 0 || K % 16 != 0 || K > 131056)
+    return fail(MIXLLM_ERR_UNSUPPORTED, "K = %lld must be a positive multiple of 16 up to 131056", static_cast<long long>(K));
+  if (rows < 0 || rows > 0x7FFFFFFF - 256) return fail(MIXLLM_ERR_INVALID_ARG, "need 0 <= %s < 2^31 - 256", what);
+  return MIXLLM_OK;
+}
+
+// The product's arguments apart from the activations.  *empty: nothing to compute.
+mixllm_status check_w8a8_product(int64_t M, int64_t K, const int8_t *W, const float *s_w, int64_t N, const void *bias,
+                                 const void *Y, const void *workspace, size_t workspace_bytes, bool from_f16,
+                                 bool *empty) {
+  *empty = false;
+  mixllm_status st = check_w8a8(M, K, "M");
+  if (st == MIXLLM_OK) st = check_w8a8(N, K, "N");
+  if (st != MIXLLM_OK) return st;
+  if (M == 0 || N == 0) {
+    *empty = true;
+    return MIXLLM_OK;
+  }
+  if (!W || !s_w || !Y) return fail(MIXLLM_ERR_INVALID_ARG, "null W, s_w or Y");
+  if (!aligned(W, 16) || !aligned(s_w, 4) || !aligned(bias, 2) || !aligned(Y, 2))
+    return fail(MIXLLM_ERR_INVALID_ARG, "W must be 16-byte aligned, s_w 4, bias and Y 2");
+  const size_t need = from_f16 ? mixllm::w8a8_linear_workspace_bytes(M, N, K) : mixllm::w8a8_gemm_workspace_bytes(M, N, K);
+  if (workspace_bytes < need)
+    return fail(MIXLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu this shape needs",
+                workspace_bytes, need);
+  if (!workspace || !aligned(workspace, 256))
+    return fail(MIXLLM_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device buffer");
+  return MIXLLM_OK;
+}
+
+mixllm_status w8a8_done(cudaError_t e, const char *msg) {
+  if (e == cudaErrorNotSupported) return fail(MIXLLM_ERR_UNSUPPORTED, "%s", msg);
+  if (e != cudaSuccess) return fail(MIXLLM_ERR_CUDA, "%s: %s", msg, cudaGetErrorString(e));
+  return ok();
 }
 
 }  // namespace
@@ -727,7 +850,7 @@ mixllm_status mixllm_kv4_attention_workspace_bytes(int64_t requests, int64_t max
   if (!bytes) return fail(MIXLLM_ERR_INVALID_ARG, "null bytes");
   mixllm::Kv4Cache cache;
   mixllm_status st = check_kv4(nullptr, nullptr, 0, kv_heads, head_dim, page_size, &cache);
-  if (st == MIXLLM_OK) st = check_kv4_heads(requests, max_q, q_heads, table_width, cache);
+  if (st == MIXLLM_OK) st = check_kv_heads(requests, max_q, q_heads, table_width, cache.H, cache.page_log2);
   if (st != MIXLLM_OK) return st;
   *bytes = mixllm::kv4_attention_workspace_bytes(static_cast<int>(requests), static_cast<int>(max_q), q_heads,
                                                  kv_heads, head_dim);
@@ -744,51 +867,209 @@ mixllm_status mixllm_kv4_attention(const void *q_f16, int64_t q_stride, int64_t 
   mixllm::Kv4Cache cache;
   mixllm_status st = check_kv4(const_cast<uint8_t *>(codes), const_cast<uint32_t *>(meta), pages, kv_heads, head_dim,
                                page_size, &cache);
-  if (st == MIXLLM_OK) st = check_kv4_heads(requests, max_q, q_heads, table_width, cache);
+  if (st == MIXLLM_OK) st = check_kv_heads(requests, max_q, q_heads, table_width, cache.H, cache.page_log2);
   if (st != MIXLLM_OK) return st;
-  if (n_tokens < 0 || n_tokens > 0x7FFFFFFF) return fail(MIXLLM_ERR_INVALID_ARG, "bad number of query tokens");
-  if (!std::isfinite(scale)) return fail(MIXLLM_ERR_INVALID_ARG, "scale must be finite");
-  if (n_tokens == 0 || requests == 0 || max_q == 0) return ok();
-  if (!q_f16 || !out_f16 || !seq_lens || !cu_q || (table_width > 0 && !block_table))
-    return fail(MIXLLM_ERR_INVALID_ARG, "null pointer");
-  if (!aligned(q_f16, 16) || !aligned(out_f16, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
-      !aligned(cu_q, 4) || !aligned(lse, 4))
-    return fail(MIXLLM_ERR_INVALID_ARG, "q and out must be 16-byte aligned, the other buffers 4-byte aligned");
-  if (q_stride % 8 != 0 || out_stride % 8 != 0)
-    return fail(MIXLLM_ERR_INVALID_ARG, "token strides must be multiples of 8 elements");
-  if (n_tokens > 1 && out_stride < static_cast<int64_t>(q_heads) * head_dim)
-    return fail(MIXLLM_ERR_INVALID_ARG, "rows of out overlap");
   const size_t need = mixllm::kv4_attention_workspace_bytes(static_cast<int>(requests), static_cast<int>(max_q),
                                                             q_heads, kv_heads, head_dim);
-  if (workspace_bytes < need)
-    return fail(MIXLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu this shape needs",
-                workspace_bytes, need);
-  if (!workspace || !aligned(workspace, 256))
-    return fail(MIXLLM_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device buffer");
+  return attend(cache, q_f16, q_stride, n_tokens, q_heads, block_table, table_stride, table_width, seq_lens, cu_q,
+                requests, max_q, scale, causal, out_f16, out_stride, lse, workspace, workspace_bytes, need,
+                mixllm::launch_kv4_attention, stream);
+}
+
+mixllm_status mixllm_w8a8_pack(const float *W, int64_t N, int64_t K, int8_t *codes, float *s_w, void *stream) {
+  mixllm_status st = check_w8a8(N, K, "N");
+  if (st != MIXLLM_OK) return st;
+  if (N == 0) return ok();
+  if (!W || !codes || !s_w) return fail(MIXLLM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(W, 16) || !aligned(codes, 16) || !aligned(s_w, 4))
+    return fail(MIXLLM_ERR_INVALID_ARG, "W and codes must be 16-byte aligned, s_w 4");
   st = check_device();
   if (st != MIXLLM_OK) return st;
-  mixllm::AttendArgs a{cache,
-                       static_cast<const __half *>(q_f16),
-                       q_stride,
-                       n_tokens,
-                       q_heads,
-                       static_cast<int>(requests),
-                       static_cast<int>(max_q),
-                       block_table,
-                       table_stride,
-                       static_cast<int>(table_width),
-                       seq_lens,
-                       cu_q,
-                       scale,
-                       causal != 0,
-                       static_cast<__half *>(out_f16),
-                       out_stride,
-                       lse};
-  const char *msg = "";
-  cudaError_t e = mixllm::launch_kv4_attention(a, workspace, static_cast<cudaStream_t>(stream), &msg);
-  if (e == cudaErrorNotSupported) return fail(MIXLLM_ERR_UNSUPPORTED, "%s", msg);
-  if (e != cudaSuccess) return fail(MIXLLM_ERR_CUDA, "%s: %s", msg, cudaGetErrorString(e));
+  cudaError_t e = mixllm::launch_w8a8_pack(W, N, K, codes, s_w, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "w8a8_pack launch");
   return ok();
+}
+
+mixllm_status mixllm_w8a8_quantize(const void *X_f16, int64_t x_stride, int64_t M, int64_t K, int8_t *A_q, float *s_a,
+                                   void *stream) {
+  mixllm_status st = check_w8a8(M, K, "M");
+  if (st != MIXLLM_OK) return st;
+  if (M == 0) return ok();
+  if (!A_q || !s_a) return fail(MIXLLM_ERR_INVALID_ARG, "null pointer");
+  st = check_heads("X", X_f16, x_stride, M, K, false);
+  if (st != MIXLLM_OK) return st;
+  if (!aligned(A_q, 16) || !aligned(s_a, 4)) return fail(MIXLLM_ERR_INVALID_ARG, "A_q must be 16-byte aligned, s_a 4");
+  st = check_device();
+  if (st != MIXLLM_OK) return st;
+  cudaError_t e = mixllm::launch_w8a8_quantize(static_cast<const __half *>(X_f16), x_stride, M, K, A_q, s_a,
+                                               static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "w8a8_quantize launch");
+  return ok();
+}
+
+mixllm_status mixllm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t from_f16, size_t *bytes) {
+  if (!bytes) return fail(MIXLLM_ERR_INVALID_ARG, "null bytes");
+  mixllm_status st = check_w8a8(M, K, "M");
+  if (st == MIXLLM_OK) st = check_w8a8(N, K, "N");
+  if (st != MIXLLM_OK) return st;
+  *bytes = from_f16 ? mixllm::w8a8_linear_workspace_bytes(M, N, K) : mixllm::w8a8_gemm_workspace_bytes(M, N, K);
+  return ok();
+}
+
+mixllm_status mixllm_w8a8_gemm(const int8_t *A_q, const float *s_a, int64_t M, int64_t K, const int8_t *W,
+                               const float *s_w, int64_t N, const void *bias_f16, void *Y_f16, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+  bool empty = false;
+  mixllm_status st = check_w8a8_product(M, K, W, s_w, N, bias_f16, Y_f16, workspace, workspace_bytes, false, &empty);
+  if (st != MIXLLM_OK) return st;
+  if (empty) return ok();
+  if (!A_q || !s_a) return fail(MIXLLM_ERR_INVALID_ARG, "null A_q or s_a");
+  if (!aligned(A_q, 16) || !aligned(s_a, 4)) return fail(MIXLLM_ERR_INVALID_ARG, "A_q must be 16-byte aligned, s_a 4");
+  st = check_device();
+  if (st != MIXLLM_OK) return st;
+  const mixllm::W8A8Args a{A_q, s_a, W, s_w, static_cast<const __half *>(bias_f16), static_cast<__half *>(Y_f16), M, N, K,
+                           workspace};
+  const char *msg = "";
+  const cudaError_t e = mixllm::launch_w8a8_gemm(a, static_cast<cudaStream_t>(stream), &msg);
+  return w8a8_done(e, msg);
+}
+
+mixllm_status mixllm_w8a8_linear(const void *X_f16, int64_t x_stride, int64_t M, int64_t K, const int8_t *W,
+                                 const float *s_w, int64_t N, const void *bias_f16, void *Y_f16, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+  bool empty = false;
+  mixllm_status st = check_w8a8_product(M, K, W, s_w, N, bias_f16, Y_f16, workspace, workspace_bytes, true, &empty);
+  if (st != MIXLLM_OK) return st;
+  if (empty) return ok();
+  st = check_heads("X", X_f16, x_stride, M, K, false);
+  if (st == MIXLLM_OK) st = check_device();
+  if (st != MIXLLM_OK) return st;
+  const mixllm::W8A8Args a{nullptr, nullptr, W, s_w, static_cast<const __half *>(bias_f16), static_cast<__half *>(Y_f16),
+                           M, N, K, workspace};
+  const char *msg = "";
+  const cudaError_t e = mixllm::launch_w8a8_linear(static_cast<const __half *>(X_f16), x_stride, a,
+                                                   static_cast<cudaStream_t>(stream), &msg);
+  return w8a8_done(e, msg);
+}
+
+mixllm_status mixllm_head_norm_rope(const void *q_f16, int64_t q_stride, int32_t q_heads, void *q_out_f16,
+                                    int64_t q_out_stride, const void *w_q_f16, const void *k_f16, int64_t k_stride,
+                                    int32_t kv_heads, void *k_out_f16, int64_t k_out_stride, const void *w_k_f16,
+                                    int64_t n_tokens, int32_t head_dim, float eps, const int32_t *positions,
+                                    const float *rope, int64_t max_pos, int32_t rotary, void *stream) {
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return fail(MIXLLM_ERR_UNSUPPORTED, "head size %d is not 64, 128 or 256", head_dim);
+  if (kv_heads < 0 || kv_heads > 65536) return fail(MIXLLM_ERR_INVALID_ARG, "%d key heads", kv_heads);
+  mixllm_status st = check_turn(n_tokens, q_heads, head_dim, w_q_f16, w_k_f16, eps, positions, rope, max_pos, rotary);
+  if (st != MIXLLM_OK) return st;
+  if (n_tokens == 0 || (q_heads == 0 && kv_heads == 0)) return ok();
+  const int64_t q_row = static_cast<int64_t>(q_heads) * head_dim, k_row = static_cast<int64_t>(kv_heads) * head_dim;
+  if (q_heads > 0) st = check_heads("q", q_f16, q_stride, n_tokens, q_row, false);
+  if (st == MIXLLM_OK && q_heads > 0) st = check_heads("q_out", q_out_f16, q_out_stride, n_tokens, q_row, true);
+  if (st == MIXLLM_OK && kv_heads > 0) st = check_heads("k", k_f16, k_stride, n_tokens, k_row, false);
+  if (st == MIXLLM_OK && kv_heads > 0) st = check_heads("k_out", k_out_f16, k_out_stride, n_tokens, k_row, true);
+  if (st == MIXLLM_OK) st = check_device();
+  if (st != MIXLLM_OK) return st;
+  mixllm::HeadArgs a{};
+  a.T = n_tokens;
+  a.q = static_cast<const __half *>(q_f16), a.k = static_cast<const __half *>(k_f16);
+  a.q_stride = q_stride, a.k_stride = k_stride;
+  a.Hq = q_heads, a.H = kv_heads;
+  a.q_out = static_cast<__half *>(q_out_f16), a.k_out = static_cast<__half *>(k_out_f16);
+  a.q_out_stride = q_out_stride, a.k_out_stride = k_out_stride;
+  a.w_q = static_cast<const __half *>(w_q_f16), a.w_k = static_cast<const __half *>(w_k_f16);
+  a.positions = positions, a.rope = rotary > 0 ? rope : nullptr;
+  a.max_pos = max_pos, a.rotary = rotary, a.eps = eps;
+  cudaError_t e = mixllm::launch_head_norm_rope(a, head_dim, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "head_norm_rope launch");
+  return ok();
+}
+
+mixllm_status mixllm_kv8_append(uint8_t *codes, float *scales, int64_t pages, int32_t kv_heads, int32_t head_dim,
+                                int32_t page_size, const int64_t *slots, int64_t n_slots, const void *k_f16,
+                                int64_t k_stride, const void *v_f16, int64_t v_stride, const void *q_f16,
+                                int64_t q_stride, int32_t q_heads, void *q_out_f16, int64_t q_out_stride,
+                                const void *w_q_f16, const void *w_k_f16, float eps, const int32_t *positions,
+                                const float *rope, int64_t max_pos, int32_t rotary, void *stream) {
+  mixllm::Kv8AppendArgs a{};
+  mixllm_status st = check_cache(codes, scales, pages, kv_heads, head_dim, page_size, &a.cache);
+  if (st == MIXLLM_OK)
+    st = check_turn(n_slots, q_heads, head_dim, w_q_f16, w_k_f16, eps, positions, rope, max_pos, rotary);
+  if (st != MIXLLM_OK) return st;
+  if (n_slots == 0) return ok();
+  if (!slots || !aligned(slots, 8)) return fail(MIXLLM_ERR_INVALID_ARG, "slots must be an 8-byte aligned device buffer");
+  const int64_t q_row = static_cast<int64_t>(q_heads) * head_dim, k_row = static_cast<int64_t>(kv_heads) * head_dim;
+  st = check_heads("k", k_f16, k_stride, n_slots, k_row, false);
+  if (st == MIXLLM_OK) st = check_heads("v", v_f16, v_stride, n_slots, k_row, false);
+  if (st == MIXLLM_OK && q_heads > 0) st = check_heads("q", q_f16, q_stride, n_slots, q_row, false);
+  if (st == MIXLLM_OK && q_heads > 0) st = check_heads("q_out", q_out_f16, q_out_stride, n_slots, q_row, true);
+  if (st == MIXLLM_OK) st = check_device();
+  if (st != MIXLLM_OK) return st;
+  a.slots = slots;
+  mixllm::HeadArgs heads{};
+  heads.T = n_slots;
+  heads.q = static_cast<const __half *>(q_f16), heads.k = static_cast<const __half *>(k_f16);
+  heads.v = static_cast<const __half *>(v_f16);
+  heads.q_stride = q_stride, heads.k_stride = k_stride, heads.v_stride = v_stride;
+  heads.Hq = q_heads, heads.H = kv_heads;
+  heads.q_out = static_cast<__half *>(q_out_f16), heads.q_out_stride = q_out_stride;
+  heads.w_q = static_cast<const __half *>(w_q_f16), heads.w_k = static_cast<const __half *>(w_k_f16);
+  heads.positions = positions, heads.rope = rotary > 0 ? rope : nullptr;
+  heads.max_pos = max_pos, heads.rotary = rotary, heads.eps = eps;
+  cudaError_t e = mixllm::launch_kv8_append(a, heads, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv8_append launch");
+  return ok();
+}
+
+mixllm_status mixllm_kv8_read(const uint8_t *codes, const float *scales, int64_t pages, int32_t kv_heads,
+                              int32_t head_dim, int32_t page_size, const int64_t *slots, int64_t n_slots, void *k_f16,
+                              void *v_f16, void *stream) {
+  mixllm::Kv8Cache cache;
+  mixllm_status st = check_cache(const_cast<uint8_t *>(codes), const_cast<float *>(scales), pages, kv_heads, head_dim,
+                                 page_size, &cache);
+  if (st != MIXLLM_OK) return st;
+  if (n_slots < 0 || n_slots > 0x7FFFFFFF) return fail(MIXLLM_ERR_INVALID_ARG, "bad number of tokens");
+  if (n_slots == 0) return ok();
+  if (!slots || !k_f16 || !v_f16) return fail(MIXLLM_ERR_INVALID_ARG, "null slots, k or v");
+  if (!aligned(slots, 8) || !aligned(k_f16, 16) || !aligned(v_f16, 16))
+    return fail(MIXLLM_ERR_INVALID_ARG, "k and v must be 16-byte aligned, slots 8");
+  st = check_device();
+  if (st != MIXLLM_OK) return st;
+  cudaError_t e = mixllm::launch_kv8_read(cache, slots, n_slots, k_f16, v_f16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv8_read launch");
+  return ok();
+}
+
+mixllm_status mixllm_kv8_attention_workspace_bytes(int64_t requests, int64_t max_q, int32_t q_heads, int32_t kv_heads,
+                                                   int32_t head_dim, int32_t page_size, int64_t table_width,
+                                                   size_t *bytes) {
+  if (!bytes) return fail(MIXLLM_ERR_INVALID_ARG, "null bytes");
+  mixllm::Kv8Cache cache;
+  mixllm_status st = check_cache<mixllm::Kv8Cache, float>(nullptr, nullptr, 0, kv_heads, head_dim, page_size, &cache);
+  if (st == MIXLLM_OK) st = check_kv_heads(requests, max_q, q_heads, table_width, cache.H, cache.page_log2);
+  if (st != MIXLLM_OK) return st;
+  *bytes = mixllm::kv8_attention_workspace_bytes(static_cast<int>(requests), static_cast<int>(max_q), q_heads, kv_heads,
+                                                 head_dim);
+  return ok();
+}
+
+mixllm_status mixllm_kv8_attention(const void *q_f16, int64_t q_stride, int64_t n_tokens, int32_t q_heads,
+                                   const uint8_t *codes, const float *scales, int64_t pages, int32_t kv_heads,
+                                   int32_t head_dim, int32_t page_size, const int32_t *block_table,
+                                   int64_t table_stride, int64_t table_width, const int32_t *seq_lens,
+                                   const int32_t *cu_q, int64_t requests, int64_t max_q, float scale, int32_t causal,
+                                   void *out_f16, int64_t out_stride, float *lse, void *workspace,
+                                   size_t workspace_bytes, void *stream) {
+  mixllm::Kv8Cache cache;
+  mixllm_status st = check_cache(const_cast<uint8_t *>(codes), const_cast<float *>(scales), pages, kv_heads, head_dim,
+                                 page_size, &cache);
+  if (st == MIXLLM_OK) st = check_kv_heads(requests, max_q, q_heads, table_width, cache.H, cache.page_log2);
+  if (st != MIXLLM_OK) return st;
+  const size_t need = mixllm::kv8_attention_workspace_bytes(static_cast<int>(requests), static_cast<int>(max_q),
+                                                            q_heads, kv_heads, head_dim);
+  return attend(cache, q_f16, q_stride, n_tokens, q_heads, block_table, table_stride, table_width, seq_lens, cu_q,
+                requests, max_q, scale, causal, out_f16, out_stride, lse, workspace, workspace_bytes, need,
+                mixllm::launch_kv8_attention, stream);
 }
 
 mixllm_status mixllm_sync_status(void *stream) {

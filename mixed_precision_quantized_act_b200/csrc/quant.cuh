@@ -37,6 +37,37 @@ namespace mixllm {
 //     moved one step toward e when |e| > s/2; within the margin (rare for real
 //     data, every tie case of the tests) the element takes the IEEE division.
 // ---------------------------------------------------------------------------
+// The codes of fp16 values by one step s (a positive amax / 127 of values that
+// x is among), computed as described above.
+struct QuantStep {
+  float s, r, half_s, margin;
+
+  static __device__ __forceinline__ QuantStep of(float step) {
+    return QuantStep{step, __frcp_rn(step), 0.5f * step, step * 0x1p-14f};
+  }
+
+  __device__ __forceinline__ uint32_t code(float xi) const {
+    // Integers below 2^22 in magnitude are rounded and converted with the
+    // 1.5*2^23 offset: fl(t + 1.5*2^23) - 1.5*2^23 is rint(t) (ties to even,
+    // the default rounding of the add), and the bits of fl(q + 1.5*2^23) are
+    // 0x4b400000 + q.  The explicit _rn intrinsics keep the compiler from
+    // fusing the multiply into the add.
+    constexpr float kMagic = 12582912.0f;
+    const float q0 = __fadd_rn(__fadd_rn(__fmul_rn(xi, r), kMagic), -kMagic);  // rint(fl(x * (1/s)))
+    const float e = __fmaf_rn(-q0, s, xi);  // exact remainder x - q0*s
+    const float d = fabsf(e) - half_s;
+    float qf;
+    if (fabsf(d) > margin) {
+      qf = d > 0.0f ? q0 + (e > 0.0f ? 1.0f : -1.0f) : q0;
+    } else {
+      // near a half-integer: the IEEE quotient, rounded
+      qf = __fadd_rn(__fadd_rn(__fdiv_rn(xi, s), kMagic), -kMagic);
+    }
+    qf = fminf(127.0f, fmaxf(-127.0f, qf));
+    return static_cast<uint32_t>(__float_as_int(__fadd_rn(qf, kMagic)) - 0x4b400000);
+  }
+};
+
 // One group of 128 activations held eight per lane by the 16 lanes of `mask`
 // (MLSys 2026 talk notes on MixLLM, notes.yuuk.io, §設計判断の概要: 8-bit
 // symmetric, group-wise RTN): s_a = amax / 127 (IEEE division), codes
@@ -60,32 +91,9 @@ __device__ __forceinline__ float quant_act_8x16(const uint4 raw, unsigned mask, 
   const float s = __fdiv_rn(amax, 127.0f);
   packed[0] = packed[1] = 0u;
   if (s != 0.0f) {
-    // Integers below 2^22 in magnitude are rounded and converted with the
-    // 1.5*2^23 offset: fl(t + 1.5*2^23) - 1.5*2^23 is rint(t) (ties to even,
-    // the default rounding of the add), and the bits of fl(q + 1.5*2^23) are
-    // 0x4b400000 + q.  The explicit _rn intrinsics keep the compiler from
-    // fusing the multiply into the add.
-    constexpr float kMagic = 12582912.0f;
-    const float r = __frcp_rn(s);
-    const float half_s = 0.5f * s;
-    const float margin = s * 0x1p-14f;
+    const QuantStep step = QuantStep::of(s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float xi = xval(i);
-      const float q0 = __fadd_rn(__fadd_rn(__fmul_rn(xi, r), kMagic), -kMagic);  // rint(fl(x * (1/s)))
-      const float e = __fmaf_rn(-q0, s, xi);  // exact remainder x - q0*s
-      const float d = fabsf(e) - half_s;
-      float qf;
-      if (fabsf(d) > margin) {
-        qf = d > 0.0f ? q0 + (e > 0.0f ? 1.0f : -1.0f) : q0;
-      } else {
-        // near a half-integer: the IEEE quotient, rounded
-        qf = __fadd_rn(__fadd_rn(__fdiv_rn(xi, s), kMagic), -kMagic);
-      }
-      qf = fminf(127.0f, fmaxf(-127.0f, qf));
-      const uint32_t qi = static_cast<uint32_t>(__float_as_int(__fadd_rn(qf, kMagic)) - 0x4b400000);
-      packed[i >> 2] |= (qi & 0xFFu) << ((i & 3) * 8);
-    }
+    for (int i = 0; i < 8; ++i) packed[i >> 2] |= (step.code(xval(i)) & 0xFFu) << ((i & 3) * 8);
   }
   return s;
 }

@@ -1,5 +1,6 @@
-"""The residual norms between the linears (mixllm_residual_norm) and the way
-back from int8 codes to fp16 (mixllm_dequantize_act)."""
+"""The residual norms between the linears (mixllm_residual_norm), the way back
+from int8 codes to fp16 (mixllm_dequantize_act), and the norms of query and key
+heads with their rotation (mixllm_head_norm_rope)."""
 from __future__ import annotations
 
 import torch
@@ -70,3 +71,40 @@ def dequantize_act(A_q, s_a, stream=None) -> torch.Tensor:
         X = torch.empty(A_q.shape, dtype=_F16, device=A_q.device)
     dequantize_act_into(A_q, s_a, X, stream)
     return X
+
+
+def turn(D: int, T: int, w_q, w_k, positions, rope, dev: int):
+    """Checks of a norm's and rotation's arguments; (max_pos, rotary)."""
+    for name, w in (("w_q", w_q), ("w_k", w_k)):
+        if w is not None:
+            need(w, name, _F16, (D,), dev)
+    if rope is None:
+        return 0, 0
+    if positions is None:
+        raise ValueError("rope needs positions")
+    need(rope, "rope", _F32, rope.shape, dev)
+    need(positions, "positions", torch.int32, (T,), dev)
+    return rope.shape
+
+
+def head_norm_rope_into(q, q_out, w_q=None, k=None, k_out=None, w_k=None, positions=None, rope=None,
+                        eps: float = 1e-6, stream=None):
+    """RMS norms of every query and key head over its own channels (weights w_q,
+    w_k fp16 [head_dim]; None: no norm), then the rotation by position, as one
+    kernel: q fp16 [T, q_heads, head_dim] into q_out (which may be q), k fp16
+    [T, kv_heads, head_dim] into k_out.  rope fp32 [max_pos, rotary] and positions
+    int32 [T] as for kv4_append_into, a negative position skipping its token.
+    Rows may be strided: slices of one qkv output serve."""
+    dev = on_cuda(q, "q")
+    T, q_heads, D = q.shape
+    q_stride, q_out_stride = rows(q, "q", _F16, q.shape, dev), rows(q_out, "q_out", _F16, q.shape, dev)
+    kv_heads = k_stride = k_out_stride = 0
+    if k is not None:
+        if k_out is None:
+            raise ValueError("k needs k_out")
+        kv_heads = k.shape[1]
+        k_stride = rows(k, "k", _F16, (T, kv_heads, D), dev)
+        k_out_stride = rows(k_out, "k_out", _F16, (T, kv_heads, D), dev)
+    max_pos, rotary = turn(D, T, w_q, w_k, positions, rope, dev)
+    call("mixllm_head_norm_rope", dev, stream, ptr(q), q_stride, q_heads, ptr(q_out), q_out_stride, ptr(w_q), ptr(k),
+         k_stride, kv_heads, ptr(k_out), k_out_stride, ptr(w_k), T, D, eps, ptr(positions), ptr(rope), max_pos, rotary)
