@@ -680,10 +680,10 @@ MIXLLM_API mixllm_status mixllm_w8a8_quantize(const void *X_f16, int64_t x_strid
                                               float *s_a, void *stream);
 
 /*
- * Bytes of workspace that mixllm_w8a8_gemm (from_f16 = 0) or mixllm_w8a8_linear
- * (from_f16 = 1) need, in *bytes (0 for an empty product).  Pure host function.
+ * Bytes of workspace that mixllm_w8a8_linear needs, in *bytes (0 for an empty
+ * product); enough for fewer tokens, too.  Pure host function.
  */
-MIXLLM_API mixllm_status mixllm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t from_f16, size_t *bytes);
+MIXLLM_API mixllm_status mixllm_w8a8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, size_t *bytes);
 
 /*
  * The linear layer in 8-bit integers:
@@ -698,18 +698,18 @@ MIXLLM_API mixllm_status mixllm_w8a8_workspace_bytes(int64_t M, int64_t K, int64
  *              -128 are allowed
  *   bias_f16   device, fp16 [N], or NULL
  *   Y_f16      device, fp16 [M, N] contiguous; overlaps no input
- *   workspace  device, at least mixllm_w8a8_workspace_bytes() bytes, 256-byte
- *              aligned, zero-filled before its first use; calls leave its
- *              counters (the first 4096 bytes) at zero, so it stays ready for
- *              calls of any sizes it is large enough for.  Two calls that run at
- *              the same time must not share one.  After MIXLLM_ERR_TIMEOUT zero
- *              it again.
- * A_q, X and W 16-byte aligned, s_a and s_w 4, bias and Y 2.  Any M and N; K as
- * above.  The result does not depend on timing.  Asynchronous on `stream`.
+ *   workspace  device, at least mixllm_w8a8_linear_workspace_bytes() bytes,
+ *              256-byte aligned: the activations' codes and scales.  Needs no
+ *              initial value; two calls that run at the same time must not share
+ *              one.
+ * A_q, X and W 16-byte aligned, s_a and s_w 4, bias and Y 2.  Any M and N whose
+ * tiles of 128 channels x 16 to 256 tokens x 128 of K number below 2^31
+ * (MIXLLM_ERR_UNSUPPORTED otherwise); K as above.  The result does not depend on
+ * timing.  Asynchronous on `stream`.
  */
 MIXLLM_API mixllm_status mixllm_w8a8_gemm(const int8_t *A_q, const float *s_a, int64_t M, int64_t K, const int8_t *W,
                                           const float *s_w, int64_t N, const void *bias_f16, void *Y_f16,
-                                          void *workspace, size_t workspace_bytes, void *stream);
+                                          void *stream);
 MIXLLM_API mixllm_status mixllm_w8a8_linear(const void *X_f16, int64_t x_stride, int64_t M, int64_t K,
                                             const int8_t *W, const float *s_w, int64_t N, const void *bias_f16,
                                             void *Y_f16, void *workspace, size_t workspace_bytes, void *stream);

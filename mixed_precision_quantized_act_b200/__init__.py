@@ -79,8 +79,8 @@ from .w8a8 import (  # noqa: F401
     w8a8_linear,
     w8a8_linear_into,
     w8a8_linear_workspace,
+    w8a8_linear_workspace_bytes,
     w8a8_pack,
     w8a8_quantize,
     w8a8_quantize_into,
-    w8a8_workspace_bytes,
 )

@@ -75,8 +75,8 @@ SIGNATURES = {
                                             _vp]),
     "mixllm_w8a8_pack": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "mixllm_w8a8_quantize": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
-    "mixllm_w8a8_workspace_bytes": (ctypes.c_int, [_i64, _i64, _i64, _i32, ctypes.POINTER(ctypes.c_size_t)]),
-    "mixllm_w8a8_gemm": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "mixllm_w8a8_linear_workspace_bytes": (ctypes.c_int, [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "mixllm_w8a8_gemm": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp]),
     "mixllm_w8a8_linear": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "mixllm_head_norm_rope": (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64,
                                              _i32, _f32, _vp, _vp, _i64, _i32, _vp]),

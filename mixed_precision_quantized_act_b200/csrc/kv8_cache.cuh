@@ -133,7 +133,7 @@ __device__ __forceinline__ void kv8_write_run(const Kv8AppendArgs &a, const Head
     }
   }
   // ---- the new rows
-  const bool none = !(s > 0.0f);
+  const bool none = !(s >= 0x1p-100f);  // nothing but zeros, or a NaN
   const QuantStep step = QuantStep::of(none ? 1.0f : s);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
@@ -142,9 +142,8 @@ __device__ __forceinline__ void kv8_write_run(const Kv8AppendArgs &a, const Head
     if (!none) {
       float f[8];
       widen8(x[p], f);
-      packed[0] = packed[1] = 0u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) packed[i >> 2] |= ((step.code(f[i]) & 0xFFu) ^ 0x80u) << ((i & 3) * 8);
+      step.codes(f, packed);
+      packed[0] ^= 0x80808080u, packed[1] ^= 0x80808080u;
     }
     *reinterpret_cast<uint2 *>(codes + row_of[p] * D + sub * 8) = make_uint2(packed[0], packed[1]);
   }

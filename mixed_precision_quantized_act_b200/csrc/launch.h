@@ -126,16 +126,15 @@ struct W8A8Args {
   const __half *bias;  // or null
   __half *Y;
   int64_t M, N, K;
-  void *ws;
 };
-size_t w8a8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 size_t w8a8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_w8a8_pack(const float *W, int64_t N, int64_t K, int8_t *codes, float *s_w, cudaStream_t stream);
 cudaError_t launch_w8a8_quantize(const __half *X, int64_t stride, int64_t M, int64_t K, int8_t *A_q, float *s_a,
                                  cudaStream_t stream);
 cudaError_t launch_w8a8_gemm(const W8A8Args &a, cudaStream_t stream, const char **msg);
-// a.A_q and a.s_a are in the workspace
-cudaError_t launch_w8a8_linear(const __half *X, int64_t stride, W8A8Args a, cudaStream_t stream, const char **msg);
+// a.A_q and a.s_a are made in the workspace, of w8a8_linear_workspace_bytes()
+cudaError_t launch_w8a8_linear(const __half *X, int64_t stride, W8A8Args a, void *ws, cudaStream_t stream,
+                               const char **msg);
 
 // The paged 4-bit KV cache (kv4_cache.cuh) and the attention over it
 // (kv4_attention.cuh).

@@ -247,8 +247,7 @@ mixllm_status check_w8a8(int64_t rows, int64_t K, const char *what) {
 
 // The product's arguments apart from the activations.  *empty: nothing to compute.
 mixllm_status check_w8a8_product(int64_t M, int64_t K, const int8_t *W, const float *s_w, int64_t N, const void *bias,
-                                 const void *Y, const void *workspace, size_t workspace_bytes, bool from_f16,
-                                 bool *empty) {
+                                 const void *Y, bool *empty) {
   *empty = false;
   mixllm_status st = check_w8a8(M, K, "M");
   if (st == MIXLLM_OK) st = check_w8a8(N, K, "N");
@@ -260,12 +259,6 @@ mixllm_status check_w8a8_product(int64_t M, int64_t K, const int8_t *W, const fl
   if (!W || !s_w || !Y) return fail(MIXLLM_ERR_INVALID_ARG, "null W, s_w or Y");
   if (!aligned(W, 16) || !aligned(s_w, 4) || !aligned(bias, 2) || !aligned(Y, 2))
     return fail(MIXLLM_ERR_INVALID_ARG, "W must be 16-byte aligned, s_w 4, bias and Y 2");
-  const size_t need = from_f16 ? mixllm::w8a8_linear_workspace_bytes(M, N, K) : mixllm::w8a8_gemm_workspace_bytes(M, N, K);
-  if (workspace_bytes < need)
-    return fail(MIXLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu this shape needs",
-                workspace_bytes, need);
-  if (!workspace || !aligned(workspace, 256))
-    return fail(MIXLLM_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device buffer");
   return MIXLLM_OK;
 }
 
@@ -907,28 +900,26 @@ mixllm_status mixllm_w8a8_quantize(const void *X_f16, int64_t x_stride, int64_t 
   return ok();
 }
 
-mixllm_status mixllm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t from_f16, size_t *bytes) {
+mixllm_status mixllm_w8a8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, size_t *bytes) {
   if (!bytes) return fail(MIXLLM_ERR_INVALID_ARG, "null bytes");
   mixllm_status st = check_w8a8(M, K, "M");
   if (st == MIXLLM_OK) st = check_w8a8(N, K, "N");
   if (st != MIXLLM_OK) return st;
-  *bytes = from_f16 ? mixllm::w8a8_linear_workspace_bytes(M, N, K) : mixllm::w8a8_gemm_workspace_bytes(M, N, K);
+  *bytes = mixllm::w8a8_linear_workspace_bytes(M, N, K);
   return ok();
 }
 
 mixllm_status mixllm_w8a8_gemm(const int8_t *A_q, const float *s_a, int64_t M, int64_t K, const int8_t *W,
-                               const float *s_w, int64_t N, const void *bias_f16, void *Y_f16, void *workspace,
-                               size_t workspace_bytes, void *stream) {
+                               const float *s_w, int64_t N, const void *bias_f16, void *Y_f16, void *stream) {
   bool empty = false;
-  mixllm_status st = check_w8a8_product(M, K, W, s_w, N, bias_f16, Y_f16, workspace, workspace_bytes, false, &empty);
+  mixllm_status st = check_w8a8_product(M, K, W, s_w, N, bias_f16, Y_f16, &empty);
   if (st != MIXLLM_OK) return st;
   if (empty) return ok();
   if (!A_q || !s_a) return fail(MIXLLM_ERR_INVALID_ARG, "null A_q or s_a");
   if (!aligned(A_q, 16) || !aligned(s_a, 4)) return fail(MIXLLM_ERR_INVALID_ARG, "A_q must be 16-byte aligned, s_a 4");
   st = check_device();
   if (st != MIXLLM_OK) return st;
-  const mixllm::W8A8Args a{A_q, s_a, W, s_w, static_cast<const __half *>(bias_f16), static_cast<__half *>(Y_f16), M, N, K,
-                           workspace};
+  const mixllm::W8A8Args a{A_q, s_a, W, s_w, static_cast<const __half *>(bias_f16), static_cast<__half *>(Y_f16), M, N, K};
   const char *msg = "";
   const cudaError_t e = mixllm::launch_w8a8_gemm(a, static_cast<cudaStream_t>(stream), &msg);
   return w8a8_done(e, msg);
@@ -938,16 +929,22 @@ mixllm_status mixllm_w8a8_linear(const void *X_f16, int64_t x_stride, int64_t M,
                                  const float *s_w, int64_t N, const void *bias_f16, void *Y_f16, void *workspace,
                                  size_t workspace_bytes, void *stream) {
   bool empty = false;
-  mixllm_status st = check_w8a8_product(M, K, W, s_w, N, bias_f16, Y_f16, workspace, workspace_bytes, true, &empty);
+  mixllm_status st = check_w8a8_product(M, K, W, s_w, N, bias_f16, Y_f16, &empty);
   if (st != MIXLLM_OK) return st;
   if (empty) return ok();
+  const size_t need = mixllm::w8a8_linear_workspace_bytes(M, N, K);
+  if (workspace_bytes < need)
+    return fail(MIXLLM_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu this shape needs",
+                workspace_bytes, need);
+  if (!workspace || !aligned(workspace, 256))
+    return fail(MIXLLM_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device buffer");
   st = check_heads("X", X_f16, x_stride, M, K, false);
   if (st == MIXLLM_OK) st = check_device();
   if (st != MIXLLM_OK) return st;
   const mixllm::W8A8Args a{nullptr, nullptr, W, s_w, static_cast<const __half *>(bias_f16), static_cast<__half *>(Y_f16),
-                           M, N, K, workspace};
+                           M, N, K};
   const char *msg = "";
-  const cudaError_t e = mixllm::launch_w8a8_linear(static_cast<const __half *>(X_f16), x_stride, a,
+  const cudaError_t e = mixllm::launch_w8a8_linear(static_cast<const __half *>(X_f16), x_stride, a, workspace,
                                                    static_cast<cudaStream_t>(stream), &msg);
   return w8a8_done(e, msg);
 }

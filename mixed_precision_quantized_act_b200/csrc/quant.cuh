@@ -37,37 +37,6 @@ namespace mixllm {
 //     moved one step toward e when |e| > s/2; within the margin (rare for real
 //     data, every tie case of the tests) the element takes the IEEE division.
 // ---------------------------------------------------------------------------
-// The codes of fp16 values by one step s (a positive amax / 127 of values that
-// x is among), computed as described above.
-struct QuantStep {
-  float s, r, half_s, margin;
-
-  static __device__ __forceinline__ QuantStep of(float step) {
-    return QuantStep{step, __frcp_rn(step), 0.5f * step, step * 0x1p-14f};
-  }
-
-  __device__ __forceinline__ uint32_t code(float xi) const {
-    // Integers below 2^22 in magnitude are rounded and converted with the
-    // 1.5*2^23 offset: fl(t + 1.5*2^23) - 1.5*2^23 is rint(t) (ties to even,
-    // the default rounding of the add), and the bits of fl(q + 1.5*2^23) are
-    // 0x4b400000 + q.  The explicit _rn intrinsics keep the compiler from
-    // fusing the multiply into the add.
-    constexpr float kMagic = 12582912.0f;
-    const float q0 = __fadd_rn(__fadd_rn(__fmul_rn(xi, r), kMagic), -kMagic);  // rint(fl(x * (1/s)))
-    const float e = __fmaf_rn(-q0, s, xi);  // exact remainder x - q0*s
-    const float d = fabsf(e) - half_s;
-    float qf;
-    if (fabsf(d) > margin) {
-      qf = d > 0.0f ? q0 + (e > 0.0f ? 1.0f : -1.0f) : q0;
-    } else {
-      // near a half-integer: the IEEE quotient, rounded
-      qf = __fadd_rn(__fadd_rn(__fdiv_rn(xi, s), kMagic), -kMagic);
-    }
-    qf = fminf(127.0f, fmaxf(-127.0f, qf));
-    return static_cast<uint32_t>(__float_as_int(__fadd_rn(qf, kMagic)) - 0x4b400000);
-  }
-};
-
 // One group of 128 activations held eight per lane by the 16 lanes of `mask`
 // (MLSys 2026 talk notes on MixLLM, notes.yuuk.io, §設計判断の概要: 8-bit
 // symmetric, group-wise RTN): s_a = amax / 127 (IEEE division), codes
@@ -91,12 +60,69 @@ __device__ __forceinline__ float quant_act_8x16(const uint4 raw, unsigned mask, 
   const float s = __fdiv_rn(amax, 127.0f);
   packed[0] = packed[1] = 0u;
   if (s != 0.0f) {
-    const QuantStep step = QuantStep::of(s);
+    // Integers below 2^22 in magnitude are rounded and converted with the
+    // 1.5*2^23 offset: fl(t + 1.5*2^23) - 1.5*2^23 is rint(t) (ties to even,
+    // the default rounding of the add), and the bits of fl(q + 1.5*2^23) are
+    // 0x4b400000 + q.  The explicit _rn intrinsics keep the compiler from
+    // fusing the multiply into the add.
+    constexpr float kMagic = 12582912.0f;
+    const float r = __frcp_rn(s);
+    const float half_s = 0.5f * s;
+    const float margin = s * 0x1p-14f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) packed[i >> 2] |= (step.code(xval(i)) & 0xFFu) << ((i & 3) * 8);
+    for (int i = 0; i < 8; ++i) {
+      const float xi = xval(i);
+      const float q0 = __fadd_rn(__fadd_rn(__fmul_rn(xi, r), kMagic), -kMagic);  // rint(fl(x * (1/s)))
+      const float e = __fmaf_rn(-q0, s, xi);  // exact remainder x - q0*s
+      const float d = fabsf(e) - half_s;
+      float qf;
+      if (fabsf(d) > margin) {
+        qf = d > 0.0f ? q0 + (e > 0.0f ? 1.0f : -1.0f) : q0;
+      } else {
+        // near a half-integer: the IEEE quotient, rounded
+        qf = __fadd_rn(__fadd_rn(__fdiv_rn(xi, s), kMagic), -kMagic);
+      }
+      qf = fminf(127.0f, fmaxf(-127.0f, qf));
+      const uint32_t qi = static_cast<uint32_t>(__float_as_int(__fadd_rn(qf, kMagic)) - 0x4b400000);
+      packed[i >> 2] |= (qi & 0xFFu) << ((i & 3) * 8);
+    }
   }
   return s;
 }
+
+// Codes of eight values by one step s >= 2^-100, |x| <= 127 s, lowest first: rne of
+// the IEEE quotients x / s, as above.  q0 = rint(x r) is off from x / s by less than
+// 1/2 + 2^-16, so it is the code wherever the exact remainder |e| = |x - q0 s|
+// stays below s/2 less a margin; the low byte of fl(x r + 1.5*2^23) is q0 itself.
+// One test of the largest remainder serves all eight, and only where it fails are
+// the quotients divided out: seven instructions a value.
+struct QuantStep {
+  float s, r, below;
+
+  static __device__ __forceinline__ QuantStep of(float step) {
+    return QuantStep{step, __frcp_rn(step), step * (0.5f - 0x1p-14f)};
+  }
+  __device__ __forceinline__ void codes(const float (&x)[8], uint32_t (&packed)[2]) const {
+    constexpr float kMagic = 12582912.0f;
+    uint32_t bits[8];
+    float worst = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = __fmaf_rn(x[i], r, kMagic);
+      bits[i] = __float_as_uint(t);
+      worst = fmaxf(worst, fabsf(__fmaf_rn(-__fadd_rn(t, -kMagic), s, x[i])));
+    }
+    if (worst > below) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        bits[i] = static_cast<uint32_t>(max(-127, min(127, __float2int_rn(__fdiv_rn(x[i], s)))));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      packed[i] = __byte_perm(__byte_perm(bits[4 * i], bits[4 * i + 1], 0x0040),
+                              __byte_perm(bits[4 * i + 2], bits[4 * i + 3], 0x0040), 0x5410);
+  }
+};
 
 // One half-warp per (token, group): 16 lanes x one 16-byte load.  The grid
 // is one wave of 8 blocks per SM where the layer allows (the register bound

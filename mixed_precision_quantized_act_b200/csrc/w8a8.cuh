@@ -20,17 +20,22 @@ namespace mixllm {
 // ---------------------------------------------------------------------------
 // One scale per row: amax over the row's K values, s = amax / 127 (IEEE fp32),
 // codes rne(x / s) by the fp32 quotient, within +-127; a row of zeros gets s = 0
-// and codes 0, one with a NaN or an infinity s = NaN and codes 0.  One block per
-// row, which stays in registers up to V runs of eight a thread and is read
-// again from there on.
+// and codes 0, one with a NaN or an infinity s = NaN and codes 0.  A block takes
+// a row at a time, which stays in registers up to four runs of eight a thread and is
+// read again from there on.
 // ---------------------------------------------------------------------------
 template <typename T>
-struct RowRun;  // eight values as loaded
+struct RowRun;  // eight values as loaded; top(): their largest magnitude, NaN or infinity if one is
 template <>
 struct RowRun<__half> {
   uint4 raw;
   __device__ __forceinline__ void load(const __half *p) { raw = *reinterpret_cast<const uint4 *>(p); }
   __device__ __forceinline__ void widen(float (&f)[8]) const { widen8(raw, f); }
+  __device__ __forceinline__ float top() const {
+    const __half2 *h = reinterpret_cast<const __half2 *>(&raw);
+    const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+    return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+  }
 };
 template <>
 struct RowRun<float> {
@@ -42,6 +47,13 @@ struct RowRun<float> {
   __device__ __forceinline__ void widen(float (&f)[8]) const {
     f[0] = lo.x, f[1] = lo.y, f[2] = lo.z, f[3] = lo.w, f[4] = hi.x, f[5] = hi.y, f[6] = hi.z, f[7] = hi.w;
   }
+  __device__ __forceinline__ float top() const {
+    float f[8], m = 0.0f;
+    widen(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fabsf(f[i]) <= 3.4028234663852886e38f ? fmaxf(m, fabsf(f[i])) : INFINITY;
+    return m;
+  }
 };
 
 constexpr int kRowQuantRuns = 4;  // of eight values, a thread's registers
@@ -50,25 +62,20 @@ template <typename T>
 __global__ void __launch_bounds__(1024) row_quantize_kernel(const T *__restrict__ X, int64_t stride, int K,
                                                             int8_t *__restrict__ codes, float *__restrict__ scales) {
   __shared__ float warp_max[32];
-  pdl_launch_dependents();
+  pdl_wait();
+  pdl_launch_dependents();  // behind all that came before this kernel: a dependent may read the weights at once
   const int64_t m = blockIdx.x;
   const T *row = X + m * stride;
-  const int step = blockDim.x * 8, k0 = threadIdx.x * 8;
+  const int step = blockDim.x * 8, k0 = threadIdx.x * 8, lane = threadIdx.x & 31;
   RowRun<T> run[kRowQuantRuns];
-  float amax = 0.0f;
-  bool odd = false;
-  const auto look = [&](const RowRun<T> &r) {
-    float f[8];
-    r.widen(f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      amax = fmaxf(amax, fabsf(f[i]));
-      odd |= !(fabsf(f[i]) <= 3.4028234663852886e38f);
-    }
-  };
 #pragma unroll
   for (int v = 0; v < kRowQuantRuns; ++v)
     if (k0 + v * step < K) run[v].load(row + k0 + v * step);
+  float amax = 0.0f;
+  const auto look = [&](const RowRun<T> &r) {
+    const float top = r.top();
+    amax = fmaxf(amax, top == top ? top : INFINITY);
+  };
 #pragma unroll
   for (int v = 0; v < kRowQuantRuns; ++v)
     if (k0 + v * step < K) look(run[v]);
@@ -77,26 +84,24 @@ __global__ void __launch_bounds__(1024) row_quantize_kernel(const T *__restrict_
     r.load(row + k);
     look(r);
   }
-  if (odd) amax = INFINITY;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
+  if (lane == 0) warp_max[threadIdx.x >> 5] = amax;
   __syncthreads();
-  amax = (threadIdx.x & 31) < (blockDim.x >> 5) ? warp_max[threadIdx.x & 31] : 0.0f;
+  amax = lane < (blockDim.x >> 5) ? warp_max[lane] : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
   const float s = amax == INFINITY ? __int_as_float(0x7FFFFFFF) : __fdiv_rn(amax, 127.0f);
   if (threadIdx.x == 0) scales[m] = s;
   const bool none = !(s > 0.0f);
+  const QuantStep q = QuantStep::of(none ? 1.0f : s);
   const auto store = [&](const RowRun<T> &r, int k) {
     uint32_t packed[2] = {0u, 0u};
     if (!none) {
       float f[8];
       r.widen(f);
       if constexpr (sizeof(T) == 2) {
-        const QuantStep q = QuantStep::of(s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) packed[i >> 2] |= (q.code(f[i]) & 0xFFu) << ((i & 3) * 8);
+        q.codes(f, packed);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -120,45 +125,73 @@ __global__ void __launch_bounds__(1024) row_quantize_kernel(const T *__restrict_
 template <typename T>
 static cudaError_t launch_row_quantize(const T *X, int64_t stride, int64_t M, int64_t K, int8_t *codes, float *scales,
                                        cudaStream_t stream) {
-  const int64_t runs = K / 8;
-  // a thread per run up to 512, then up to four runs a thread
-  int64_t threads = runs <= 512 ? runs : (runs + kRowQuantRuns - 1) / kRowQuantRuns;
-  threads = threads < 256 && runs > 512 ? 256 : threads;
-  threads = threads > 1024 ? 1024 : (threads + 31) / 32 * 32;
-  row_quantize_kernel<T><<<static_cast<unsigned>(M), static_cast<unsigned>(threads), 0, stream>>>(
-      X, stride, static_cast<int>(K), codes, scales);
-  return cudaGetLastError();
+  // Few rows: a run a thread, for latency.  Many: four, so that what a block does once costs each value less.
+  const int64_t runs = K / 8, each = M >= 512 || runs > 1024 ? kRowQuantRuns : 1;
+  int64_t threads = ((runs + each - 1) / each + 31) / 32 * 32;
+  if (threads > 1024) threads = 1024;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // starts while the kernel before it ends
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(M));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, row_quantize_kernel<T>, X, stride, static_cast<int>(K), codes, scales);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 // ---------------------------------------------------------------------------
 // The product.  Channels are the tensor core's 128-row side and tokens its
-// column side (NT of them, 16 to 256), so that a few tokens cost no more than
+// column side (NT of them, 16 to 64 here), so that a few tokens cost no more than
 // their columns and the weights stream through shared memory at any number of
-// tokens.  Work is cut into chunks of 128 channels x NT tokens x 128 values of K;
-// block c takes the units (runs of `per` chunks) [c U / P, (c + 1) U / P) of
-// their sequence, K innermost, tokens next.  With `per` the whole of K a block
-// has whole tiles; with 1 the ends of its share may cut a tile, whose int32 parts
-// go to the workspace, and the last block to arrive adds them: integers, so the
-// result is the same whoever is last.
+// tokens.  A tile's K is cut into S even shares, one for each block of a cluster
+// (S = 1: none), so that few tiles still use every SM; a block of no cluster
+// takes tiles in turn, an even run of them.
 //
 // Warp 0 loads both operands by TMA (128-byte swizzle), warp 1 issues
-// tcgen05.mma kind::i8, warps 4-7 scale the accumulators and write Y while the
-// next tile's products run (two accumulators in tensor memory).
+// tcgen05.mma kind::i8, warps 4-11 are the epilogue: thread = channel, four warps
+// to one half of the tokens.  They scale the accumulator and write Y by way of
+// shared memory, 16 bytes a lane, while the next tile's products run (two
+// accumulators in tensor memory).  The blocks of a cluster give each other their
+// parts through distributed shared memory, each block adding four tokens at a time
+// of its own share: whole numbers, so the sum does not depend on who was first.
 // ---------------------------------------------------------------------------
-constexpr int kW8Threads = 256;
+constexpr int kW8Threads = 384;
 constexpr int kW8Rows = 128;   // channels of a tile
 constexpr int kW8Chunk = 128;  // values of K of a chunk
-constexpr int kW8MaxGrid = 148;
+
+// Walks a block's chunks: tile by tile, tokens innermost, n chunks of K from k0 on.
+struct W8Walk {
+  int rt, tt, chunk, TT, k0, k1;
+
+  __device__ __forceinline__ W8Walk(int tile, int token_tiles, int first, int end) : chunk(first), TT(token_tiles), k0(first), k1(end) {
+    rt = tile / TT, tt = tile - rt * TT;
+  }
+  __device__ __forceinline__ void next() {
+    if (++chunk == k1) {
+      chunk = k0;
+      if (++tt == TT) tt = 0, ++rt;
+    }
+  }
+};
 
 template <int NT>
 struct W8Cfg {
   static constexpr int kStageW = kW8Rows * kW8Chunk, kStageA = NT * kW8Chunk, kStage = kStageW + kStageA;
-  static constexpr int kStages = 200 * 1024 / kStage < 10 ? 200 * 1024 / kStage : 10;
-  static constexpr int kSmem = kStages * kStage + 1024;
+  static constexpr int kCols = NT / 2 < 32 ? NT / 2 : 32;  // tokens of one load from tensor memory
+  static constexpr int kOutCols = kCols < 16 ? kCols : 16;  // and of one round through shared memory
+  static constexpr int kOut = 8 * kOutCols * 32 * 2;       // bytes: eight warps' tokens x 32 channels, fp16
+  static constexpr int kRoom = 112 * 1024 - kOut - 1024 - 2 * NT * 4;
+  static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
+  static constexpr int kSmem = kStages * kStage + kOut + 1024;
   static constexpr int kTmem = 2 * NT < 32 ? 32 : 2 * NT;
-  static constexpr int kStep = NT < 32 ? 16 : 32;  // columns of one load from tensor memory
-  static constexpr int kPart = kW8Rows * NT;       // int32 values of a part
-  static_assert(kSmem + 4096 <= 227 * 1024, "shared memory of a block");
+  static constexpr int kGroups = NT / 4;  // of four tokens
+  // parts that a block receives: of each block of the cluster, its groups' tokens x channels, int32
+  static constexpr int received(int S) { return S * ((kGroups + S - 1) / S) * 4 * kW8Rows * 4; }
+  static_assert(received(2) <= kStages * kStage && received(4) <= kStages * kStage, "parts in the operands' place");
+  static_assert(2 * (kSmem + 2048) <= 227 * 1024, "two blocks an SM");
 };
 
 struct W8Job {
@@ -166,29 +199,99 @@ struct W8Job {
   const __half *bias;  // or null
   __half *Y;
   int64_t M, N;
-  int KC;       // chunks along K
-  int TT;       // token tiles
-  int64_t U;    // units
-  int per;      // chunks of a unit: 1 or KC
-  bool early;   // the kernel before this one does not write W: its loads need not wait
-  bool pairs;   // Y may be written two channels at a time
-  uint32_t *counters;
-  int32_t *parts;
+  int KC;      // chunks along K
+  int TT;      // token tiles
+  int tiles;   // S = 1: of the run that the blocks share
+  int S;
+  bool early;  // the kernel before this one does not write W: its loads need not wait
+  bool wide;   // Y may be written 16 bytes at a time
 };
 
+// A whole tile's accumulator (128 channels from ch0 x NT tokens from m0) once `full` completes: scaled, and written
+// by way of `out`.  Warps 4-11, which go on together or not at all (false).
+template <typename C, int NT>
+__device__ __forceinline__ bool w8_write_tile(const W8Job &a, int64_t ch0, int64_t m0, uint32_t tmem, uint64_t *full,
+                                              uint32_t parity, float *token_scale, uint8_t *out, volatile int *abort) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int half = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+  const int64_t ch = ch0 + r, ch8 = ch0 + (warp & 3) * 32 + (lane & 3) * 8;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), a.M - m0));
+  out += (warp - 4) * (C::kOutCols * 64);
+  for (int j = tid - 128; j < NT; j += 256) token_scale[j] = j < tokens ? a.s_a[m0 + j] : 0.0f;
+  const float sw = ch < a.N ? a.s_w[ch] : 0.0f;
+  const float bias = a.bias && ch < a.N ? __half2float(a.bias[ch]) : 0.0f;
+  if (!named_bar_and(1, 256, mbar_wait(full, parity, abort))) return false;  // also publishes the scales
+  tc_fence_after();
+  const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+#pragma unroll 1
+  for (int j0 = half * (NT / 2); j0 < (half + 1) * (NT / 2) && j0 < tokens; j0 += C::kCols) {
+    uint32_t v[C::kCols];
+    tmem_ld_cols(at + j0, v);
+    tmem_ld_wait();
+    reg_fence(v);
+    const float *scale = token_scale + j0;
+#pragma unroll
+    for (int j = 0; j < C::kCols; j += 4) {
+      const float4 sa = *reinterpret_cast<const float4 *>(scale + j);
+      const float f[4] = {sa.x, sa.y, sa.z, sa.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        v[j + x] = __float_as_uint(fmaf(static_cast<float>(static_cast<int32_t>(v[j + x])) * f[x], sw, bias));
+    }
+    if (a.wide) {
+      // 32 channels of kOutCols tokens at a time; lane = 8 channels of every eighth token
+#pragma unroll
+      for (int j1 = 0; j1 < C::kCols; j1 += C::kOutCols) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < C::kOutCols; ++j)
+          *reinterpret_cast<__half *>(out + j * 64 + lane * 2) = __float2half_rn(__uint_as_float(v[j1 + j]));
+        __syncwarp();
+        __half *to = a.Y + (m0 + j0 + j1 + (lane >> 2)) * a.N + ch8;
+#pragma unroll
+        for (int j = 0; j < C::kOutCols; j += 8)
+          if (j0 + j1 + j + (lane >> 2) < tokens && ch8 < a.N)
+            *reinterpret_cast<uint4 *>(to + j * a.N) =
+                *reinterpret_cast<const uint4 *>(out + (j + (lane >> 2)) * 64 + (lane & 3) * 16);
+      }
+    } else if (ch < a.N) {
+      __half *to = a.Y + (m0 + j0) * a.N + ch;
+#pragma unroll
+      for (int j = 0; j < C::kCols; ++j)
+        if (j0 + j < tokens) to[j * a.N] = __float2half_rn(__uint_as_float(v[j]));
+    }
+  }
+  return true;
+}
+
 template <int NT>
-__global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_constant__ CUtensorMap tm_w,
-                                                             const __grid_constant__ CUtensorMap tm_a, const W8Job a) {
+__global__ void __launch_bounds__(kW8Threads, 2)
+    w8a8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const W8Job a) {
   using C = W8Cfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drained;
-  __shared__ __align__(16) float token_scale[NT];
+  __shared__ __align__(16) float token_scale[2][NT];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
-  __shared__ int join_first, join_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // ---- this block's tiles, and its share of their K
+  int tile0, tile1, k0 = 0, k1 = a.KC;
+  if (a.S > 1) {
+    const int r = static_cast<int>(cluster_rank());
+    tile0 = static_cast<int>(blockIdx.x) / a.S, tile1 = tile0 + 1;
+    k0 = a.KC * r / a.S, k1 = a.KC * (r + 1) / a.S;
+  } else {
+    const int P = gridDim.x, share = a.tiles / P, rest = a.tiles - share * P, c = blockIdx.x;
+    tile0 = share * c + min(c, rest), tile1 = tile0 + share + (c < rest ? 1 : 0);
+  }
+  const int chunks = (tile1 - tile0) * (k1 - k0);
+  const auto weights = [&](int s, const W8Walk &w) {
+    mbar_arrive_expect_tx(&full[s], C::kStage);
+    tma_load_2d(smem + s * C::kStage, &tm_w, &full[s], w.chunk * kW8Chunk, w.rt * kW8Rows);
+  };
+  int ahead = 0;  // chunks whose weights are under way
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -196,71 +299,50 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 128);
+      mbar_init(&acc_empty[i], 256);
     }
     mbar_init(&drained, 1);
     fence_mbar_init();
+    fence_proxy_async_smem();
     abort_flag = 0;
+  }
+  __syncwarp();
+  if (warp == 0 && a.early) {
+    for (W8Walk w(tile0, a.TT, k0, k1); ahead < C::kStages && ahead < chunks; ++ahead, w.next()) {
+      if (elect_one()) weights(ahead, w);
+      __syncwarp();
+    }
   }
   if (warp == 2) {
     tmem_alloc(&tmem_slot, C::kTmem);
     tmem_relinquish();
   }
+  if (tid == 96) prefetch_tmap(&tm_a);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();  // only now: a dependent may take tensor memory as it starts
   const uint32_t tmem = tmem_slot;
 
-  const int P = gridDim.x, c = blockIdx.x;
-  const int64_t share = a.U / P;
-  const int rest = static_cast<int>(a.U - share * P);
-  const auto block_start = [&](int b) { return (share * b + static_cast<int64_t>(rest) * b / P) * a.per; };
-  const int64_t start = block_start(c), end = block_start(c + 1);
-
   if (warp == 0) {
     // ------------------------------------------------------------ loads
-    if (lane == 0) {
-      prefetch_tmap(&tm_w);
-      prefetch_tmap(&tm_a);
-      const int64_t tile0 = start / a.KC;
-      int row_tile = static_cast<int>(tile0 / a.TT), token_tile = static_cast<int>(tile0 - static_cast<int64_t>(row_tile) * a.TT);
-      int kc = static_cast<int>(start - tile0 * a.KC);
-      const auto weights = [&](int s, int rt, int k) {
-        mbar_arrive_expect_tx(&full[s], C::kStage);
-        tma_load_2d(smem + s * C::kStage, &tm_w, &full[s], k * kW8Chunk, rt * kW8Rows);
-      };
-      int ahead = 0;  // chunks whose weights are under way
-      if (a.early) {
-        int rt = row_tile, tt = token_tile, k = kc;
-        for (; ahead < C::kStages && start + ahead < end; ++ahead) {
-          weights(ahead, rt, k);
-          if (++k == a.KC) {
-            k = 0;
-            if (++tt == a.TT) tt = 0, ++rt;
-          }
-        }
+    // The whole warp walks and waits, an elected lane issues: from a one-lane branch a chunk's two copies took
+    // 600 clocks to issue, more than its products.
+    pdl_wait();
+    int s = 0, issued = 0;
+    uint32_t phase = 1;
+    for (W8Walk w(tile0, a.TT, k0, k1); issued < chunks; ++issued, w.next()) {
+      if (issued >= C::kStages && !warp_wait(&empty[s], phase, &abort_flag)) break;
+      if (elect_one()) {
+        if (issued >= ahead) weights(s, w);
+        tma_load_2d(smem + s * C::kStage + C::kStageW, &tm_a, &full[s], w.chunk * kW8Chunk, w.tt * NT);
       }
-      pdl_wait();
-      int s = 0;
-      uint32_t phase = 1;
-      int64_t issued = 0;
-      for (int64_t x = start; x < end; ++x, ++issued) {
-        if (issued >= C::kStages && !mbar_wait(&empty[s], phase, &abort_flag)) break;
-        if (issued >= ahead) weights(s, row_tile, kc);
-        tma_load_2d(smem + s * C::kStage + C::kStageW, &tm_a, &full[s], kc * kW8Chunk, token_tile * NT);
-        if (++s == C::kStages) s = 0, phase ^= 1;
-        if (++kc == a.KC) {
-          kc = 0;
-          if (++token_tile == a.TT) token_tile = 0, ++row_tile;
-        }
-      }
-      if (abort_flag) {  // the last copies into each stage land before the block's memory goes to another
-        for (int i = 0; i < C::kStages && i < issued; ++i) {
-          const int64_t last = (issued - 1 - i) / C::kStages;  // uses of stage i before this one
-          mbar_wait_drain(&full[i], static_cast<uint32_t>(last & 1), 1ll << 24);
-        }
-      }
+      __syncwarp();
+      if (++s == C::kStages) s = 0, phase ^= 1;
+    }
+    if (abort_flag) {  // the last copies into each stage land before the block's memory goes to another
+      for (int i = 0; i < C::kStages && i < issued; ++i)
+        mbar_wait_drain(&full[i], static_cast<uint32_t>((issued - 1 - i) / C::kStages & 1), 1ll << 24);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -269,15 +351,12 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint64_t w_desc = sw128_kmajor_desc(smem_u32(smem)), a_desc = sw128_kmajor_desc(smem_u32(smem) + C::kStageW);
     int s = 0;
-    uint32_t phase = 0, piece = 0;
+    uint32_t phase = 0;
     bool ok = true;
-    for (int64_t x = start; x < end && ok; ++piece) {
-      const int k0 = static_cast<int>(x % a.KC);
-      const int n = static_cast<int>(min(static_cast<int64_t>(a.KC - k0), end - x));
-      x += n;
-      const int acc = piece & 1;
-      ok = warp_wait(&acc_empty[acc], (piece >> 1 & 1) ^ 1, &abort_flag);
-      for (int k = 0; k < n && ok; ++k) {
+    for (int i = 0; i < tile1 - tile0 && ok; ++i) {
+      const int acc = i & 1;
+      ok = warp_wait(&acc_empty[acc], (i >> 1 & 1) ^ 1, &abort_flag);
+      for (int k = k0; k < k1 && ok; ++k) {
         ok = warp_wait(&full[s], phase, &abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -285,9 +364,9 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
           const uint64_t off = static_cast<uint64_t>(s * C::kStage >> 4);
 #pragma unroll
           for (int j = 0; j < kW8Chunk / 32; ++j)
-            mma_i8(tm + acc * NT, w_desc + off + 2 * j, a_desc + off + 2 * j, kIdesc, k > 0 || j > 0);
+            mma_i8(tm + acc * NT, w_desc + off + 2 * j, a_desc + off + 2 * j, kIdesc, k > k0 || j > 0);
           mma_commit(&empty[s]);
-          if (k + 1 == n) mma_commit(&acc_full[acc]);
+          if (k + 1 == k1) mma_commit(&acc_full[acc]);
         }
         __syncwarp();
         if (++s == C::kStages) s = 0, phase ^= 1;
@@ -298,96 +377,73 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
       mbar_wait_drain(&drained, 0, 1ll << 24);
     }
     __syncwarp();
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------ scales and Y: thread = channel of the tile
-    pdl_wait();  // s_a, and the parts' counters
-    const int r = tid - 128;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    uint32_t piece = 0;
-    for (int64_t x = start; x < end; ++piece) {
-      const int64_t tile = x / a.KC;
-      const int k0 = static_cast<int>(x - tile * a.KC);
-      const int n = static_cast<int>(min(static_cast<int64_t>(a.KC - k0), end - x));
-      x += n;
-      const int row_tile = static_cast<int>(tile / a.TT), token_tile = static_cast<int>(tile - static_cast<int64_t>(row_tile) * a.TT);
-      const int64_t ch = static_cast<int64_t>(row_tile) * kW8Rows + r, m0 = static_cast<int64_t>(token_tile) * NT;
-      const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), a.M - m0));
-      named_bar_sync(1, 128);  // everyone is done with the last piece's scales
-      for (int j = r; j < tokens; j += 128) token_scale[j] = a.s_a[m0 + j];
-      const float sw = ch < a.N ? a.s_w[ch] : 0.0f;
-      const float bias = a.bias && ch < a.N ? __half2float(a.bias[ch]) : 0.0f;
-      const int acc = piece & 1;
-      // the four warps go on together or not at all: they meet at barriers below
-      if (!named_bar_and(1, 128, mbar_wait(&acc_full[acc], piece >> 1 & 1, &abort_flag))) break;
-      tc_fence_after();
-      const uint32_t at = tmem + lanes + acc * NT;
-      const bool cut = n < a.KC;
-      bool write = true;
-      int first = c, last = c;
-      if (cut) {
-        // this block's part, then whether it is the last one to arrive
-        int32_t *mine = a.parts + (static_cast<int64_t>(c) * 2 + (k0 == 0 ? 1 : 0)) * C::kPart + r;
-#pragma unroll 1
-        for (int j0 = 0; j0 < tokens; j0 += C::kStep) {
-          uint32_t v[C::kStep];
-          tmem_ld_cols(at + j0, v);
-          tmem_ld_wait();
-          reg_fence(v);
-#pragma unroll
-          for (int j = 0; j < C::kStep; ++j) __stcg(mine + (j0 + j) * kW8Rows, static_cast<int32_t>(v[j]));
-        }
-        named_bar_sync(1, 128);
-        if (r == 0) {
-          // chunk x is in block ((x + 1) P - 1) / U of those with a unit of one chunk each
-          const int64_t t0 = tile * a.KC;
-          join_first = static_cast<int>(((t0 + 1) * P - 1) / a.U);
-          join_last = static_cast<int>(((t0 + a.KC) * P - 1) / a.U);
-          // a block's end cuts one tile at most: the first block of a tile names its counter
-          const uint32_t arrived = atom_add_acq_rel_gpu_u32(a.counters + join_first, 1u);
-          if (arrived == static_cast<uint32_t>(join_last - join_first)) a.counters[join_first] = 0;
-          else join_last = -1;
-        }
-        named_bar_sync(1, 128);
-        first = join_first, last = join_last;
-        write = last >= 0;
-      }
-      if (write) {
-#pragma unroll 1
-        for (int j0 = 0; j0 < tokens; j0 += C::kStep) {
-          uint32_t v[C::kStep];
-          tmem_ld_cols(at + j0, v);
-          tmem_ld_wait();
-          reg_fence(v);
-          for (int b = first; b <= last; ++b) {
-            if (b == c) continue;
-            const int32_t *part = a.parts + (static_cast<int64_t>(b) * 2 + (b == first ? 1 : 0)) * C::kPart + r;
-#pragma unroll
-            for (int j = 0; j < C::kStep; ++j) v[j] += static_cast<uint32_t>(__ldcg(part + (j0 + j) * kW8Rows));
-          }
-          float f[C::kStep];
-#pragma unroll
-          for (int j = 0; j < C::kStep; ++j)
-            f[j] = fmaf(static_cast<float>(static_cast<int32_t>(v[j])) * token_scale[j0 + j], sw, bias);
-          __half *to = a.Y + (m0 + j0) * a.N + ch;
-          if (a.pairs) {
-            // neighbouring lanes swap, so that each writes two channels of every other token
-            const bool odd = lane & 1;
-#pragma unroll
-            for (int j = 0; j < C::kStep; j += 2) {
-              const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? f[j] : f[j + 1], 1);
-              const __half2 h = odd ? __floats2half2_rn(got, f[j + 1]) : __floats2half2_rn(f[j], got);
-              if (j0 + j + odd < tokens && ch < a.N)
-                *reinterpret_cast<__half2 *>(to + (j + odd) * a.N - odd) = h;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < C::kStep; ++j)
-              if (j0 + j < tokens && ch < a.N) to[j * a.N] = __float2half_rn(f[j]);
-          }
-        }
-      }
+  } else if (warp >= 4 && a.S == 1) {
+    // ------------------------------------------------------------ scales and Y
+    pdl_wait();  // s_a
+    for (int tile = tile0, i = 0; tile < tile1; ++tile, ++i) {
+      const int rt = tile / a.TT, tt = tile - rt * a.TT, acc = i & 1;
+      if (!w8_write_tile<C, NT>(a, static_cast<int64_t>(rt) * kW8Rows, static_cast<int64_t>(tt) * NT, tmem + acc * NT,
+                                &acc_full[acc], i >> 1 & 1, token_scale[acc], smem + C::kStages * C::kStage, &abort_flag))
+        break;
       tc_fence_before();
       mbar_arrive(&acc_empty[acc]);
+    }
+  }
+  if (a.S > 1) {
+    // ------------------------------------------------------------ a cluster's parts: thread = channel
+    const int S = a.S, me = static_cast<int>(cluster_rank()), half = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+    const int most = (C::kGroups + S - 1) / S;  // groups of a block
+    const auto first_group = [&](int b) { return (C::kGroups * b + S - 1) / S; };  // owner of group g: g S / kGroups
+    const int rt = tile0 / a.TT, tt = tile0 - rt * a.TT;
+    const int64_t ch = static_cast<int64_t>(rt) * kW8Rows + r, m0 = static_cast<int64_t>(tt) * NT;
+    const int groups = static_cast<int>((min(static_cast<int64_t>(NT), a.M - m0) + 3) / 4);  // with tokens in them
+    bool there = true;
+    if (warp >= 4) there = mbar_wait(&acc_full[0], 0, &abort_flag);
+    __syncwarp();
+    tc_fence_after();
+    cluster_arrive();  // every block is done with its operands: parts take their place
+    cluster_wait();
+    if (warp >= 4 && __all_sync(0xFFFFFFFFu, there)) {
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(me * most * kW8Rows + r) * 16;
+#pragma unroll 1
+      for (int j0 = half * (NT / 2); j0 < (half + 1) * (NT / 2) && j0 < groups * 4; j0 += C::kCols) {
+        uint32_t v[C::kCols];
+        tmem_ld_cols(tmem + lanes + j0, v);
+        tmem_ld_wait();
+        reg_fence(v);
+#pragma unroll
+        for (int j = 0; j < C::kCols; j += 4) {
+          const int g = (j0 + j) / 4, owner = g * S / C::kGroups;
+          const uint32_t at = mine + static_cast<uint32_t>((g - first_group(owner)) * kW8Rows) * 16;
+          st_cluster_v4(cluster_map(at, owner), v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+      }
+    }
+    tc_fence_before();
+    cluster_arrive();
+    cluster_wait();
+    if (warp >= 4) {
+      pdl_wait();  // s_a, and Y's earlier readers
+      const float sw = ch < a.N ? a.s_w[ch] : 0.0f;
+      const float bias = a.bias && ch < a.N ? __half2float(a.bias[ch]) : 0.0f;
+      const int g0 = first_group(me), g1 = min(first_group(me + 1), groups);
+      for (int g = g0 + half; g < g1; g += 2) {
+        const int64_t m = m0 + g * 4;
+        float sa[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sa[x] = m + x < a.M ? a.s_a[m + x] : 0.0f;
+        int4 sum = make_int4(0, 0, 0, 0);
+        const int4 *part = reinterpret_cast<const int4 *>(smem) + (g - g0) * kW8Rows + r;
+        for (int b = 0; b < S; ++b) {
+          const int4 v = part[b * most * kW8Rows];
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        const int p[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (m + x < a.M && ch < a.N) a.Y[(m + x) * a.N + ch] = __float2half_rn(fmaf(static_cast<float>(p[x]) * sa[x], sw, bias));
+      }
     }
   }
   __syncthreads();
@@ -395,52 +451,197 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
+// The same with two blocks on one product (cta_group::2): a tile is 256 channels
+// x NT tokens, each block of a pair loads its 128 channels and half of the
+// tokens, and the pair's tensor cores read both halves.  One block alone is bound
+// by what an SM takes from L2 (some 60 bytes a clock; 128 x 256 tiles ask for 96 at
+// full rate, these for 64).  The loads of both complete on the first block's
+// barriers, its warp 1 issues the products and frees the stages of both.
+// ---------------------------------------------------------------------------
+template <int NT>
+struct W8PairCfg {
+  static constexpr int kStageW = kW8Rows * kW8Chunk, kStageA = NT / 2 * kW8Chunk, kStage = kStageW + kStageA;
+  static constexpr int kCols = 32, kOutCols = 16, kOut = 8 * kOutCols * 32 * 2;
+  static constexpr int kRoom = 224 * 1024 - kOut - 1024 - 2 * NT * 4;
+  static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
+  static constexpr int kSmem = kStages * kStage + kOut + 1024;
+  static constexpr int kTmem = 2 * NT;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kW8Threads, 1)
+    w8a8_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const W8Job a) {
+  using C = W8PairCfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drained;
+  __shared__ __align__(16) float token_scale[2][NT];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int side = static_cast<int>(cluster_rank());
+  const int P = gridDim.x / 2, c = blockIdx.x / 2, share = a.tiles / P, rest = a.tiles - share * P;
+  const int tile0 = share * c + min(c, rest), tile1 = tile0 + share + (c < rest ? 1 : 0);
+  const int chunks = (tile1 - tile0) * a.KC;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 512);
+    }
+    mbar_init(&drained, 1);
+    fence_mbar_init();
+    abort_flag = 0;
+  }
+  if (tid == 96) {
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_a);
+  }
+  __syncwarp();
+  cluster_arrive();
+  if (warp == 2) {
+    tmem_alloc_pair(&tmem_slot, C::kTmem);
+    tmem_relinquish_pair();
+  }
+  cluster_wait();  // both blocks' barriers exist
+  const auto weights = [&](int s, const W8Walk &w) {
+    if (side == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
+    tma_load_2d_pair(smem + s * C::kStage, &tm_w, cluster_map(smem_u32(&full[s]), 0), w.chunk * kW8Chunk,
+                     (2 * w.rt + side) * kW8Rows);
+  };
+  int ahead = 0;  // chunks whose weights are under way
+  if (warp == 0 && a.early) {
+    for (W8Walk w(tile0, a.TT, 0, a.KC); ahead < C::kStages && ahead < chunks; ++ahead, w.next()) {
+      if (elect_one()) weights(ahead, w);
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();  // only now: a dependent may take tensor memory as it starts
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads, each block's own
+    pdl_wait();
+    int s = 0;
+    uint32_t phase = 1;
+    W8Walk w(tile0, a.TT, 0, a.KC);
+    for (int issued = 0; issued < chunks; ++issued, w.next()) {
+      if (issued >= C::kStages && !warp_wait(&empty[s], phase, &abort_flag)) break;
+      if (elect_one()) {
+        if (issued >= ahead) weights(s, w);
+        tma_load_2d_pair(smem + s * C::kStage + C::kStageW, &tm_a, cluster_map(smem_u32(&full[s]), 0),
+                         w.chunk * kW8Chunk, w.tt * NT + side * (NT / 2));
+      }
+      __syncwarp();
+      if (++s == C::kStages) s = 0, phase ^= 1;
+    }
+    __syncwarp();
+  } else if (warp == 1 && side == 0) {
+    // ------------------------------------------------------------ products, for both blocks
+    constexpr uint32_t kIdesc = idesc_i8(2 * kW8Rows, NT);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint64_t w_desc = sw128_kmajor_desc(smem_u32(smem)), a_desc = sw128_kmajor_desc(smem_u32(smem) + C::kStageW);
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int i = 0; i < tile1 - tile0 && ok; ++i) {
+      const int acc = i & 1;
+      ok = warp_wait(&acc_empty[acc], (i >> 1 & 1) ^ 1, &abort_flag);
+      for (int k = 0; k < a.KC && ok; ++k) {
+        ok = warp_wait(&full[s], phase, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t off = static_cast<uint64_t>(s * C::kStage >> 4);
+#pragma unroll
+          for (int j = 0; j < kW8Chunk / 32; ++j)
+            mma_i8_pair(tm + acc * NT, w_desc + off + 2 * j, a_desc + off + 2 * j, kIdesc, k > 0 || j > 0);
+          mma_commit_pair(&empty[s], 3);
+          if (k + 1 == a.KC) mma_commit_pair(&acc_full[acc], 3);
+        }
+        __syncwarp();
+        if (++s == C::kStages) s = 0, phase ^= 1;
+      }
+    }
+    if (!ok && elect_one()) {  // let the products in flight end before tensor memory goes
+      mma_commit_pair(&drained, 1);
+      mbar_wait_drain(&drained, 0, 1ll << 24);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ scales and Y, each block's own channels
+    pdl_wait();  // s_a
+    for (int tile = tile0, i = 0; tile < tile1; ++tile, ++i) {
+      const int rt = tile / a.TT, tt = tile - rt * a.TT, acc = i & 1;
+      if (!w8_write_tile<C, NT>(a, static_cast<int64_t>(2 * rt + side) * kW8Rows, static_cast<int64_t>(tt) * NT,
+                                tmem + acc * NT, &acc_full[acc], i >> 1 & 1, token_scale[acc],
+                                smem + C::kStages * C::kStage, &abort_flag))
+        break;
+      tc_fence_before();
+      mbar_arrive_cluster(cluster_map(smem_u32(&acc_empty[acc]), 0));
+    }
+  }
+  __syncwarp();
+  if (abort_flag) __nanosleep(1000000);  // copies in flight land before the block's memory goes to another
+  __syncthreads();
+  cluster_arrive();  // neither block's barriers and tensor memory are in use any more
+  cluster_wait();
+  if (warp == 2) tmem_dealloc_pair(tmem, C::kTmem);
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 
 struct W8Plan {
-  int NT, KC, TT, per, grid;
-  int64_t U;
+  int NT, KC, TT, S, tiles, grid;
+  bool pair;
 };
 
-static W8Plan w8a8_plan(int64_t M, int64_t N, int64_t K) {
+// False where the tiles and chunks pass 32 bits.
+static bool w8a8_plan(int64_t M, int64_t N, int64_t K, W8Plan *plan) {
   W8Plan p;
-  const int64_t sms = kW8MaxGrid;
-  const int64_t rows = (N + kW8Rows - 1) / kW8Rows;
+  const int64_t sms = device_sm_count();
+  const int64_t rows = (N + kW8Rows - 1) / kW8Rows, pairs = (rows + 1) / 2;
   p.KC = static_cast<int>((K + kW8Chunk - 1) / kW8Chunk);
-  p.NT = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : rows * ((M + 255) / 256) >= sms ? 256 : 128;
-  p.TT = static_cast<int>((M + p.NT - 1) / p.NT);
-  const int64_t tiles = rows * p.TT;
-  // Whole tiles where they fill the GPU in nearly whole rounds, else even shares of chunks.
-  const int64_t rounds = (tiles + sms - 1) / sms;
-  p.per = tiles * 10 >= rounds * sms * 9 ? p.KC : 1;
-  p.U = tiles * p.KC / p.per;
-  p.grid = static_cast<int>(p.U < sms ? p.U : sms);
-  return p;
+  p.NT = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  // Two blocks on a tile where that still leaves 64 of them (N = 4096: 256 tokens 11.7 against 12.3 us, 128 tokens,
+  // which leave 32, 11.6 against 10.4; N = 28672, 128 tokens: 25 against 33 us).  A chunk of 128 tokens takes
+  // some 250 ns, one of 256 some 350: whichever needs less for its rounds (N = 4096: 512 tokens 12.4 against
+  // 15.1 us, 1024 tokens 19.8 against 15.9).
+  const int64_t narrow = pairs * ((M + 127) / 128), broad = pairs * ((M + 255) / 256), slots = sms / 2;
+  p.pair = M > 64 && narrow >= 32;
+  if (p.pair) p.NT = M > 128 && (broad + slots - 1) / slots * 7 < (narrow + slots - 1) / slots * 5 ? 256 : 128;
+  const int64_t TT = (M + p.NT - 1) / p.NT, tiles = (p.pair ? pairs : rows) * TT;
+  if (tiles * p.KC > 0x7FFFFFFF) return false;
+  p.TT = static_cast<int>(TT), p.tiles = static_cast<int>(tiles);
+  p.S = 1;  // shares of K: as many as leave every cluster an SM to be on (N = 6144, one token: 4 8.2 us, 6 11.9 us)
+  if (p.pair) {
+    p.grid = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2) * 2;
+  } else {
+    while (p.S < 4 && tiles * p.S * 2 <= 256 && p.S * 2 <= p.KC) p.S *= 2;
+    p.grid = static_cast<int>(p.S > 1 ? tiles * p.S : tiles < 2 * sms ? tiles : 2 * sms);
+  }
+  *plan = p;
+  return true;
 }
 
-constexpr size_t kW8CounterBytes = 4096;
-static_assert(kW8MaxGrid * sizeof(uint32_t) <= kW8CounterBytes, "one counter per block");
-
-// Room for two parts of every block at the widest tile that up to M tokens take: enough for fewer tokens, too.
-size_t w8a8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (M == 0 || N == 0) return 0;
-  const int64_t widest = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  return kW8CounterBytes + static_cast<size_t>(kW8MaxGrid) * 2 * kW8Rows * widest * sizeof(int32_t);
-}
-
-// The layer from fp16 adds the codes and scales of its activations.
+// The layer from fp16 keeps the codes and scales of its activations.
 size_t w8a8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M == 0 || N == 0) return 0;
-  const size_t codes = (static_cast<size_t>(M) * K + 255) / 256 * 256;
-  return w8a8_gemm_workspace_bytes(M, N, K) + codes + (static_cast<size_t>(M) * 4 + 255) / 256 * 256;
+  return (static_cast<size_t>(M) * K + 255) / 256 * 256 + (static_cast<size_t>(M) * 4 + 255) / 256 * 256;
 }
 
-template <int NT>
-static cudaError_t launch_w8a8_type(const W8A8Args &a, const W8Plan &p, const CUtensorMap &tm_w, const CUtensorMap &tm_a,
-                                    bool early, cudaStream_t stream, const char **msg) {
-  using C = W8Cfg<NT>;
-  auto kern = w8a8_kernel<NT>;
+template <typename C, typename Kernel>
+static cudaError_t launch_w8a8_type(Kernel kern, const W8A8Args &a, const W8Plan &p, const CUtensorMap &tm_w,
+                                    const CUtensorMap &tm_a, bool early, cudaStream_t stream, const char **msg) {
   static std::atomic<unsigned long long> configured{0};  // one bit per device ordinal
   int dev = 0;
   cudaGetDevice(&dev);
@@ -452,46 +653,53 @@ static cudaError_t launch_w8a8_type(const W8A8Args &a, const W8Plan &p, const CU
     }
     if (dev < 64) configured.fetch_or(1ull << dev);
   }
-  const bool pairs = a.N % 2 == 0 && (reinterpret_cast<uintptr_t>(a.Y) & 3) == 0;
-  const W8Job job{a.s_a, a.s_w, a.bias, a.Y, a.M, a.N, p.KC, p.TT, p.U, p.per, early, pairs,
-                  static_cast<uint32_t *>(a.ws), reinterpret_cast<int32_t *>(static_cast<uint8_t *>(a.ws) + kW8CounterBytes)};
-  cudaLaunchAttribute attr[1];
+  const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.Y) & 15) == 0;
+  const W8Job job{a.s_a, a.s_w, a.bias, a.Y, a.M, a.N, p.KC, p.TT, p.tiles, p.S, early, wide};
+  const int cluster = p.pair ? 2 : p.S;
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // starts while the kernel before it ends
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
   cfg.blockDim = dim3(kW8Threads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm_w, tm_a, job);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) *msg = "launch of the 8-bit product failed";
   return e;
 }
 
-// `early`: the kernel before this one on the stream is the quantizer, behind everything that came before.
+// `early`: the kernel before this one on the stream is the quantizer, which starts behind all that came before.
 static cudaError_t launch_w8a8(const W8A8Args &a, bool early, cudaStream_t stream, const char **msg) {
   auto enc = get_encode_fn();
   if (!enc) {
     *msg = "cuTensorMapEncodeTiled is not available from the driver";
     return cudaErrorNotSupported;
   }
-  const W8Plan p = w8a8_plan(a.M, a.N, a.K);
+  W8Plan p;
+  if (!w8a8_plan(a.M, a.N, a.K, &p)) {
+    *msg = "the product's tiles x chunks of K pass 2^31";
+    return cudaErrorNotSupported;
+  }
   CUtensorMap tm_w, tm_a;
   if (!encode_2d_u8_uncached(enc, &tm_w, a.W, a.K, a.N, kW8Chunk, kW8Rows, true) ||
-      !encode_2d_u8_uncached(enc, &tm_a, a.A_q, a.K, a.M, kW8Chunk, p.NT, true)) {
+      !encode_2d_u8_uncached(enc, &tm_a, a.A_q, a.K, a.M, kW8Chunk, p.pair ? p.NT / 2 : p.NT, true)) {
     *msg = "tensor map encoding of W or A_q failed";
     return cudaErrorInvalidValue;
   }
-  switch (p.NT) {
-    case 16: return launch_w8a8_type<16>(a, p, tm_w, tm_a, early, stream, msg);
-    case 32: return launch_w8a8_type<32>(a, p, tm_w, tm_a, early, stream, msg);
-    case 64: return launch_w8a8_type<64>(a, p, tm_w, tm_a, early, stream, msg);
-    case 128: return launch_w8a8_type<128>(a, p, tm_w, tm_a, early, stream, msg);
-    default: return launch_w8a8_type<256>(a, p, tm_w, tm_a, early, stream, msg);
-  }
+  if (p.pair)
+    return p.NT == 256
+               ? launch_w8a8_type<W8PairCfg<256>>(w8a8_pair_kernel<256>, a, p, tm_w, tm_a, early, stream, msg)
+               : launch_w8a8_type<W8PairCfg<128>>(w8a8_pair_kernel<128>, a, p, tm_w, tm_a, early, stream, msg);
+  if (p.NT == 16) return launch_w8a8_type<W8Cfg<16>>(w8a8_kernel<16>, a, p, tm_w, tm_a, early, stream, msg);
+  if (p.NT == 32) return launch_w8a8_type<W8Cfg<32>>(w8a8_kernel<32>, a, p, tm_w, tm_a, early, stream, msg);
+  return launch_w8a8_type<W8Cfg<64>>(w8a8_kernel<64>, a, p, tm_w, tm_a, early, stream, msg);
 }
 
 cudaError_t launch_w8a8_pack(const float *W, int64_t N, int64_t K, int8_t *codes, float *s_w, cudaStream_t stream) {
@@ -504,12 +712,13 @@ cudaError_t launch_w8a8_quantize(const __half *X, int64_t stride, int64_t M, int
 cudaError_t launch_w8a8_gemm(const W8A8Args &a, cudaStream_t stream, const char **msg) {
   return launch_w8a8(a, false, stream, msg);
 }
-cudaError_t launch_w8a8_linear(const __half *X, int64_t stride, W8A8Args a, cudaStream_t stream, const char **msg) {
-  uint8_t *codes = static_cast<uint8_t *>(a.ws) + w8a8_gemm_workspace_bytes(a.M, a.N, a.K);
+cudaError_t launch_w8a8_linear(const __half *X, int64_t stride, W8A8Args a, void *ws, cudaStream_t stream,
+                               const char **msg) {
+  int8_t *codes = static_cast<int8_t *>(ws);
   float *s_a = reinterpret_cast<float *>(codes + (static_cast<size_t>(a.M) * a.K + 255) / 256 * 256);
-  a.A_q = reinterpret_cast<const int8_t *>(codes);
+  a.A_q = codes;
   a.s_a = s_a;
-  cudaError_t e = launch_w8a8_quantize(X, stride, a.M, a.K, reinterpret_cast<int8_t *>(codes), s_a, stream);
+  cudaError_t e = launch_w8a8_quantize(X, stride, a.M, a.K, codes, s_a, stream);
   if (e != cudaSuccess) {
     *msg = "launch of the activations' quantizer failed";
     return e;

@@ -67,39 +67,35 @@ def w8a8_quantize(X, stream=None):
     return A_q, s_a
 
 
-def w8a8_workspace_bytes(M: int, K: int, N: int, from_f16: bool = True) -> int:
+def w8a8_linear_workspace_bytes(M: int, K: int, N: int) -> int:
     out = ctypes.c_size_t(0)
-    _lib._check(_lib.load().mixllm_w8a8_workspace_bytes(M, K, N, from_f16, ctypes.byref(out)),
-                "mixllm_w8a8_workspace_bytes")
+    _lib._check(_lib.load().mixllm_w8a8_linear_workspace_bytes(M, K, N, ctypes.byref(out)),
+                "mixllm_w8a8_linear_workspace_bytes")
     return out.value
 
 
-def w8a8_linear_workspace(M: int, p: W8Weights, from_f16: bool = True) -> torch.Tensor:
-    """A zero-filled workspace for w8a8_linear_into with up to M tokens, or with
-    from_f16=False for w8a8_gemm_into (calls leave its counters at zero; calls
-    that overlap in time must not share one).  Filled on the current stream: a
-    first call on another has to wait for it."""
-    n = w8a8_workspace_bytes(M, p.K, p.N, from_f16)
-    return torch.zeros(max(256, n), dtype=torch.uint8, device=p.device)
+def w8a8_linear_workspace(M: int, p: W8Weights) -> torch.Tensor:
+    """A workspace for w8a8_linear_into with up to M tokens (calls that overlap
+    in time must not share one; it needs no initial value)."""
+    n = w8a8_linear_workspace_bytes(M, p.K, p.N)
+    return torch.empty(max(256, n), dtype=torch.uint8, device=p.device)
 
 
-def _product(fn, head, M, p, Y, workspace, bias, stream):
-    dev = p.index
-    need(Y, "Y", _F16, (M, p.N), dev)
-    need(workspace, "workspace", torch.uint8, (workspace.shape[0],), dev)
+def _checked(M, p, Y, bias):
+    need(Y, "Y", _F16, (M, p.N), p.index)
     if bias is not None:
-        need(bias, "bias", _F16, (p.N,), dev)
-    call(fn, dev, stream, *head, M, p.K, ptr(p.codes), ptr(p.s_w), p.N, ptr(bias), ptr(Y), ptr(workspace),
-         workspace.shape[0])
+        need(bias, "bias", _F16, (p.N,), p.index)
 
 
-def w8a8_gemm_into(A_q, s_a, p: W8Weights, Y, workspace, bias=None, stream=None):
+def w8a8_gemm_into(A_q, s_a, p: W8Weights, Y, bias=None, stream=None):
     """Y fp16 [M, N] from A_q int8 [M, K] and s_a fp32 [M] (mixllm_w8a8_gemm);
     bias fp16 [N] or None."""
     M = A_q.shape[0]
     need(A_q, "A_q", _I8, (M, p.K), p.index)
     need(s_a, "s_a", _F32, (M,), p.index)
-    _product("mixllm_w8a8_gemm", (ptr(A_q), ptr(s_a)), M, p, Y, workspace, bias, stream)
+    _checked(M, p, Y, bias)
+    call("mixllm_w8a8_gemm", p.index, stream, ptr(A_q), ptr(s_a), M, p.K, ptr(p.codes), ptr(p.s_w), p.N, ptr(bias),
+         ptr(Y))
 
 
 def w8a8_linear_into(X, p: W8Weights, Y, workspace, bias=None, stream=None):
@@ -107,7 +103,10 @@ def w8a8_linear_into(X, p: W8Weights, Y, workspace, bias=None, stream=None):
     the way (mixllm_w8a8_linear); bias fp16 [N] or None."""
     M = X.shape[0]
     stride = rows(X, "X", _F16, (M, p.K), p.index)
-    _product("mixllm_w8a8_linear", (ptr(X), stride), M, p, Y, workspace, bias, stream)
+    _checked(M, p, Y, bias)
+    need(workspace, "workspace", torch.uint8, (workspace.shape[0],), p.index)
+    call("mixllm_w8a8_linear", p.index, stream, ptr(X), stride, M, p.K, ptr(p.codes), ptr(p.s_w), p.N, ptr(bias),
+         ptr(Y), ptr(workspace), workspace.shape[0])
 
 
 def w8a8_linear(X, p: W8Weights, bias=None, workspace=None, stream=None) -> torch.Tensor:
