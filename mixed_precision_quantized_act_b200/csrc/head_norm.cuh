@@ -98,30 +98,54 @@ struct HeadTurn {
 };
 
 // One block takes 256 / (D / 8) tokens and `per` heads of queries or of keys; a
-// lane loads four heads ahead.
+// lane loads four heads ahead, the first ones before it knows its position.
 constexpr int kHeadThreads = 256, kHeadsAhead = 4;
 
-// One kind's rows of one token: heads h0 .. h_end of src, into dst.
 template <int D>
-__device__ __forceinline__ void turn_heads(const HeadTurn<D> &turn, const __half *src, __half *dst, int h0, int h_end,
-                                           float eps) {
-  const int c0 = threadIdx.x % HeadTurn<D>::kLanes * 8;
-  for (int h = h0; h < h_end; h += kHeadsAhead) {
-    uint4 ahead[kHeadsAhead];
-#pragma unroll
-    for (int x = 0; x < kHeadsAhead; ++x)
-      if (h + x < h_end) ahead[x] = *reinterpret_cast<const uint4 *>(src + (h + x) * D + c0);
-#pragma unroll
-    for (int x = 0; x < kHeadsAhead; ++x)
-      if (h + x < h_end) *reinterpret_cast<uint4 *>(dst + (h + x) * D + c0) = turn.apply(ahead[x], eps);
+struct HeadRows {
+  const __half *src;
+  __half *dst;
+  int h, h_end;
+  uint4 ahead[kHeadsAhead];
+
+  // heads h0 .. end of one token, rows of src into dst
+  __device__ __forceinline__ void start(const __half *from, __half *to, int h0, int end) {
+    const int c0 = threadIdx.x % (D / 8) * 8;
+    src = from + c0, dst = to + c0, h = h0, h_end = end;
+    load();
   }
-}
+  __device__ __forceinline__ void load() {
+#pragma unroll
+    for (int x = 0; x < kHeadsAhead; ++x)
+      if (h + x < h_end) ahead[x] = *reinterpret_cast<const uint4 *>(src + (h + x) * D);
+  }
+  __device__ __forceinline__ void run(const HeadTurn<D> &turn, float eps) {
+    while (true) {
+#pragma unroll
+      for (int x = 0; x < kHeadsAhead; ++x)
+        if (h + x < h_end) *reinterpret_cast<uint4 *>(dst + (h + x) * D) = turn.apply(ahead[x], eps);
+      h += kHeadsAhead;
+      if (h >= h_end) return;
+      load();
+    }
+  }
+};
 
 template <int D>
-__global__ void __launch_bounds__(kHeadThreads) head_norm_rope_kernel(const HeadArgs a, int per, int q_groups) {
+__global__ void __launch_bounds__(kHeadThreads, 4) head_norm_rope_kernel(const HeadArgs a, int per, int q_groups) {
   constexpr int kLanes = D / 8;
+  pdl_launch_dependents();
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kHeadThreads / kLanes) + threadIdx.x / kLanes;
   if (t >= a.T) return;
+  const bool key = static_cast<int>(blockIdx.y) >= q_groups;
+  const int g = key ? blockIdx.y - q_groups : blockIdx.y, heads = key ? a.H : a.Hq;
+  HeadRows<D> rows;
+  rows.start(key ? a.k + t * a.k_stride : a.q + t * a.q_stride,
+             key ? a.k_out + t * a.k_out_stride : a.q_out + t * a.q_out_stride, g * per, min(heads, (g + 1) * per));
+  if (a.slots) {  // the cache's append: what it skips for keys
+    const int64_t slot = a.slots[t];
+    if (slot < 0 || slot >= a.limit) return;
+  }
   const float *angle = nullptr;
   if (a.rope) {
     const int64_t pos = a.positions[t];
@@ -132,22 +156,18 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_rope_kernel(const Head
     }
     angle = a.rope + pos * a.rotary;
   }
-  const bool key = static_cast<int>(blockIdx.y) >= q_groups;
-  const int g = key ? blockIdx.y - q_groups : blockIdx.y, heads = key ? a.H : a.Hq;
   HeadTurn<D> turn;
   turn.start(angle, a.rotary, key ? a.w_k : a.w_q);
-  turn_heads<D>(turn, key ? a.k + t * a.k_stride : a.q + t * a.q_stride,
-                key ? a.k_out + t * a.k_out_stride : a.q_out + t * a.q_out_stride, g * per, min(heads, (g + 1) * per),
-                a.eps);
+  rows.run(turn, a.eps);
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 
-// Heads of one lane: eight where the call fills the GPU all the same, one where it is latency that counts.
+// Heads of one lane: sixteen where the call fills the GPU all the same, one where it is latency that counts.
 static int turn_heads_per_lane(int64_t T, int heads, int D) {
-  int per = T * heads * (D / 8) >= 8ll * 148 * 2048 ? 8 : 1;
+    int per = T * heads * (D / 8) >= 8ll * 148 * 2048 ? 16 : 1;
   while ((heads + per - 1) / per > 65535 / 2) ++per;
   return per;
 }

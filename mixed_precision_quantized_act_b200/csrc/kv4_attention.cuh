@@ -95,6 +95,8 @@ struct KvCfg {
   static constexpr int kWarps = D * NT <= 128 ? 16 : 8;  // by registers: 128 and 255 a thread
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NT;
+  static constexpr int kLeast = 2;  // units of a warp
+  static constexpr bool kWholeHeads = false;
   static constexpr int kRowBytes = D / 2;
   static constexpr int kCodes = 32 * kRowBytes;  // bytes of 32 tokens' key (or value) codes
   static constexpr int kStage = 2 * (kCodes + 32 * 4);

@@ -207,7 +207,11 @@ struct Pm4 {
   using Args = AttendArgs;
   static constexpr int kVec = D / 32;  // 16-byte loads of a row's codes
   static constexpr int kIssueRegs = 64, kUnpackRegs = 96;  // of a thread; with 2 x 176 of the softmax, 4 x 128
+  // thread = token; r: its row, or -1
   static __device__ __forceinline__ uint32_t load(const Kv4Cache &c, int64_t r, uint4 (&codes)[kVec]) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) codes[i] = make_uint4(0, 0, 0, 0);
+    if (r < 0) return 0;
     const uint4 *src = reinterpret_cast<const uint4 *>(c.codes + r * (D / 2));
 #pragma unroll
     for (int i = 0; i < kVec; ++i) codes[i] = src[i];
@@ -216,16 +220,21 @@ struct Pm4 {
   static __device__ __forceinline__ float scale(uint32_t meta) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&meta)).x;
   }
-  // chunk k (eight channels) of the row goes to put(k, eight fp16 values)
-  template <typename Put>
-  static __device__ __forceinline__ void unpack(const uint4 (&codes)[kVec], uint32_t meta, const Put &put) {
+  // into the rows of an operand's 128 tokens at `to`
+  static __device__ __forceinline__ void store(uint8_t *to, const uint4 (&codes)[kVec], uint32_t meta) {
     const uint32_t z = meta >> 16 & 15u;
     const uint32_t zlo = 0xE400E400u | z * 0x00010001u, zhi = 0xD400D400u | z * 0x00100010u;
+    const int tk = threadIdx.x & 127;
+    uint8_t *line = to + tk * 128;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const uint32_t words[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) put(4 * i + j, unpack_codes(words[j], zlo, zhi));
+      for (int j = 0; j < 4; ++j) {
+        const int chunk = 4 * i + j;
+        *reinterpret_cast<uint4 *>(line + (chunk >> 3) * PmCfg<D>::kPanel + (((chunk & 7) ^ (tk & 7)) << 4)) =
+            unpack_codes(words[j], zlo, zhi);
+      }
     }
   }
   // eight channels in order -> 0 4 1 5 2 6 3 7
@@ -418,22 +427,13 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typenam
           record_status(kStatusBounds);
       }
     };
-    const auto load = [&](int64_t r, uint4 (&codes)[kVec], uint32_t &meta) {
-      meta = 0;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) codes[i] = make_uint4(0, 0, 0, 0);
-      if (r >= 0) meta = F::load(a.cache, r, codes);
-    };
     const auto store = [&](uint8_t *to, const uint4 (&codes)[kVec], uint32_t meta) {
-      uint8_t *line = to + tk * 128;
-      F::unpack(codes, meta, [&](int chunk, const uint4 v) {
-        *reinterpret_cast<uint4 *>(line + (chunk >> 3) * kPanel + (((chunk & 7) ^ (tk & 7)) << 4)) = v;
-      });
+      F::store(to, codes, meta);
       fence_proxy_async_smem();
     };
     look_up();
-    load(row, kr, km);
-    load(row < 0 ? row : row + to_value, vr, vm);
+    km = F::load(a.cache, row, kr);
+    vm = F::load(a.cache, row < 0 ? row : row + to_value, vr);
     bool ok_now = page_ok;
     for (uint32_t it = 0; left > 0; --left, ++it) {
       const int s = it & 1;
@@ -463,11 +463,11 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typenam
       }
       store(k_s + s * kOperand, kr, km);
       mbar_arrive(&k_full[s]);
-      if (left > 1) load(row, kr, km);
+      if (left > 1) km = F::load(a.cache, row, kr);
       if (!mbar_wait(&v_empty[s], phase ^ 1, &abort_flag)) break;
       store(v_s + s * kOperand, vr, vm);
       mbar_arrive(&v_full[s]);
-      if (left > 1) load(row < 0 ? row : row + to_value, vr, vm);
+      if (left > 1) vm = F::load(a.cache, row < 0 ? row : row + to_value, vr);
       ok_now = next_ok;
     }
   } else {

@@ -57,6 +57,8 @@ struct Kv8Cfg {
   static constexpr int kWarps = 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NT;
+  static constexpr int kLeast = 1;  // units of a warp
+  static constexpr bool kWholeHeads = true;
   static constexpr int kCodes = 32 * D;  // bytes of 32 tokens' key (or value) codes
   static constexpr int kStage = 2 * kCodes + 16;  // and two blocks' (key, value) scales
   static constexpr int kStages = D == 128 ? 3 : 5;
@@ -389,21 +391,37 @@ struct Pm8 {
   using Args = Attend8Args;
   static constexpr int kVec = D / 16;  // 16-byte loads of a row's codes
   static constexpr int kIssueRegs = 48, kUnpackRegs = 112;  // a key's and a value's codes are held at once
+  // A row's 16-byte pieces are neighbouring lanes' (each lane a row of its own took 32 lines a load): lane l has
+  // piece l % kVec of rows l / kVec, + 32 / kVec, .. of the warp's 32.  `row` is the lane's token's, or -1; a block of
+  // 16 tokens lies in one page, so its rows follow on its first one's, seen or not.
   static __device__ __forceinline__ uint32_t load(const Kv8Cache &c, int64_t r, uint4 (&codes)[kVec]) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(c.codes + r * D);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) codes[i] = src[i];
-    return __float_as_uint(c.scales[r >> 4]);
-  }
-  static __device__ __forceinline__ float scale(uint32_t meta) { return __uint_as_float(meta); }
-  template <typename Put>
-  static __device__ __forceinline__ void unpack(const uint4 (&codes)[kVec], uint32_t, const Put &put) {
+    const int lane = threadIdx.x & 31;
+    const int64_t first[2] = {__shfl_sync(0xFFFFFFFFu, r, 0), __shfl_sync(0xFFFFFFFFu, r, 16)};
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      put(2 * i, make_uint4(codes_f16(codes[i].x, kLowPair), codes_f16(codes[i].x, kHighPair),
-                            codes_f16(codes[i].y, kLowPair), codes_f16(codes[i].y, kHighPair)));
-      put(2 * i + 1, make_uint4(codes_f16(codes[i].z, kLowPair), codes_f16(codes[i].z, kHighPair),
-                                codes_f16(codes[i].w, kLowPair), codes_f16(codes[i].w, kHighPair)));
+      const int64_t from = first[i >= kVec / 2];
+      const int row = (i % (kVec / 2)) * (32 / kVec) + lane / kVec;
+      codes[i] = from >= 0 ? *reinterpret_cast<const uint4 *>(c.codes + (from + row) * D + lane % kVec * 16)
+                           : make_uint4(0, 0, 0, 0);
+    }
+    return r >= 0 ? __float_as_uint(c.scales[r >> 4]) : 0u;
+  }
+  static __device__ __forceinline__ float scale(uint32_t meta) { return __uint_as_float(meta); }
+  static __device__ __forceinline__ void store(uint8_t *to, const uint4 (&codes)[kVec], uint32_t) {
+    const int lane = threadIdx.x & 31, piece = lane % kVec;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int tk = (threadIdx.x & 96) + i * (32 / kVec) + lane / kVec;
+      const uint4 low = make_uint4(codes_f16(codes[i].x, kLowPair), codes_f16(codes[i].x, kHighPair),
+                                   codes_f16(codes[i].y, kLowPair), codes_f16(codes[i].y, kHighPair));
+      const uint4 high = make_uint4(codes_f16(codes[i].z, kLowPair), codes_f16(codes[i].z, kHighPair),
+                                    codes_f16(codes[i].w, kLowPair), codes_f16(codes[i].w, kHighPair));
+      // the second panel's lanes begin with their second half: eight lanes then meet all banks
+      const bool swap = piece >= 4;
+      uint8_t *line = to + tk * 128 + (piece >> 2) * PmCfg<D>::kPanel;
+      const int chunk = (2 * piece & 7) ^ (tk & 7);
+      *reinterpret_cast<uint4 *>(line + ((chunk ^ (swap ? 1 : 0)) << 4)) = swap ? high : low;
+      *reinterpret_cast<uint4 *>(line + ((chunk ^ (swap ? 0 : 1)) << 4)) = swap ? low : high;
     }
   }
   static __device__ __forceinline__ uint4 order(const uint4 v) { return v; }

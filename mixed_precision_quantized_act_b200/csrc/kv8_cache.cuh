@@ -20,9 +20,9 @@ namespace mixllm {
 constexpr int kKv8Block = 16;  // tokens of one scale
 
 // ---------------------------------------------------------------------------
-// Append.  A block of 16 tokens shares a scale, so its tokens are one warp's
-// work: the warp takes a run of new tokens of one block (neighbours in the list
-// of slots) for one head, key or value, keeps their rows in registers, and
+// Append.  A block of 16 tokens shares a scale, so its tokens are two warps'
+// work: they take a run of new tokens of one block (neighbours in the list of
+// slots) for one head, key or value, keep their rows in registers, and
 //   s = max(s before, amax / 127)   (before: 0 where the run holds the block's first row)
 //   code = 128 + rne(x / s), and where s has grown the block's other rows are
 //   re-coded: 128 + rne((code - 128) * (s before / s)).
@@ -46,90 +46,98 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
   return r;
 }
 
-// One run's rows of one head, key (kv = 0) or value: the whole warp.  Lane i's
-// `slot` is that of token t0 + i, or -1.
+// What the two warps of a run tell each other: the largest magnitude of their rows
+// (infinity where one is not finite) and the rows themselves, bit by row.
+struct Kv8Half {
+  float amax;
+  uint32_t rows;
+};
+
+// One run's rows of one head, key (kv = 0) or value: two warps, eight tokens each.
+// Lane i's `slot` and `pos` are those of token t0 + i (slot -1: none).  What depends
+// on slot and position alone is loaded before anything is used.
 template <int D>
 __device__ __forceinline__ void kv8_write_run(const Kv8AppendArgs &a, const HeadArgs &heads, int64_t t0, int64_t slot,
-                                              int first, int count, int kv, int h) {
-  constexpr int kLanes = D / 8, kTogether = 32 / kLanes, kPasses = kKv8Block / kTogether;
-  const int lane = threadIdx.x & 31, sub = lane % kLanes, in = lane / kLanes;
+                                              int pos, int first, int count, int kv, int h, Kv8Half *halves) {
+  constexpr int kLanes = D / 8, kTogether = 32 / kLanes, kPasses = kKv8Block / 2 / kTogether;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % kLanes;
+  const int mine = (warp & 1) * (kKv8Block / 2) + lane / kLanes;  // of the run's tokens, this lane's first
   const int64_t block = __shfl_sync(0xFFFFFFFFu, slot, first) >> 4;
-  // ---- the rows, normalized and rotated
-  uint4 x[kPasses];
-  uint32_t rows = 0;  // of the block, bit by row, that are written
-  int row_of[kPasses];
-  float amax = 0.0f;
-  bool odd = false;
+  const int64_t base = kv8_row(a.cache, block << 4, kv, h);
+  float *scale = a.cache.scales + (base >> 4);
+  const float old_scale = *scale;
   const __half *src = kv ? heads.v + t0 * heads.v_stride : heads.k + t0 * heads.k_stride;
   const int64_t stride = kv ? heads.v_stride : heads.k_stride;
+  uint4 x[kPasses];
+  int row_of[kPasses];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int j = p * kTogether + in;
+    const int j = mine + p * kTogether;
     row_of[p] = static_cast<int>(__shfl_sync(0xFFFFFFFFu, slot, (first + j) & 31)) & (kKv8Block - 1);
     x[p] = make_uint4(0, 0, 0, 0);
     if (j < count) x[p] = *reinterpret_cast<const uint4 *>(src + (first + j) * stride + h * D + sub * 8);
     else row_of[p] = -1;
   }
+  // ---- the rows, normalized and rotated
+  uint32_t rows = 0;
+  float amax = 0.0f;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    if (p * kTogether >= count) continue;  // the same for the whole warp
+    if ((warp & 1) * (kKv8Block / 2) + p * kTogether >= count) continue;  // the same for the whole warp
+    const int at = __shfl_sync(0xFFFFFFFFu, pos, (first + mine + p * kTogether) & 31);
+    if (heads.rope && row_of[p] >= 0 && (at < 0 || at >= heads.max_pos)) {
+      if (kv == 0 && sub == 0) record_status(kStatusBounds);
+      row_of[p] = -1;  // a value is skipped where its key is
+    }
     if (kv == 0 && (heads.rope || heads.w_k)) {
-      const int j = p * kTogether + in;
-      const float *angle = nullptr;
-      if (heads.rope && row_of[p] >= 0) {
-        const int64_t pos = heads.positions[t0 + first + j];
-        if (pos < 0 || pos >= heads.max_pos) {
-          if (sub == 0) record_status(kStatusBounds);
-          row_of[p] = -1;
-          x[p] = make_uint4(0, 0, 0, 0);
-        } else {
-          angle = heads.rope + pos * heads.rotary;
-        }
-      }
       HeadTurn<D> turn;
-      turn.start(angle, heads.rotary, heads.w_k);
+      turn.start(heads.rope && row_of[p] >= 0 ? heads.rope + static_cast<int64_t>(at) * heads.rotary : nullptr,
+                 heads.rotary, heads.w_k);
       turn.any = heads.rope != nullptr;  // every lane takes part in the exchange
       x[p] = turn.apply(x[p], heads.eps);
-    } else if (heads.rope && row_of[p] >= 0) {  // a value is skipped where its key is
-      const int64_t pos = heads.positions[t0 + first + p * kTogether + in];
-      if (pos < 0 || pos >= heads.max_pos) row_of[p] = -1;
     }
     if (row_of[p] >= 0) {
       rows |= 1u << row_of[p];
-      float f[8];
-      widen8(x[p], f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        amax = fmaxf(amax, fabsf(f[i]));
-        odd |= !(fabsf(f[i]) <= 65504.0f);
-      }
+      const __half2 *h2 = reinterpret_cast<const __half2 *>(&x[p]);
+      const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(h2[0]), __habs2(h2[1])), __hmax2_nan(__habs2(h2[2]), __habs2(h2[3])));
+      const float top = __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+      amax = fmaxf(amax, top <= 65504.0f ? top : INFINITY);
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
   rows = __reduce_or_sync(0xFFFFFFFFu, rows);
-  odd = __any_sync(0xFFFFFFFFu, odd);
+  if (lane == 0) halves[warp] = Kv8Half{amax, rows};
+  named_bar_sync(1 + (warp >> 1), 64);  // also: both have read the scale
+  const Kv8Half other = halves[warp ^ 1];
+  named_bar_sync(1 + (warp >> 1), 64);  // before either writes its next run's
+  amax = fmaxf(amax, other.amax);
+  rows |= other.rows;
   if (rows == 0) return;
   // ---- the scale
-  const int64_t base = kv8_row(a.cache, block << 4, kv, h);
-  float *scale = a.cache.scales + (base >> 4);
   const bool anew = rows & 1u;
-  const float before = anew ? 0.0f : *scale;
+  const float before = anew ? 0.0f : old_scale;
   float s = fmaxf(before, __fdiv_rn(amax, 127.0f));
-  if (odd || before != before) s = __int_as_float(0x7FFFFFFF);
-  __syncwarp();  // every lane has read the scale
-  if (lane == 0) *scale = s;
+  if (amax == INFINITY || before != before) s = __int_as_float(0x7FFFFFFF);
+  if (lane == 0 && (warp & 1) == 0) *scale = s;
   uint8_t *codes = a.cache.codes + base * D;
   if (s > before && !anew) {
-    // the older rows: 16 bytes a lane and step
+    // the older rows, eight a warp: 16 bytes a lane and step
     const float ratio = __fdiv_rn(before, s);
+    constexpr int kSteps = kKv8Block / 2 * D / 512;
+    const int from = (warp & 1) * (kKv8Block / 2 * D);
+    uint4 old[kSteps];
 #pragma unroll
-    for (int i = 0; i < kKv8Block * D / 512; ++i) {
-      const int at = (i * 32 + lane) * 16;
+    for (int i = 0; i < kSteps; ++i) {
+      const int at = from + (i * 32 + lane) * 16;
+      if (!(rows >> (at / D) & 1u)) old[i] = *reinterpret_cast<const uint4 *>(codes + at);
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int at = from + (i * 32 + lane) * 16;
       if (rows >> (at / D) & 1u) continue;
-      uint4 *p = reinterpret_cast<uint4 *>(codes + at);
-      const uint4 c = *p;
-      *p = make_uint4(recode4(c.x, ratio), recode4(c.y, ratio), recode4(c.z, ratio), recode4(c.w, ratio));
+      *reinterpret_cast<uint4 *>(codes + at) = make_uint4(recode4(old[i].x, ratio), recode4(old[i].y, ratio),
+                                                          recode4(old[i].z, ratio), recode4(old[i].w, ratio));
     }
   }
   // ---- the new rows
@@ -153,11 +161,11 @@ struct Kv8Grid {
   unsigned q_blocks, q_groups;  // blocks of queries; groups of `per` heads
   int per;
   unsigned groups;  // of `pairs` (head, kind) pairs
-  int pairs;
+  int pairs, split;  // split: blocks that share a group's runs
 };
 
 template <int D>
-__global__ void __launch_bounds__(kHeadThreads) kv8_append_kernel(const Kv8AppendArgs a, const HeadArgs heads,
+__global__ void __launch_bounds__(kHeadThreads, 3) kv8_append_kernel(const Kv8AppendArgs a, const HeadArgs heads,
                                                                   const Kv8Grid grid) {
   constexpr int kLanes = D / 8;
   const int64_t limit = a.cache.pages << a.cache.page_log2;
@@ -166,6 +174,9 @@ __global__ void __launch_bounds__(kHeadThreads) kv8_append_kernel(const Kv8Appen
     const unsigned tile = blockIdx.x / grid.q_groups, g = blockIdx.x - tile * grid.q_groups;
     const int64_t t = static_cast<int64_t>(tile) * (kHeadThreads / kLanes) + threadIdx.x / kLanes;
     if (t >= heads.T) return;
+    HeadRows<D> rows;
+    rows.start(heads.q + t * heads.q_stride, heads.q_out + t * heads.q_out_stride, static_cast<int>(g) * grid.per,
+               min(heads.Hq, static_cast<int>(g + 1) * grid.per));
     const int64_t slot = a.slots[t];
     if (slot < 0 || slot >= limit) return;  // recorded with the keys
     const float *angle = nullptr;
@@ -176,25 +187,27 @@ __global__ void __launch_bounds__(kHeadThreads) kv8_append_kernel(const Kv8Appen
     }
     HeadTurn<D> turn;
     turn.start(angle, heads.rotary, heads.w_q);
-    turn_heads<D>(turn, heads.q + t * heads.q_stride, heads.q_out + t * heads.q_out_stride, static_cast<int>(g) * grid.per,
-                  min(heads.Hq, static_cast<int>(g + 1) * grid.per), heads.eps);
+    rows.run(turn, heads.eps);
     return;
   }
   // ------------------------------------------------------------ keys and values: the runs that begin in 16 tokens
-  const unsigned id = blockIdx.x - grid.q_blocks, tile = id / grid.groups, g = id - tile * grid.groups;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned id = (blockIdx.x - grid.q_blocks) / grid.split, part = blockIdx.x - grid.q_blocks - id * grid.split;
+  const unsigned tile = id / grid.groups, g = id - tile * grid.groups;
+  constexpr int kTeams = kHeadThreads / 64;  // of two warps
+  __shared__ Kv8Half halves[kHeadThreads / 32];
+  const int lane = threadIdx.x & 31, team = threadIdx.x >> 6;
   const int64_t t0 = static_cast<int64_t>(tile) * kKv8Block;
-  const auto slot_of = [&](int64_t t) {
-    int64_t s = t >= 0 && t < heads.T ? a.slots[t] : -1;
-    if (s >= limit) {
-      record_status(kStatusBounds);
-      s = -1;
-    }
-    return s;
-  };
-  const int64_t slot = slot_of(t0 + lane);
-  int64_t prev = __shfl_up_sync(0xFFFFFFFFu, slot, 1);
-  if (lane == 0) prev = slot_of(t0 - 1);
+  int64_t slot = t0 + lane < heads.T ? a.slots[t0 + lane] : -1, prev = lane == 0 && t0 > 0 ? a.slots[t0 - 1] : -1;
+  const int pos = heads.rope && t0 + lane < heads.T ? heads.positions[t0 + lane] : 0;
+  if (slot >= limit) {
+    record_status(kStatusBounds);
+    slot = -1;
+  }
+  if (prev >= limit) prev = -1;
+  {
+    const int64_t left = __shfl_up_sync(0xFFFFFFFFu, slot, 1);
+    if (lane > 0) prev = left;
+  }
   const bool begins = slot >= 0 && (prev < 0 || prev >> 4 != slot >> 4);
   const uint32_t begin = __ballot_sync(0xFFFFFFFFu, begins);
   const uint32_t ends = begin | __ballot_sync(0xFFFFFFFFu, slot < 0);  // no run goes on here
@@ -209,11 +222,12 @@ __global__ void __launch_bounds__(kHeadThreads) kv8_append_kernel(const Kv8Appen
       count = kKv8Block;
     }
     for (int p = 0; p < pairs; ++p, ++item) {
-      if ((item & (kHeadThreads / 32 - 1)) != warp) continue;
+      if (item % (grid.split * kTeams) != static_cast<int>(part) * kTeams + team) continue;
       const int pair = pair0 + p, kv = pair >= a.cache.H;
-      kv8_write_run<D>(a, heads, t0, slot, first, count, kv, pair - kv * a.cache.H);
+      kv8_write_run<D>(a, heads, t0, slot, pos, first, count, kv, pair - kv * a.cache.H, halves);
     }
   }
+  pdl_wait();  // the queries' kernel, where there is one, runs beside this one: who waits for this waits for it
 }
 
 // The cached rows of the given slots as fp16: s * (code - 128), rounded once and
@@ -255,19 +269,38 @@ __global__ void __launch_bounds__(kHeadThreads) kv8_read_kernel(const Kv8Cache c
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs &a, const HeadArgs &heads, cudaStream_t stream) {
   const int D = a.cache.D, H = a.cache.H;
+  const bool few = heads.T <= 512;
   Kv8Grid g;
   g.per = heads.Hq > 0 ? turn_heads_per_lane(heads.T, heads.Hq, D) : 1;
   g.q_groups = static_cast<unsigned>((heads.Hq + g.per - 1) / g.per);
   const int tokens = kHeadThreads / (D / 8);
+  if (!few && heads.Hq > 0) {
+    // The runs' registers leave an SM 16 warps, too few for the queries' traffic: those take a kernel of their own,
+    // which many tokens do not notice.
+    HeadArgs q = heads;
+    q.H = 0, q.slots = a.slots, q.limit = a.cache.pages << a.cache.page_log2;
+    const cudaError_t e = launch_head_norm_rope(q, D, stream);
+    if (e != cudaSuccess) return e;
+    g.q_groups = 0;
+  }
   g.q_blocks = static_cast<unsigned>((heads.T + tokens - 1) / tokens) * g.q_groups;
-  // a warp's work is a run's pair: few tokens may be a run each, many are long runs
-  g.pairs = heads.T <= 512 ? 1 : kHeadThreads / 32;
+  // two warps' work is a run's pair: few tokens may be a run each, many are long runs
+  g.pairs = few ? 1 : kHeadThreads / 64;
+  g.split = few ? 4 : 1;
   g.groups = static_cast<unsigned>((2 * H + g.pairs - 1) / g.pairs);
-  const unsigned blocks = g.q_blocks + static_cast<unsigned>((heads.T + kKv8Block - 1) / kKv8Block) * g.groups;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(g.q_blocks + static_cast<unsigned>((heads.T + kKv8Block - 1) / kKv8Block) * g.groups * g.split);
+  cfg.blockDim = dim3(kHeadThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = !few && heads.Hq > 0 ? 1 : 0;  // behind the queries' kernel, which it does not depend on
   if (g.q_groups == 0) g.q_groups = 1;
-  if (D == 128) kv8_append_kernel<128><<<blocks, kHeadThreads, 0, stream>>>(a, heads, g);
-  else kv8_append_kernel<64><<<blocks, kHeadThreads, 0, stream>>>(a, heads, g);
-  return cudaGetLastError();
+  const cudaError_t e = D == 128 ? cudaLaunchKernelEx(&cfg, kv8_append_kernel<128>, a, heads, g)
+                                 : cudaLaunchKernelEx(&cfg, kv8_append_kernel<64>, a, heads, g);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 cudaError_t launch_kv8_read(const Kv8Cache &c, const int64_t *slots, int64_t T, void *k, void *v, cudaStream_t stream) {

@@ -255,8 +255,14 @@ __device__ __forceinline__ bool kv_first_units(const A &a, KvShared<C::kWarps> &
 #pragma unroll
     for (int x = 0; x < kWarps; ++x) U += shared.warp_units[x];
   }
-  // at least two units a warp: fewer blocks share a short context, whose joining would cost more than a unit
-  if (U < P * kWarps * 2) P = (U + kWarps * 2 - 1) / (kWarps * 2);
+  if (C::kWholeHeads && a.B == 1 && U < P * kWarps * 4 && P >= a.cache.H) {
+    // a single request's heads are alike: the same number of blocks to each, one where two units a warp do
+    const int tiles = U / a.cache.H;
+    P = a.cache.H * (tiles <= 2 * kWarps ? 1 : min((tiles + kWarps - 1) / kWarps, P / a.cache.H));
+  } else if (U < P * kWarps * C::kLeast) {
+    // at least kLeast units a warp: fewer blocks share a short context, whose joining would cost more than a unit
+    P = (U + kWarps * C::kLeast - 1) / (kWarps * C::kLeast);
+  }
   if (c >= P) return false;  // every other block has a unit
   const int share = U / P, rest = U - share * P;
   const auto block_start = [&](int b) { return share * b + rest * b / P; };  // rest, b < 2^8
@@ -338,7 +344,8 @@ __device__ __forceinline__ void kv_join_parts(const A &a, KvShared<C::kWarps> &s
       shared.cut_first[side] = seg_first;
       shared.cut_at[side] = seg;
     }
-    for (int r = 0; r < kRows; ++r, ++item) {
+    const int rows = min(kRows, seg.n * (a.Hq / a.cache.H));  // that there are
+    for (int r = 0; r < rows; ++r, ++item) {
       if (item % kWarps != warp) continue;
       row.clear();
       const bool in = these >> lane & 1u;
@@ -406,7 +413,7 @@ __device__ __forceinline__ void kv_join_parts(const A &a, KvShared<C::kWarps> &s
   for (int item = warp; item < 2 * kRows; item += kWarps) {
     const int side = item / kRows, r = item % kRows;
     const int c0 = shared.join_blocks[side][0], c1 = shared.join_blocks[side][1];
-    if (c1 < 0) continue;
+    if (c1 < 0 || r >= shared.cut_at[side].n * (a.Hq / a.cache.H)) continue;
     // the segment is the first block's last one and every other's first one
     const auto part_of = [&](int b) { return block_parts + (b * 2 + (b == c0 ? 1 : 0)) * C::kPart; };
     const int at = r * C::kPitch + lane * KvRow<D>::kCh, n = c1 - c0 + 1;

@@ -218,6 +218,8 @@ struct HeadArgs {
   int64_t max_pos;
   int rotary;
   float eps;
+  const int64_t *slots = nullptr;  // the cache's append only: tokens without a slot below `limit` are left alone
+  int64_t limit = 0;
 };
 cudaError_t launch_head_norm_rope(const HeadArgs &a, int D, cudaStream_t stream);
 
