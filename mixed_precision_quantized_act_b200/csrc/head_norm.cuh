@@ -70,7 +70,7 @@ struct HeadTurn {
       for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-      inv = rsqrtf(ss * (1.0f / D) + eps);
+      inv = rsqrtf(fmaf(ss, 1.0f / D, eps));
     }
     if (any) {
       uint4 far_raw;

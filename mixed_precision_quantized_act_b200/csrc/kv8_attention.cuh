@@ -61,7 +61,10 @@ struct Kv8Cfg {
   static constexpr bool kWholeHeads = true;
   static constexpr int kCodes = 32 * D;  // bytes of 32 tokens' key (or value) codes
   static constexpr int kStage = 2 * kCodes + 16;  // and two blocks' (key, value) scales
-  static constexpr int kStages = D == 128 ? 3 : 5;
+  // One unit a warp under way beside the one at work (64 KB a block), with 64 channels two.  With twice that the memory
+  // system serves some SMs (always the same ones) 15 % slower than others, and their blocks end last: 4 requests of
+  // 100000 to 131071 tokens took 175 us then, 164 so; 64 of 100 to 8100 109 and 102.
+  static constexpr int kStages = D == 128 ? 2 : 3;
   static constexpr int kRing = kStages * kStage;  // of one warp
   static constexpr int kPitch = D + 8;            // floats of a part's row: two rows further, 16 banks further
   static constexpr int kPart = kRows * (kPitch + 4);  // floats of one part: sums, then m, the two sums of p per row

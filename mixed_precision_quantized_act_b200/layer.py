@@ -18,11 +18,11 @@ GEMV quantizes its own slice of X and the layer is a single kernel.  Buffers
 are allocated once, at construction; a replay allocates nothing.
 """
 from dataclasses import dataclass
-from typing import List, Optional
+from typing import List, Optional, Union
 
 import torch
 
-from . import _lib, kv4, norm
+from . import _lib, kv4, kv8, norm, w8a8
 
 
 @dataclass
@@ -113,22 +113,27 @@ class LinearChain:
 
 
 class AttentionBlock:
-    """The attention half of one decoder layer over a 4-bit paged cache:
+    """The attention half of one decoder layer over a paged cache in 4 or 8 bits:
 
-        r <- r + x;  y = norm(r);  q, k, v = qkv(y);  q, k <- rotated;
-        cache <- k, v in 4 bits;  out = o_proj(attention(q, cache))
+        r <- r + x;  y = norm(r);  q, k, v = qkv(y);  q, k <- normalized, rotated;
+        cache <- k, v in its own format;  out = o_proj(attention(q, cache))
 
     for up to `tokens` tokens of up to `requests` requests at a time.  x is the
-    output of the block before (the residual update and its norm are one kernel
-    with the quantization for the qkv linear); `out` is this one's, for the block
-    after to add.  Buffers are allocated once, and ready for any stream when the
-    constructor returns; `run` allocates nothing and can be captured into a graph,
+    output of the block before; `out` is this one's, for the block after to add.
+    Either linear may be a W4.4A8 one (PackedLinear) or one in 8 bits (W8Weights);
+    before a W4.4A8 qkv the residual update and its norm are one kernel with the
+    quantization.  w_q and w_k, fp16 [head_dim], are the weights of the query and
+    key heads' norms (None: none); with a KV8Cache these, the rotation and the
+    write are one kernel.  Buffers are allocated once, and ready for any stream when
+    the constructor returns; `run` allocates nothing and can be captured into a graph,
     lengths and slots being device tensors (kv4_assign_into).
     """
 
-    def __init__(self, w_norm: torch.Tensor, qkv: _lib.PackedLinear, o_proj: _lib.PackedLinear, q_heads: int,
-                 cache: kv4.KV4Cache, rope: Optional[torch.Tensor], tokens: int, requests: int, max_q: int,
-                 table_width: int, eps: float = 1e-5):
+    def __init__(self, w_norm: torch.Tensor, qkv: Union[_lib.PackedLinear, w8a8.W8Weights],
+                 o_proj: Union[_lib.PackedLinear, w8a8.W8Weights], q_heads: int,
+                 cache: Union[kv4.KV4Cache, kv8.KV8Cache], rope: Optional[torch.Tensor], tokens: int, requests: int,
+                 max_q: int, table_width: int, eps: float = 1e-5, w_q: Optional[torch.Tensor] = None,
+                 w_k: Optional[torch.Tensor] = None, head_eps: float = 1e-6):
         H, D = cache.kv_heads, cache.head_dim
         _lib._require(qkv.N == (q_heads + 2 * H) * D, "qkv must have (q_heads + 2 kv_heads) x head_dim channels")
         _lib._require(o_proj.K == q_heads * D and o_proj.N == qkv.K, "o_proj must lead from the heads to qkv's inputs")
@@ -137,20 +142,60 @@ class AttentionBlock:
         _lib._require(all(t.device == dev for p in (qkv, o_proj) for t in p.buffers()),
                       f"the packed linears must be on the cache's device, {dev}")
         self.w_norm, self.qkv, self.o_proj, self.cache, self.rope, self.eps = w_norm, qkv, o_proj, cache, rope, eps
+        self.w_q, self.w_k, self.head_eps = w_q, w_k, head_eps
         self.q_heads, self.tokens, self.max_q = q_heads, tokens, max_q
-        self.A_q = torch.empty((tokens, qkv.K), dtype=torch.int8, device=dev)
-        self.s_a = torch.empty((tokens, qkv.K // _lib.GROUP), dtype=torch.float32, device=dev)
-        self.heads = torch.empty((tokens, q_heads + 2 * H, D), dtype=torch.float16, device=dev)
+        self.eight = isinstance(cache, kv8.KV8Cache)
+        half = lambda *shape: torch.empty(shape, dtype=torch.float16, device=dev)  # noqa: E731
+        self.heads = half(tokens, q_heads + 2 * H, D)
         self.q = torch.zeros((tokens, q_heads, D), dtype=torch.float16, device=dev)
         self.att = torch.zeros((tokens, q_heads, D), dtype=torch.float16, device=dev)
-        self.out = torch.empty((tokens, o_proj.N), dtype=torch.float16, device=dev)
+        self.out = half(tokens, o_proj.N)
         self.few = tokens <= _lib.SMALL_M_MAX
-        self.ws_qkv = _lib.small_m_workspace(tokens, qkv, dev) if self.few else None
-        self.ws_o = _lib.linear_workspace(tokens, o_proj, dev)
-        self.ws_att = kv4.kv4_attention_workspace(requests, max_q, q_heads, cache, table_width)
+        self.ws_qkv = None
+        if isinstance(qkv, w8a8.W8Weights):
+            self.y = half(tokens, qkv.K)
+            self.ws_qkv = w8a8.w8a8_linear_workspace(tokens, qkv)
+        else:
+            self.A_q = torch.empty((tokens, qkv.K), dtype=torch.int8, device=dev)
+            self.s_a = torch.empty((tokens, qkv.K // _lib.GROUP), dtype=torch.float32, device=dev)
+            if self.few:
+                self.ws_qkv = _lib.small_m_workspace(tokens, qkv, dev)
+        self.k = torch.zeros((tokens, H, D), dtype=torch.float16, device=dev) \
+            if not self.eight and (w_q is not None or w_k is not None) else None
+        self.ws_o = w8a8.w8a8_linear_workspace(tokens, o_proj) if isinstance(o_proj, w8a8.W8Weights) \
+            else _lib.linear_workspace(tokens, o_proj, dev)
+        workspace = kv8.kv8_attention_workspace if self.eight else kv4.kv4_attention_workspace
+        self.ws_att = workspace(requests, max_q, q_heads, cache, table_width)
         # the fills above went to the current stream, and `run` may be given any: its kernels' counters start at zero
         if not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(dev).synchronize()
+
+    def _qkv(self, r, x, stream):
+        r_out = None if x is None else r
+        Y = self.heads.view(self.tokens, -1)
+        if isinstance(self.qkv, w8a8.W8Weights):
+            norm.residual_norm_into(r, self.w_norm, self.y, x=x, r_out=r_out, eps=self.eps, stream=stream)
+            w8a8.w8a8_linear_into(self.y, self.qkv, Y, self.ws_qkv, stream=stream)
+            return
+        norm.residual_norm_quantize_into(r, self.w_norm, self.A_q, self.s_a, x=x, r_out=r_out, eps=self.eps,
+                                         stream=stream)
+        if self.few:
+            _lib.gemm_w4w8a8_small_m_into(self.A_q, self.s_a, self.qkv, Y, self.ws_qkv, stream)
+        else:
+            _lib.gemm_w4w8a8_into(self.A_q, self.s_a, self.qkv, Y, stream)
+
+    def _append(self, slots, positions, stream):
+        H = self.cache.kv_heads
+        q, k, v = self.heads.split((self.q_heads, H, H), 1)
+        turn = dict(positions=positions, rope=self.rope, stream=stream)
+        if self.eight:
+            kv8.kv8_append_into(k, v, slots, self.cache, q=q, q_out=self.q, w_q=self.w_q, w_k=self.w_k,
+                                eps=self.head_eps, **turn)
+        elif self.k is not None:
+            norm.head_norm_rope_into(q, self.q, self.w_q, k=k, k_out=self.k, w_k=self.w_k, eps=self.head_eps, **turn)
+            kv4.kv4_append_into(self.k, v, slots, self.cache, stream=stream)
+        else:
+            kv4.kv4_append_into(k, v, slots, self.cache, q=q, q_out=self.q, **turn)
 
     def run(self, r: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, cu_q: torch.Tensor,
             slots: torch.Tensor, positions: torch.Tensor, x: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -159,18 +204,13 @@ class AttentionBlock:
         new tokens (behind those cached); rows behind cu_q's last entry are padding
         and their outputs of no meaning."""
         with torch.cuda.device(self.cache.device):  # whatever the current device is
-            H = self.cache.kv_heads
-            norm.residual_norm_quantize_into(r, self.w_norm, self.A_q, self.s_a, x=x, r_out=None if x is None else r,
-                                             eps=self.eps, stream=stream)
-            Y = self.heads.view(self.tokens, -1)
-            if self.few:
-                _lib.gemm_w4w8a8_small_m_into(self.A_q, self.s_a, self.qkv, Y, self.ws_qkv, stream)
+            self._qkv(r, x, stream)
+            self._append(slots, positions, stream)
+            attention = kv8.kv8_attention_into if self.eight else kv4.kv4_attention_into
+            attention(self.q, self.cache, block_table, seq_lens, cu_q, self.max_q, self.att, self.ws_att, stream=stream)
+            att = self.att.view(self.tokens, -1)
+            if isinstance(self.o_proj, w8a8.W8Weights):
+                w8a8.w8a8_linear_into(att, self.o_proj, self.out, self.ws_o, stream=stream)
             else:
-                _lib.gemm_w4w8a8_into(self.A_q, self.s_a, self.qkv, Y, stream)
-            q, k, v = self.heads.split((self.q_heads, H, H), 1)
-            kv4.kv4_append_into(k, v, slots, self.cache, q=q, q_out=self.q, positions=positions, rope=self.rope,
-                                stream=stream)
-            kv4.kv4_attention_into(self.q, self.cache, block_table, seq_lens, cu_q, self.max_q, self.att, self.ws_att,
-                                   stream=stream)
-            _lib.linear_into(self.att.view(self.tokens, -1), self.o_proj, self.out, self.ws_o, stream)
+                _lib.linear_into(att, self.o_proj, self.out, self.ws_o, stream)
         return self.out
