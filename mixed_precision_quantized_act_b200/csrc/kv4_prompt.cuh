@@ -71,6 +71,7 @@ constexpr int kPmMaxGrid = 148;
 constexpr int kPmScaleRing = 4;
 constexpr float kPmLift = 7.0f;        // log2 of a row's largest weight where its reference is set
 constexpr float kPmTopWeight = 0x1p15f;  // and the largest before it is moved
+constexpr float kPmLeastScale = 0x1p-40f;  // a value's block scale counts as this much at least
 constexpr float kPmTopSum = 0x1p80f;   // sum of p: larger ones are zero-valued tokens' alone, and move it too
 
 template <int D>
@@ -207,6 +208,7 @@ struct Pm4 {
   using Args = AttendArgs;
   static constexpr int kVec = D / 32;  // 16-byte loads of a row's codes
   static constexpr int kIssueRegs = 64, kUnpackRegs = 96;  // of a thread; with 2 x 176 of the softmax, 4 x 128
+  static constexpr bool kBlocks = false;  // a scale for each token
   // thread = token; r: its row, or -1
   static __device__ __forceinline__ uint32_t load(const Kv4Cache &c, int64_t r, uint4 (&codes)[kVec]) {
 #pragma unroll
@@ -454,10 +456,18 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typenam
       if (!mbar_wait(&k_empty[s], phase ^ 1, &abort_flag)) break;
       const int at = it & (kPmScaleRing - 1);
       {
-        const float vs = F::scale(vm);
-        k_scale[at * kPmTile + tk] = F::scale(km) * scale2;
-        v_scale[at * kPmTile + tk] = vs;
-        v_log[at * kPmTile + tk] = __log2f(fmaxf(vs, 0x1p-24f));
+        const float ks = F::scale(km) * scale2, vs = F::scale(vm);
+        if constexpr (F::kBlocks) {
+          if ((tk & 15) == 0) {
+            const float held = vs < kPmLeastScale ? kPmLeastScale : vs;  // a NaN stays one
+            reinterpret_cast<float4 *>(k_scale)[at * (kPmTile / 16) + (tk >> 4)] =
+                make_float4(ks, __log2f(held), __fdividef(1.0f, held), 0.0f);
+          }
+        } else {
+          k_scale[at * kPmTile + tk] = ks;
+          v_scale[at * kPmTile + tk] = vs;
+          v_log[at * kPmTile + tk] = __log2f(fmaxf(vs, 0x1p-24f));
+        }
         const uint32_t bits = __ballot_sync(0xFFFFFFFFu, ok_now);
         if (lane == 0) seen[at][warp - 4] = bits;
       }
@@ -525,6 +535,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typenam
         tc_fence_after();
         const float *ks = k_scale + at * kPmTile + 64 * h, *vs = v_scale + at * kPmTile + 64 * h,
                     *vl = v_log + at * kPmTile + 64 * h;
+        // of each 16 columns: the keys' factor, the values' log2 and reciprocal
+        const float4 *blocks = reinterpret_cast<const float4 *>(k_scale) + at * (kPmTile / 16) + 4 * h;
         const uint2 there = *reinterpret_cast<const uint2 *>(&seen[at][2 * h]);
         const bool whole = base + 64 <= lim_min && (there.x & there.y) == 0xFFFFFFFFu;
         // bit k: column 32 b + k is seen by this row
@@ -546,7 +558,13 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typenam
             const uint32_t see = visible(b);
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const float v = fmaf(__uint_as_float(c[k]), ks[32 * b + k], vl[32 * b + k]);
+              float v;
+              if constexpr (F::kBlocks) {
+                const float4 bl = blocks[2 * b + k / 16];
+                v = fmaf(__uint_as_float(c[k]), bl.x, bl.y);
+              } else {
+                v = fmaf(__uint_as_float(c[k]), ks[32 * b + k], vl[32 * b + k]);
+              }
               top = fmaxf(top, see >> k & 1u ? v : -INFINITY);
             }
           }
@@ -567,22 +585,44 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typenam
             reg_fence(c);
             if (b == 0) tmem_ld_32x32b_x32(sh_at + 32, x[1]);
             const uint32_t see = kAll ? 0xFFFFFFFFu : visible(b);
+            if constexpr (F::kBlocks) {
+              // p s_v at once, as 2^(score + log2 s_v - R): 16 columns' sum takes the scale off again
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const ulonglong2 f = lds_2x2f(ks + 32 * b + 4 * k), g = lds_2x2f(vs + 32 * b + 4 * k);
+              for (int s = 0; s < 2; ++s) {
+                const float4 bl = blocks[2 * b + s];
+                const uint64_t f2 = pack_f2(bl.x, bl.x), to2 = pack_f2(bl.y - ref, bl.y - ref);
+                uint64_t part2 = 0;
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int at2 = 4 * k + 2 * q;
-                float2 v = unpack_f2(
-                    fma_f2(pack_f2(__uint_as_float(c[at2]), __uint_as_float(c[at2 + 1])), q ? f.y : f.x, ref2));
-                if constexpr (!kAll) v.x = see >> at2 & 1u ? v.x : -INFINITY, v.y = see >> (at2 + 1) & 1u ? v.y : -INFINITY;
-                const uint64_t e2 = pack_f2(ex2(v.x), ex2(v.y));
-                sum2 = add_f2(sum2, e2);
-                float2 pv = unpack_f2(mul_f2(e2, q ? g.y : g.x));
-                // a value's scale may be NaN: select, not multiply
-                if constexpr (!kAll) pv.x = see >> at2 & 1u ? pv.x : 0.0f, pv.y = see >> (at2 + 1) & 1u ? pv.y : 0.0f;
-                hi[q] = fmaxf(fmaxf(hi[q], pv.x), pv.y);
-                p[16 * b + 2 * k + q] = half2_bits(pv.x, pv.y);
+                for (int q = 0; q < 8; ++q) {
+                  const int at2 = 16 * s + 2 * q;
+                  float2 v = unpack_f2(fma_f2(pack_f2(__uint_as_float(c[at2]), __uint_as_float(c[at2 + 1])), f2, to2));
+                  float2 pv = make_float2(ex2(v.x), ex2(v.y));
+                  // what is not seen is selected away: a scale may be NaN
+                  if constexpr (!kAll) pv.x = see >> at2 & 1u ? pv.x : 0.0f, pv.y = see >> (at2 + 1) & 1u ? pv.y : 0.0f;
+                  part2 = add_f2(part2, pack_f2(pv.x, pv.y));
+                  hi[q & 1] = fmaxf(fmaxf(hi[q & 1], pv.x), pv.y);
+                  p[16 * b + 8 * s + q] = half2_bits(pv.x, pv.y);
+                }
+                if (kAll || (see >> (16 * s) & 0xFFFFu) != 0) sum2 = fma_f2(part2, pack_f2(bl.z, bl.z), sum2);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const ulonglong2 f = lds_2x2f(ks + 32 * b + 4 * k), g = lds_2x2f(vs + 32 * b + 4 * k);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const int at2 = 4 * k + 2 * q;
+                  float2 v = unpack_f2(
+                      fma_f2(pack_f2(__uint_as_float(c[at2]), __uint_as_float(c[at2 + 1])), q ? f.y : f.x, ref2));
+                  if constexpr (!kAll) v.x = see >> at2 & 1u ? v.x : -INFINITY, v.y = see >> (at2 + 1) & 1u ? v.y : -INFINITY;
+                  const uint64_t e2 = pack_f2(ex2(v.x), ex2(v.y));
+                  sum2 = add_f2(sum2, e2);
+                  float2 pv = unpack_f2(mul_f2(e2, q ? g.y : g.x));
+                  // a value's scale may be NaN: select, not multiply
+                  if constexpr (!kAll) pv.x = see >> at2 & 1u ? pv.x : 0.0f, pv.y = see >> (at2 + 1) & 1u ? pv.y : 0.0f;
+                  hi[q] = fmaxf(fmaxf(hi[q], pv.x), pv.y);
+                  p[16 * b + 2 * k + q] = half2_bits(pv.x, pv.y);
+                }
               }
             }
           }

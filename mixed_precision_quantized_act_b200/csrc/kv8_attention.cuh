@@ -394,6 +394,7 @@ struct Pm8 {
   using Args = Attend8Args;
   static constexpr int kVec = D / 16;  // 16-byte loads of a row's codes
   static constexpr int kIssueRegs = 48, kUnpackRegs = 112;  // a key's and a value's codes are held at once
+  static constexpr bool kBlocks = true;  // one scale for 16 tokens
   // A row's 16-byte pieces are neighbouring lanes' (each lane a row of its own took 32 lines a load): lane l has
   // piece l % kVec of rows l / kVec, + 32 / kVec, .. of the warp's 32.  `row` is the lane's token's, or -1; a block of
   // 16 tokens lies in one page, so its rows follow on its first one's, seen or not.
@@ -410,10 +411,14 @@ struct Pm8 {
     return r >= 0 ? __float_as_uint(c.scales[r >> 4]) : 0u;
   }
   static __device__ __forceinline__ float scale(uint32_t meta) { return __uint_as_float(meta); }
-  static __device__ __forceinline__ void store(uint8_t *to, const uint4 (&codes)[kVec], uint32_t) {
+  // (a scale of zero makes zeros of any codes: the softmax does not multiply by it)
+  static __device__ __forceinline__ void store(uint8_t *to, const uint4 (&held)[kVec], uint32_t meta) {
     const int lane = threadIdx.x & 31, piece = lane % kVec;
+    const bool zero[2] = {__shfl_sync(0xFFFFFFFFu, meta, 0) == 0, __shfl_sync(0xFFFFFFFFu, meta, 16) == 0};
+    uint4 codes[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
+      codes[i] = zero[i >= kVec / 2] ? make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u) : held[i];
       const int tk = (threadIdx.x & 96) + i * (32 / kVec) + lane / kVec;
       const uint4 low = make_uint4(codes_f16(codes[i].x, kLowPair), codes_f16(codes[i].x, kHighPair),
                                    codes_f16(codes[i].y, kLowPair), codes_f16(codes[i].y, kHighPair));
