@@ -27,6 +27,9 @@ def rows(t, name: str, dtype, shape, device: int) -> int:
         raise ValueError(f"{name} must be a {dtype} {list(shape)} on cuda:{device}, "
                          f"not {t.dtype} {list(t.shape)} on {t.device}")
     strides = t.stride()
+    n = len(strides)
+    if n == 3 and strides[2] == 1 and strides[1] == shape[2] and shape[0] > 1 or n == 2 and strides[1] == 1 and shape[0] > 1:
+        return strides[0]
     inner = 1
     for i in range(len(shape) - 1, 0, -1):
         if strides[i] != inner and shape[i] != 1 and t.numel() > 0:

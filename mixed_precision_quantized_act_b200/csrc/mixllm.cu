@@ -5,6 +5,7 @@
 // launches kernels; every step of the layer's arithmetic runs on the GPU.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -62,12 +63,15 @@ mixllm_status check_device() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  static std::atomic<unsigned long long> known{0};  // one bit per device ordinal that is sm_100
+  if (dev < 64 && (known.load(std::memory_order_relaxed) >> dev & 1)) return MIXLLM_OK;
   int major = 0, minor = 0;
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
   if (major != 10 || minor != 0)
     return fail(MIXLLM_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a only", dev, major,
                 minor);
+  if (dev < 64) known.fetch_or(1ull << dev);
   return MIXLLM_OK;
 }
 

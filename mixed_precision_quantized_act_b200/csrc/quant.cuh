@@ -10,6 +10,7 @@
 #include <cuda_fp16.h>
 #include <cstdint>
 
+#include "kv4_ptx.cuh"  // pairs of floats
 #include "launch.h"
 #include "ptx_sm100.cuh"
 
@@ -95,7 +96,7 @@ __device__ __forceinline__ float quant_act_8x16(const uint4 raw, unsigned mask, 
 // 1/2 + 2^-16, so it is the code wherever the exact remainder |e| = |x - q0 s|
 // stays below s/2 less a margin; the low byte of fl(x r + 1.5*2^23) is q0 itself.
 // One test of the largest remainder serves all eight, and only where it fails are
-// the quotients divided out: seven instructions a value.
+// the quotients divided out: five instructions a value.
 struct QuantStep {
   float s, r, below;
 
@@ -104,13 +105,16 @@ struct QuantStep {
   }
   __device__ __forceinline__ void codes(const float (&x)[8], uint32_t (&packed)[2]) const {
     constexpr float kMagic = 12582912.0f;
+    const uint64_t r2 = pack_f2(r, r), minus_s2 = pack_f2(-s, -s), magic2 = pack_f2(kMagic, kMagic),
+                   minus_magic2 = pack_f2(-kMagic, -kMagic);
     uint32_t bits[8];
     float worst = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = __fmaf_rn(x[i], r, kMagic);
-      bits[i] = __float_as_uint(t);
-      worst = fmaxf(worst, fabsf(__fmaf_rn(-__fadd_rn(t, -kMagic), s, x[i])));
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t x2 = pack_f2(x[i], x[i + 1]), t2 = fma_f2(x2, r2, magic2);
+      const float2 t = unpack_f2(t2), e = unpack_f2(fma_f2(add_f2(t2, minus_magic2), minus_s2, x2));
+      bits[i] = __float_as_uint(t.x), bits[i + 1] = __float_as_uint(t.y);
+      worst = fmaxf(fmaxf(worst, fabsf(e.x)), fabsf(e.y));
     }
     if (worst > below) {
 #pragma unroll
