@@ -772,7 +772,8 @@ MIXLLM_API mixllm_status mixllm_head_norm_rope(const void *q_f16, int64_t q_stri
  *   w_q, w_k  device fp16 [head_dim], or NULL: no norm
  *   positions, rope, max_pos, rotary   as of mixllm_kv4_append; a token whose
  *             position is out of range is skipped and recorded
- * Alignment and strides as there.  n_slots = 0 is a no-op.  Asynchronous.
+ * Alignment and strides as there.  n_slots = 0 is a no-op.  Tokens / 16 x key
+ * heads / 2 below 2^31 (MIXLLM_ERR_UNSUPPORTED otherwise).  Asynchronous.
  */
 MIXLLM_API mixllm_status mixllm_kv8_append(uint8_t *codes, float *scales, int64_t pages, int32_t kv_heads,
                                            int32_t head_dim, int32_t page_size, const int64_t *slots,
@@ -832,7 +833,7 @@ MIXLLM_API mixllm_status mixllm_selftest_wait_timeout(uint32_t limit_us, void *s
 
 /*
  * 1 if this is the checked build of the library (every tensor- and
- * shared-memory access of the GEMM kernels is range-checked first; a failed
+ * shared-memory access of the W4.4A8 GEMM kernels is range-checked first; a failed
  * check skips the access and records MIXLLM_ERR_BOUNDS), 0 for the release
  * build.  Pure host function.
  */

@@ -274,6 +274,14 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs &a, const HeadArgs &heads, cud
   g.per = heads.Hq > 0 ? turn_heads_per_lane(heads.T, heads.Hq, D) : 1;
   g.q_groups = static_cast<unsigned>((heads.Hq + g.per - 1) / g.per);
   const int tokens = kHeadThreads / (D / 8);
+  if (!few) g.q_groups = 0;
+  g.q_blocks = static_cast<unsigned>((heads.T + tokens - 1) / tokens) * g.q_groups;
+  // two warps' work is a run's pair: few tokens may be a run each, many are long runs
+  g.pairs = few ? 1 : kHeadThreads / 64;
+  g.split = few ? 4 : 1;
+  g.groups = static_cast<unsigned>((2 * H + g.pairs - 1) / g.pairs);
+  const int64_t blocks = g.q_blocks + (heads.T + kKv8Block - 1) / kKv8Block * g.groups * g.split;
+  if (blocks > 0x7FFFFFFF) return cudaErrorNotSupported;
   if (!few && heads.Hq > 0) {
     // The runs' registers leave an SM 16 warps, too few for the queries' traffic: those take a kernel of their own,
     // which many tokens do not notice.
@@ -281,18 +289,12 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs &a, const HeadArgs &heads, cud
     q.H = 0, q.slots = a.slots, q.limit = a.cache.pages << a.cache.page_log2;
     const cudaError_t e = launch_head_norm_rope(q, D, stream);
     if (e != cudaSuccess) return e;
-    g.q_groups = 0;
   }
-  g.q_blocks = static_cast<unsigned>((heads.T + tokens - 1) / tokens) * g.q_groups;
-  // two warps' work is a run's pair: few tokens may be a run each, many are long runs
-  g.pairs = few ? 1 : kHeadThreads / 64;
-  g.split = few ? 4 : 1;
-  g.groups = static_cast<unsigned>((2 * H + g.pairs - 1) / g.pairs);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(g.q_blocks + static_cast<unsigned>((heads.T + kKv8Block - 1) / kKv8Block) * g.groups * g.split);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kHeadThreads);
   cfg.stream = stream;
   cfg.attrs = attr;

@@ -1018,6 +1018,7 @@ mixllm_status mixllm_kv8_append(uint8_t *codes, float *scales, int64_t pages, in
   heads.positions = positions, heads.rope = rotary > 0 ? rope : nullptr;
   heads.max_pos = max_pos, heads.rotary = rotary, heads.eps = eps;
   cudaError_t e = mixllm::launch_kv8_append(a, heads, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return fail(MIXLLM_ERR_UNSUPPORTED, "more than 2^31 blocks of tokens and heads");
   if (e != cudaSuccess) return cuda_fail(e, "kv8_append launch");
   return ok();
 }
