@@ -20,7 +20,15 @@ namespace mixllm {
 // factors, which all heads of a token share, and the norm's own factor comes off
 // the sum: inv * (x own + x_far far).  Without weights inv = 1 and own, far are
 // the cosine and the signed sine: every product and sum rounded on its own, the
-// bits of the 4-bit cache's rotation.
+// bits of the 4-bit cache's rotation.  (Pairs of floats would need a third of the
+// instructions fewer, but ptxas joins their products and sums; the time is the same.)
+//
+// HBM-bound: 4 bytes a channel, and the table's 8 bytes a channel of a token once
+// for sixteen heads.  4099 tokens of 64 + 8 heads of 128, half of their channels
+// rotated: 30.9 us on B200, 4.9 TB/s (75 % of the measured copy rate).  A block's
+// latencies follow one another (heads and position, table, stores); more warps an SM
+// (40 or 48 for 32, with two heads ahead) took 34 to 40 us, eight heads ahead 33.6,
+// the first heads loaded behind the position 35.
 // ---------------------------------------------------------------------------
 template <int D>
 struct HeadTurn {

@@ -49,6 +49,12 @@ namespace mixllm {
 // by the sum of p as that rounding leaves it, where the block's scale is not far
 // below the largest, S (a weight that is an fp16 subnormal says little about p).
 // Sums stay in fp32.
+//
+// Measured on B200 (as a CUDA graph): 64 requests of 100 to 8100 tokens, 32 query and
+// 8 key heads of 128: 102 us, 5.3 TB/s (81 % of the measured copy rate; the loops take
+// 82 us of it, at that rate, the rest is the first loads, SMs that end 10 us apart, and
+// the joins); 4 requests of 100000 to 131071 tokens, 64 and 8 heads: 164 us, 5.9 TB/s
+// (90 %); one request of 1003 tokens: 9.6 us.
 // ---------------------------------------------------------------------------
 constexpr float kKv8LeastScale = 0x1p-40f;
 
@@ -387,7 +393,12 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT>::kThreads, 1) kv8_decode_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Prompts: the 4-bit cache's kernel (kv4_prompt.cuh) with these rows.
+// Prompts: the 4-bit cache's kernel (kv4_prompt.cuh) with these rows.  A block's
+// scales are taken once for 16 columns, the values' as a summand of the exponent.
+// 1024 and 866 new tokens behind contexts of 8192 and 6354, 32 query and 8 key heads
+// of 128: 250 us, 845 TFLOP/s (52 % of the measured bf16 burst rate); 16 and 4 heads
+// of 64: 120 us.  The softmax bounds it: 64 columns take its warps some 2200 clocks, of
+// which the exponentials of both tiles need 1024.
 // ---------------------------------------------------------------------------
 template <int D>
 struct Pm8 {
