@@ -63,7 +63,7 @@ struct Kv8Half {
 // One run's rows of one head, key (kv = 0) or value: two warps, eight tokens each.
 // Lane i's `slot` and `pos` are those of token t0 + i (slot -1: none).  What depends
 // on slot and position alone is loaded before anything is used.
-template <int D>
+template <int D, int kNorm>
 __device__ __forceinline__ void kv8_write_run(const Kv8AppendArgs &a, const HeadArgs &heads, int64_t t0, int64_t slot,
                                               int pos, int first, int count, int kv, int h, Kv8Half *halves) {
   constexpr int kLanes = D / 8, kTogether = 32 / kLanes, kPasses = kKv8Block / 2 / kTogether;
@@ -96,8 +96,8 @@ __device__ __forceinline__ void kv8_write_run(const Kv8AppendArgs &a, const Head
       if (kv == 0 && sub == 0) record_status(kStatusBounds);
       row_of[p] = -1;  // a value is skipped where its key is
     }
-    if (kv == 0 && (heads.rope || heads.w_k)) {
-      HeadTurn<D> turn;
+    if (kv == 0 && (heads.rope || kNorm)) {
+      HeadTurn<D, kNorm> turn;
       turn.start(heads.rope && row_of[p] >= 0 ? heads.rope + static_cast<int64_t>(at) * heads.rotary : nullptr,
                  heads.rotary, heads.w_k);
       turn.any = heads.rope != nullptr;  // every lane takes part in the exchange
@@ -171,7 +171,8 @@ struct Kv8Grid {
   int pairs, split;  // split: blocks that share a group's runs
 };
 
-template <int D>
+// kNorm: whether there are norms of keys
+template <int D, int kNorm>
 __global__ void __launch_bounds__(kHeadThreads, 3) kv8_append_kernel(const Kv8AppendArgs a, const HeadArgs heads,
                                                                   const Kv8Grid grid) {
   constexpr int kLanes = D / 8;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kHeadThreads, 3) kv8_append_kernel(const Kv8Ap
     for (int p = 0; p < pairs; ++p, ++item) {
       if (item % (grid.split * kTeams) != static_cast<int>(part) * kTeams + team) continue;
       const int pair = pair0 + p, kv = pair >= a.cache.H;
-      kv8_write_run<D>(a, heads, t0, slot, pos, first, count, kv, pair - kv * a.cache.H, halves);
+      kv8_write_run<D, kNorm>(a, heads, t0, slot, pos, first, count, kv, pair - kv * a.cache.H, halves);
     }
   }
   pdl_wait();  // the queries' kernel, where there is one, runs beside this one: who waits for this waits for it
@@ -307,8 +308,10 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs &a, const HeadArgs &heads, cud
   cfg.attrs = attr;
   cfg.numAttrs = !few && heads.Hq > 0 ? 1 : 0;  // behind the queries' kernel, which it does not depend on
   if (g.q_groups == 0) g.q_groups = 1;
-  const cudaError_t e = D == 128 ? cudaLaunchKernelEx(&cfg, kv8_append_kernel<128>, a, heads, g)
-                                 : cudaLaunchKernelEx(&cfg, kv8_append_kernel<64>, a, heads, g);
+  const bool norm = heads.w_k != nullptr;
+  const auto kern = D == 128 ? (norm ? kv8_append_kernel<128, 1> : kv8_append_kernel<128, 0>)
+                             : (norm ? kv8_append_kernel<64, 1> : kv8_append_kernel<64, 0>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, heads, g);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
