@@ -590,20 +590,21 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typenam
 #pragma unroll
               for (int s = 0; s < 2; ++s) {
                 const float4 bl = blocks[2 * b + s];
-                const uint64_t f2 = pack_f2(bl.x, bl.x), to2 = pack_f2(bl.y - ref, bl.y - ref);
-                uint64_t part2 = 0;
+                const float to = bl.y - ref;
+                float part[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                   const int at2 = 16 * s + 2 * q;
-                  float2 v = unpack_f2(fma_f2(pack_f2(__uint_as_float(c[at2]), __uint_as_float(c[at2 + 1])), f2, to2));
-                  float2 pv = make_float2(ex2(v.x), ex2(v.y));
+                  float2 pv = make_float2(ex2(fmaf(__uint_as_float(c[at2]), bl.x, to)),
+                                          ex2(fmaf(__uint_as_float(c[at2 + 1]), bl.x, to)));
                   // what is not seen is selected away: a scale may be NaN
                   if constexpr (!kAll) pv.x = see >> at2 & 1u ? pv.x : 0.0f, pv.y = see >> (at2 + 1) & 1u ? pv.y : 0.0f;
-                  part2 = add_f2(part2, pack_f2(pv.x, pv.y));
+                  part[0] += pv.x, part[1] += pv.y;
                   hi[q & 1] = fmaxf(fmaxf(hi[q & 1], pv.x), pv.y);
                   p[16 * b + 8 * s + q] = half2_bits(pv.x, pv.y);
                 }
-                if (kAll || (see >> (16 * s) & 0xFFFFu) != 0) sum2 = fma_f2(part2, pack_f2(bl.z, bl.z), sum2);
+                if (kAll || (see >> (16 * s) & 0xFFFFu) != 0)
+                  sum2 = fma_f2(pack_f2(part[0], part[1]), pack_f2(bl.z, bl.z), sum2);
               }
             } else {
 #pragma unroll
