@@ -31,10 +31,10 @@ constexpr int kKv8Block = 16;  // tokens of one scale
 // tokens in a kernel of their own that runs beside this one.
 //
 // HBM-bound by its bytes, in fact by latency: slots, then rows, table and scale
-// together, then the write.  4101 tokens of 64 + 8 heads of 128: 41 us (queries 27,
-// keys and values 20, overlapping) and 8.5 us to read back, for 28.6 us of traffic;
+// together, then the write.  4101 tokens of 64 + 8 heads of 128: 39.6 us (queries 27,
+// keys and values 17.4, overlapping) and 8.5 us to read back, for 28.6 us of traffic;
 // one warp a run took 24 us for keys and values (128 registers, 16 warps an SM; now 24),
-// queries in this kernel 37.  32 tokens: 8 us.
+// queries in this kernel 37.  32 tokens: 8.8 us.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int64_t kv8_row(const Kv8Cache &c, int64_t slot, int kv, int h) {
   const int64_t page = slot >> c.page_log2;
@@ -291,7 +291,7 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs &a, const HeadArgs &heads, cud
   const int64_t blocks = g.q_blocks + (heads.T + kKv8Block - 1) / kKv8Block * g.groups * g.split;
   if (blocks > 0x7FFFFFFF) return cudaErrorNotSupported;
   if (!few && heads.Hq > 0) {
-    // The runs' registers leave an SM 16 warps, too few for the queries' traffic: those take a kernel of their own,
+    // The runs' registers leave an SM 24 warps, too few for the queries' traffic: those take a kernel of their own,
     // which many tokens do not notice.
     HeadArgs q = heads;
     q.H = 0, q.slots = a.slots, q.limit = a.cache.pages << a.cache.page_log2;
