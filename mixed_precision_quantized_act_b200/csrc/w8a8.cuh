@@ -6,6 +6,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "gemm_w4w8a8.cuh"  // device_sm_count, tensor maps
@@ -161,8 +162,8 @@ static cudaError_t launch_row_quantize(const T *X, int64_t stride, int64_t M, in
 //
 // A few tokens are bound by the weights' bytes.  Two blocks an SM with 90 KB of
 // copies under way each serve that better than one with 200 (112 tiles or fewer
-// would else leave SMs idle, 224 load them unevenly); copies of the weights
-// start while the quantizer still runs.  Measured on B200 (graph of quantizer and
+// would else leave SMs idle, 224 load them unevenly), but for 33 to 64 tokens and few
+// tiles; the first copies of the weights start while the quantizer still runs.  Measured on B200 (graph of quantizer and
 // product, weights from HBM): 1 token, 4096 -> 6144: 9.6 us (weights alone 3.8; the
 // product by itself 8.2: its blocks run 7.6 us, 5 of them for the weights, 1.2 for the
 // exchange of parts), 37 tokens, 4096 -> 28672: 23 us, 5.2 TB/s.  Parts left in global
@@ -187,21 +188,29 @@ struct W8Walk {
   }
 };
 
-template <int NT>
+// kAlone: one block an SM, with a deeper ring of stages and a place of their own for a cluster's parts (a barrier of
+// the cluster less).
+template <int NT, bool kAlone = false>
 struct W8Cfg {
   static constexpr int kStageW = kW8Rows * kW8Chunk, kStageA = NT * kW8Chunk, kStage = kStageW + kStageA;
   static constexpr int kCols = NT / 2 < 32 ? NT / 2 : 32;  // tokens of one load from tensor memory
   static constexpr int kOutCols = kCols < 16 ? kCols : 16;  // and of one round through shared memory
   static constexpr int kOut = 8 * kOutCols * 32 * 2;       // bytes: eight warps' tokens x 32 channels, fp16
-  static constexpr int kRoom = 112 * 1024 - kOut - 1024 - 2 * NT * 4;
-  static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
-  static constexpr int kSmem = kStages * kStage + kOut + 1024;
-  static constexpr int kTmem = 2 * NT < 32 ? 32 : 2 * NT;
   static constexpr int kGroups = NT / 4;  // of four tokens
   // parts that a block receives: of each block of the cluster, its groups' tokens x channels, int32
   static constexpr int received(int S) { return S * ((kGroups + S - 1) / S) * 4 * kW8Rows * 4; }
-  static_assert(received(2) <= kStages * kStage && received(4) <= kStages * kStage, "parts in the operands' place");
-  static_assert(2 * (kSmem + 2048) <= 227 * 1024, "two blocks an SM");
+  static constexpr int kParts = !kAlone ? 0 : received(3) > received(4) ? received(3) : received(4);
+  static constexpr int kRoom = (kAlone ? 224 : 112) * 1024 - kOut - kParts - 1024 - 2 * NT * 4;
+  static constexpr int kMost = kAlone ? 12 : 8;
+  static constexpr int kStages = kRoom / kStage < kMost ? kRoom / kStage : kMost;
+  static constexpr int kSmem = kStages * kStage + kOut + kParts + 1024;
+  // Chunks of weights that are asked for while the quantizer runs: more would make its own loads wait (1 token,
+  // 4096 -> 4096: three 8.45 us, five 8.7, none 8.65; a block alone, 64 tokens, 4096 -> 6144: none 12.3, one 12.8,
+  // all 13.8).
+  static constexpr int kEarly = kAlone ? 0 : 3;
+  static constexpr int kTmem = 2 * NT < 32 ? 32 : 2 * NT;
+  static_assert(kAlone || (received(2) <= kStages * kStage && received(4) <= kStages * kStage), "parts in the operands' place");
+  static_assert((kAlone ? 1 : 2) * (kSmem + 2048) <= 227 * 1024, "the blocks of an SM");
 };
 
 struct W8Job {
@@ -274,10 +283,10 @@ __device__ __forceinline__ bool w8_write_tile(const W8Job &a, int64_t ch0, int64
   return true;
 }
 
-template <int NT>
+template <int NT, bool kAlone>
 __global__ void __launch_bounds__(kW8Threads, 2)
     w8a8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const W8Job a) {
-  using C = W8Cfg<NT>;
+  using C = W8Cfg<NT, kAlone>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drained;
@@ -318,7 +327,7 @@ __global__ void __launch_bounds__(kW8Threads, 2)
   }
   __syncwarp();
   if (warp == 0 && a.early) {
-    for (W8Walk w(tile0, a.TT, k0, k1); ahead < C::kStages && ahead < chunks; ++ahead, w.next()) {
+    for (W8Walk w(tile0, a.TT, k0, k1); ahead < C::kEarly && ahead < chunks; ++ahead, w.next()) {
       if (elect_one()) weights(ahead, w);
       __syncwarp();
     }
@@ -333,6 +342,7 @@ __global__ void __launch_bounds__(kW8Threads, 2)
   tc_fence_after();
   pdl_launch_dependents();  // only now: a dependent may take tensor memory as it starts
   const uint32_t tmem = tmem_slot;
+  if (kAlone && a.S > 1) cluster_arrive();  // this block runs: others may write to its shared memory
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
@@ -403,6 +413,7 @@ __global__ void __launch_bounds__(kW8Threads, 2)
     // ------------------------------------------------------------ a cluster's parts: thread = channel
     const int S = a.S, me = static_cast<int>(cluster_rank()), half = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
     const int most = (C::kGroups + S - 1) / S;  // groups of a block
+    uint8_t *parts = smem + (kAlone ? C::kStages * C::kStage + C::kOut : 0);
     const auto first_group = [&](int b) { return (C::kGroups * b + S - 1) / S; };  // owner of group g: g S / kGroups
     const int rt = tile0 / a.TT, tt = tile0 - rt * a.TT;
     const int64_t ch = static_cast<int64_t>(rt) * kW8Rows + r, m0 = static_cast<int64_t>(tt) * NT;
@@ -411,11 +422,11 @@ __global__ void __launch_bounds__(kW8Threads, 2)
     if (warp >= 4) there = mbar_wait(&acc_full[0], 0, &abort_flag);
     __syncwarp();
     tc_fence_after();
-    cluster_arrive();  // every block is done with its operands: parts take their place
+    if (!kAlone) cluster_arrive();  // every block is done with its operands: parts take their place
     cluster_wait();
     if (warp >= 4 && __all_sync(0xFFFFFFFFu, there)) {
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(me * most * kW8Rows + r) * 16;
+      const uint32_t mine = smem_u32(parts) + static_cast<uint32_t>(me * most * kW8Rows + r) * 16;
 #pragma unroll 1
       for (int j0 = half * (NT / 2); j0 < (half + 1) * (NT / 2) && j0 < groups * 4; j0 += C::kCols) {
         uint32_t v[C::kCols];
@@ -444,7 +455,7 @@ __global__ void __launch_bounds__(kW8Threads, 2)
 #pragma unroll
         for (int x = 0; x < 4; ++x) sa[x] = m + x < a.M ? a.s_a[m + x] : 0.0f;
         int4 sum = make_int4(0, 0, 0, 0);
-        const int4 *part = reinterpret_cast<const int4 *>(smem) + (g - g0) * kW8Rows + r;
+        const int4 *part = reinterpret_cast<const int4 *>(parts) + (g - g0) * kW8Rows + r;
         for (int b = 0; b < S; ++b) {
           const int4 v = part[b * most * kW8Rows];
           sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
@@ -494,7 +505,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const int side = static_cast<int>(cluster_rank());
   const int P = gridDim.x / 2, c = blockIdx.x / 2, share = a.tiles / P, rest = a.tiles - share * P;
   const int tile0 = share * c + min(c, rest), tile1 = tile0 + share + (c < rest ? 1 : 0);
@@ -617,12 +628,41 @@ __global__ void __launch_bounds__(kW8Threads, 1)
 
 struct W8Plan {
   int NT, KC, TT, S, tiles, grid;
-  bool pair;
+  bool pair, alone;
 };
+
+// The clusters of S blocks of the kernel with one block an SM that fit on the current device at once (0 where the
+// runtime cannot say).
+static int w8a8_clusters(int S) {
+  using C = W8Cfg<64, true>;
+  const auto kern = w8a8_kernel<64, true>;
+  static std::atomic<int> known[64][5];  // by device ordinal and S, 1 + the number: what a device holds does not change
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && known[dev][S].load() > 0) return known[dev][S].load() - 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(S));
+  cfg.blockDim = dim3(kW8Threads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (dev < 64) known[dev][S].store(n + 1);
+  return n;
+}
 
 // False where the tiles and chunks pass 32 bits.
 static bool w8a8_plan(int64_t M, int64_t N, int64_t K, W8Plan *plan) {
-  W8Plan p;
+  W8Plan p{};
   const int64_t sms = device_sm_count();
   const int64_t rows = (N + kW8Rows - 1) / kW8Rows, pairs = (rows + 1) / 2;
   p.KC = static_cast<int>((K + kW8Chunk - 1) / kW8Chunk);
@@ -641,7 +681,13 @@ static bool w8a8_plan(int64_t M, int64_t N, int64_t K, W8Plan *plan) {
   if (p.pair) {
     p.grid = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2) * 2;
   } else {
-    while (p.S < 4 && tiles * p.S * 2 <= 256 && p.S * 2 <= p.KC) p.S *= 2;
+    // 33 to 64 tokens: one block an SM where that leaves two thirds of the SMs a block or more and every cluster a
+    // place (64 tokens, 4096 -> 4096: 10.5 against 10.8 us, the product by itself 8.4 against 9.7; 14336 -> 4096:
+    // 18.9 against 20.2; 17 to 32 tokens gain nothing: 14336 -> 4096 17.8 against 17.6).
+    for (int S = 4; S >= 1 && p.NT == 64 && !p.alone; --S)
+      if (tiles * S <= sms && tiles * S * 3 >= sms * 2 - 8 && S * 2 <= p.KC && (S == 1 || tiles <= w8a8_clusters(S)))
+        p.alone = true, p.S = S;
+    while (!p.alone && p.S < 4 && tiles * p.S * 2 <= 256 && p.S * 2 <= p.KC) p.S *= 2;
     p.grid = static_cast<int>(p.S > 1 ? tiles * p.S : tiles < 2 * sms ? tiles : 2 * sms);
   }
   *plan = p;
@@ -712,9 +758,10 @@ static cudaError_t launch_w8a8(const W8A8Args &a, bool early, cudaStream_t strea
     return p.NT == 256
                ? launch_w8a8_type<W8PairCfg<256>>(w8a8_pair_kernel<256>, a, p, tm_w, tm_a, early, stream, msg)
                : launch_w8a8_type<W8PairCfg<128>>(w8a8_pair_kernel<128>, a, p, tm_w, tm_a, early, stream, msg);
-  if (p.NT == 16) return launch_w8a8_type<W8Cfg<16>>(w8a8_kernel<16>, a, p, tm_w, tm_a, early, stream, msg);
-  if (p.NT == 32) return launch_w8a8_type<W8Cfg<32>>(w8a8_kernel<32>, a, p, tm_w, tm_a, early, stream, msg);
-  return launch_w8a8_type<W8Cfg<64>>(w8a8_kernel<64>, a, p, tm_w, tm_a, early, stream, msg);
+  if (p.NT == 16) return launch_w8a8_type<W8Cfg<16>>(w8a8_kernel<16, false>, a, p, tm_w, tm_a, early, stream, msg);
+  if (p.NT == 32) return launch_w8a8_type<W8Cfg<32>>(w8a8_kernel<32, false>, a, p, tm_w, tm_a, early, stream, msg);
+  return p.alone ? launch_w8a8_type<W8Cfg<64, true>>(w8a8_kernel<64, true>, a, p, tm_w, tm_a, early, stream, msg)
+                 : launch_w8a8_type<W8Cfg<64>>(w8a8_kernel<64, false>, a, p, tm_w, tm_a, early, stream, msg);
 }
 
 cudaError_t launch_w8a8_pack(const float *W, int64_t N, int64_t K, int8_t *codes, float *s_w, cudaStream_t stream) {

@@ -1,5 +1,9 @@
 """The 8-bit linears on the GPU: weights and activations against the quantizer's
 definition, the product against exact integers.  GPU only."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -64,6 +68,39 @@ def test_product_of_given_codes(dev, M, N, K, with_bias):
     again = torch.full_like(Y, float("nan"))
     mx.w8a8_gemm_into(A, s_a, p, again, bias=bias)
     assert torch.equal(Y.view(torch.int16), again.view(torch.int16))
+
+
+# one block an SM: whole K, two, three or four shares of it, the last tile of channels full, ragged and of one channel;
+# four tokens of which the last are one, and none
+ALONE = [(64, 4096, 1024), (33, 3969, 4096), (50, 6000, 784), (61, 6144, 2064), (40, 8193, 2064), (63, 9472, 512),
+         (34, 13001, 272), (64, 18944, 400), (49, 5000, 14336)]
+
+
+@pytest.mark.parametrize("M,N,K", ALONE)
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_some_tokens_of_few_tiles(dev, M, N, K, with_bias):
+    test_product_of_given_codes(dev, M, N, K, with_bias)
+    test_linear_is_quantizer_and_product(dev, M, N, K)
+
+
+def test_a_first_call_within_a_capture():
+    """Nothing that the launch asks the runtime for, once a process, is refused while a stream is captured."""
+    code = """
+import torch, mixed_precision_quantized_act_b200 as mx
+mx.load()
+p = mx.W8Weights(torch.ones((4096, 1024), dtype=torch.int8, device="cuda"), torch.ones(4096, device="cuda"))
+X = torch.full((64, 1024), 0.5, device="cuda").half()
+Y, ws = torch.zeros((64, 4096), device="cuda").half(), mx.w8a8_linear_workspace(64, p)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    mx.w8a8_linear_into(X, p, Y, ws)
+assert not Y.any()
+g.replay()
+torch.cuda.synchronize()
+assert (Y == 512).all()
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 
 @pytest.mark.parametrize("K", [131056, 131056 - 64])
