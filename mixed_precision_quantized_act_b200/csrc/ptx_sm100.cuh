@@ -354,6 +354,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 // A barrier of all threads of the cluster; what came before an arrival is seen behind the wait.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// The same where nothing has to be seen behind the wait but that this block runs.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The address of this block's shared address `addr` in block `rank` of the cluster, and a store there.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {

@@ -188,8 +188,9 @@ struct W8Walk {
   }
 };
 
-// kAlone: one block an SM, with a deeper ring of stages and a place of their own for a cluster's parts (a barrier of
-// the cluster less).
+// kAlone: one block an SM, with a deeper ring of stages.  kApart: a cluster's parts have a place of their own, not that
+// of the operands (a barrier of the cluster less: 1 token, 4096 -> 4096, 8.5 against 8.0 us); two blocks of 32
+// or 64 tokens have no room for it.
 template <int NT, bool kAlone = false>
 struct W8Cfg {
   static constexpr int kStageW = kW8Rows * kW8Chunk, kStageA = NT * kW8Chunk, kStage = kStageW + kStageA;
@@ -199,17 +200,19 @@ struct W8Cfg {
   static constexpr int kGroups = NT / 4;  // of four tokens
   // parts that a block receives: of each block of the cluster, its groups' tokens x channels, int32
   static constexpr int received(int S) { return S * ((kGroups + S - 1) / S) * 4 * kW8Rows * 4; }
-  static constexpr int kParts = !kAlone ? 0 : received(3) > received(4) ? received(3) : received(4);
+  static constexpr bool kApart = kAlone || NT == 16;
+  static constexpr int kParts = !kApart ? 0 : received(3) > received(4) ? received(3) : received(4);
   static constexpr int kRoom = (kAlone ? 224 : 112) * 1024 - kOut - kParts - 1024 - 2 * NT * 4;
   static constexpr int kMost = kAlone ? 12 : 8;
   static constexpr int kStages = kRoom / kStage < kMost ? kRoom / kStage : kMost;
   static constexpr int kSmem = kStages * kStage + kOut + kParts + 1024;
   // Chunks of weights that are asked for while the quantizer runs: more would make its own loads wait (1 token,
-  // 4096 -> 4096: three 8.45 us, five 8.7, none 8.65; a block alone, 64 tokens, 4096 -> 6144: none 12.3, one 12.8,
-  // all 13.8).
-  static constexpr int kEarly = kAlone ? 0 : 3;
+  // 4096 -> 4096: none 8.65 us, three 8.45, five 8.7; a block alone, 14336 -> 4096, 64 tokens: none 18.8, three
+  // 18.1, four 18.5).
+  static constexpr int kEarly = 3;
+  static_assert(kEarly <= kStages, "the early chunks lie in the ring");
   static constexpr int kTmem = 2 * NT < 32 ? 32 : 2 * NT;
-  static_assert(kAlone || (received(2) <= kStages * kStage && received(4) <= kStages * kStage), "parts in the operands' place");
+  static_assert(kApart || (received(2) <= kStages * kStage && received(4) <= kStages * kStage), "parts in the operands' place");
   static_assert((kAlone ? 1 : 2) * (kSmem + 2048) <= 227 * 1024, "the blocks of an SM");
 };
 
@@ -342,7 +345,9 @@ __global__ void __launch_bounds__(kW8Threads, 2)
   tc_fence_after();
   pdl_launch_dependents();  // only now: a dependent may take tensor memory as it starts
   const uint32_t tmem = tmem_slot;
-  if (kAlone && a.S > 1) cluster_arrive();  // this block runs: others may write to its shared memory
+  // This block runs: others may write to its shared memory.  Relaxed: a release would wait for this warp's copies
+  // of weights (9.8 instead of 9.0 us, 1 token, 4096 -> 6144).
+  if (C::kApart && a.S > 1) cluster_arrive_relaxed();
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(kW8Threads, 2)
     // ------------------------------------------------------------ a cluster's parts: thread = channel
     const int S = a.S, me = static_cast<int>(cluster_rank()), half = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
     const int most = (C::kGroups + S - 1) / S;  // groups of a block
-    uint8_t *parts = smem + (kAlone ? C::kStages * C::kStage + C::kOut : 0);
+    uint8_t *parts = smem + (C::kApart ? C::kStages * C::kStage + C::kOut : 0);
     const auto first_group = [&](int b) { return (C::kGroups * b + S - 1) / S; };  // owner of group g: g S / kGroups
     const int rt = tile0 / a.TT, tt = tile0 - rt * a.TT;
     const int64_t ch = static_cast<int64_t>(rt) * kW8Rows + r, m0 = static_cast<int64_t>(tt) * NT;
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(kW8Threads, 2)
     if (warp >= 4) there = mbar_wait(&acc_full[0], 0, &abort_flag);
     __syncwarp();
     tc_fence_after();
-    if (!kAlone) cluster_arrive();  // every block is done with its operands: parts take their place
+    if (!C::kApart) cluster_arrive();  // every block is done with its operands: parts take their place
     cluster_wait();
     if (warp >= 4 && __all_sync(0xFFFFFFFFu, there)) {
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -682,8 +687,8 @@ static bool w8a8_plan(int64_t M, int64_t N, int64_t K, W8Plan *plan) {
     p.grid = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2) * 2;
   } else {
     // 33 to 64 tokens: one block an SM where that leaves two thirds of the SMs a block or more and every cluster a
-    // place (64 tokens, 4096 -> 4096: 10.5 against 10.8 us, the product by itself 8.4 against 9.7; 14336 -> 4096:
-    // 18.9 against 20.2; 17 to 32 tokens gain nothing: 14336 -> 4096 17.8 against 17.6).
+    // place (64 tokens, 4096 -> 4096: 9.8 against 10.8 us, the product by itself 8.2 against 9.7; 14336 -> 4096:
+    // 18.1 against 20.2; 17 to 32 tokens gain nothing: 14336 -> 4096 17.8 against 17.6).
     for (int S = 4; S >= 1 && p.NT == 64 && !p.alone; --S)
       if (tiles * S <= sms && tiles * S * 3 >= sms * 2 - 8 && S * 2 <= p.KC && (S == 1 || tiles <= w8a8_clusters(S)))
         p.alone = true, p.S = S;
