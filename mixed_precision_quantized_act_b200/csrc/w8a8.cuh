@@ -161,11 +161,10 @@ static cudaError_t launch_row_quantize(const T *X, int64_t stride, int64_t M, in
 // of its own share: whole numbers, so the sum does not depend on who was first.
 //
 // A few tokens are bound by the weights' bytes.  Two blocks an SM with 90 KB of
-// copies under way each serve that better than one with 200 (112 tiles or fewer
-// would else leave SMs idle, 224 load them unevenly), but for 33 to 64 tokens and few
-// tiles; the first copies of the weights start while the quantizer still runs.  Measured on B200 (graph of quantizer and
-// product, weights from HBM): 1 token, 4096 -> 6144: 9.6 us (weights alone 3.8; the
-// product by itself 8.2: its blocks run 7.6 us, 5 of them for the weights, 1.2 for the
+// copies under way each serve that better than one with 200 (224 tiles would load the
+// SMs unevenly), but for few tiles (w8a8_plan); the first copies of the weights start while the quantizer still runs.  Measured on B200 (graph of quantizer and
+// product, weights from HBM): 1 token, 4096 -> 6144: 9.0 us (weights alone 3.8; the
+// product by itself 7.7: its blocks run 7 us, 5 of them for the weights, 0.8 for the
 // exchange of parts), 37 tokens, 4096 -> 28672: 23 us, 5.2 TB/s.  Parts left in global
 // memory for the last block to join them took 14.7 and 31 us.
 // ---------------------------------------------------------------------------
@@ -636,8 +635,8 @@ struct W8Plan {
   bool pair, alone;
 };
 
-// The clusters of S blocks of the kernel with one block an SM that fit on the current device at once (0 where the
-// runtime cannot say).
+// The clusters of S blocks of the kernels with one block an SM that fit on the current device at once (0 where the
+// runtime cannot say): asked for the one of 64 tokens, the others are as large.
 static int w8a8_clusters(int S) {
   using C = W8Cfg<64, true>;
   const auto kern = w8a8_kernel<64, true>;
@@ -686,11 +685,14 @@ static bool w8a8_plan(int64_t M, int64_t N, int64_t K, W8Plan *plan) {
   if (p.pair) {
     p.grid = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2) * 2;
   } else {
-    // 33 to 64 tokens: one block an SM where that leaves two thirds of the SMs a block or more and every cluster a
-    // place (64 tokens, 4096 -> 4096: 9.8 against 10.8 us, the product by itself 8.2 against 9.7; 14336 -> 4096:
-    // 18.1 against 20.2; 17 to 32 tokens gain nothing: 14336 -> 4096 17.8 against 17.6).
-    for (int S = 4; S >= 1 && p.NT == 64 && !p.alone; --S)
-      if (tiles * S <= sms && tiles * S * 3 >= sms * 2 - 8 && S * 2 <= p.KC && (S == 1 || tiles <= w8a8_clusters(S)))
+    // One block an SM.  17 to 64 tokens: where that gives two thirds of the SMs a block and every cluster a place
+    // (4096 -> 4096, 64 tokens: 9.8 against 10.8 us, 32 tokens: 8.7 against 9.1; 14336 -> 4096, 64 tokens: 18.1
+    // against 20.2; 4096 -> 12288, 32 tokens: 13.0 against 15.4).  Up to 16: where K then is not cut, but would be for
+    // two blocks an SM (4096 -> 14336, 1 token: 13.7 against 14.8); with K cut both ways two blocks an SM are
+    // better (4096 -> 6144: 9.0 against 9.4), and with neither (4096 -> 18432: 15.7 against 16.4).
+    for (int S = 4; S >= 1 && !p.alone; --S)
+      if ((p.NT > 16 || (S == 1 && tiles <= 128)) && tiles * S <= sms && tiles * S * 3 >= sms * 2 - 8 &&
+          S * 2 <= p.KC && (S == 1 || tiles <= w8a8_clusters(S)))
         p.alone = true, p.S = S;
     while (!p.alone && p.S < 4 && tiles * p.S * 2 <= 256 && p.S * 2 <= p.KC) p.S *= 2;
     p.grid = static_cast<int>(p.S > 1 ? tiles * p.S : tiles < 2 * sms ? tiles : 2 * sms);
@@ -741,6 +743,13 @@ static cudaError_t launch_w8a8_type(Kernel kern, const W8A8Args &a, const W8Plan
   return e;
 }
 
+template <int NT>
+static cudaError_t launch_w8a8_tokens(const W8A8Args &a, const W8Plan &p, const CUtensorMap &tm_w,
+                                      const CUtensorMap &tm_a, bool early, cudaStream_t stream, const char **msg) {
+  return p.alone ? launch_w8a8_type<W8Cfg<NT, true>>(w8a8_kernel<NT, true>, a, p, tm_w, tm_a, early, stream, msg)
+                 : launch_w8a8_type<W8Cfg<NT>>(w8a8_kernel<NT, false>, a, p, tm_w, tm_a, early, stream, msg);
+}
+
 // `early`: the kernel before this one on the stream is the quantizer, which starts behind all that came before.
 static cudaError_t launch_w8a8(const W8A8Args &a, bool early, cudaStream_t stream, const char **msg) {
   auto enc = get_encode_fn();
@@ -763,10 +772,9 @@ static cudaError_t launch_w8a8(const W8A8Args &a, bool early, cudaStream_t strea
     return p.NT == 256
                ? launch_w8a8_type<W8PairCfg<256>>(w8a8_pair_kernel<256>, a, p, tm_w, tm_a, early, stream, msg)
                : launch_w8a8_type<W8PairCfg<128>>(w8a8_pair_kernel<128>, a, p, tm_w, tm_a, early, stream, msg);
-  if (p.NT == 16) return launch_w8a8_type<W8Cfg<16>>(w8a8_kernel<16, false>, a, p, tm_w, tm_a, early, stream, msg);
-  if (p.NT == 32) return launch_w8a8_type<W8Cfg<32>>(w8a8_kernel<32, false>, a, p, tm_w, tm_a, early, stream, msg);
-  return p.alone ? launch_w8a8_type<W8Cfg<64, true>>(w8a8_kernel<64, true>, a, p, tm_w, tm_a, early, stream, msg)
-                 : launch_w8a8_type<W8Cfg<64>>(w8a8_kernel<64, false>, a, p, tm_w, tm_a, early, stream, msg);
+  if (p.NT == 16) return launch_w8a8_tokens<16>(a, p, tm_w, tm_a, early, stream, msg);
+  if (p.NT == 32) return launch_w8a8_tokens<32>(a, p, tm_w, tm_a, early, stream, msg);
+  return launch_w8a8_tokens<64>(a, p, tm_w, tm_a, early, stream, msg);
 }
 
 cudaError_t launch_w8a8_pack(const float *W, int64_t N, int64_t K, int8_t *codes, float *s_w, cudaStream_t stream) {

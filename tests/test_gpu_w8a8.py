@@ -73,7 +73,8 @@ def test_product_of_given_codes(dev, M, N, K, with_bias):
 # one block an SM: whole K, two, three or four shares of it, the last tile of channels full, ragged and of one channel;
 # four tokens of which the last are one, and none
 ALONE = [(64, 4096, 1024), (33, 3969, 4096), (50, 6000, 784), (61, 6144, 2064), (40, 8193, 2064), (63, 9472, 512),
-         (34, 13001, 272), (64, 18944, 400), (49, 5000, 14336)]
+         (34, 13001, 272), (64, 18944, 400), (49, 5000, 14336), (1, 12300, 1024), (16, 16384, 400), (3, 14337, 4096),
+         (32, 4096, 1024), (17, 6000, 784), (25, 13001, 272), (20, 8193, 2064), (31, 18432, 336)]
 
 
 @pytest.mark.parametrize("M,N,K", ALONE)
