@@ -209,7 +209,7 @@ struct W8Cfg {
   // 4096 -> 4096: none 8.65 us, three 8.45, five 8.7; a block alone, 14336 -> 4096, 64 tokens: none 18.8, three
   // 18.1, four 18.5).
   static constexpr int kEarly = 3;
-  static_assert(kEarly <= kStages, "the early chunks lie in the ring");
+  static_assert(kEarly < kStages, "the early chunks lie in the ring");
   static constexpr int kTmem = 2 * NT < 32 ? 32 : 2 * NT;
   static_assert(kApart || (received(2) <= kStages * kStage && received(4) <= kStages * kStage), "parts in the operands' place");
   static_assert((kAlone ? 1 : 2) * (kSmem + 2048) <= 227 * 1024, "the blocks of an SM");
@@ -353,13 +353,21 @@ __global__ void __launch_bounds__(kW8Threads, 2)
     // The whole warp walks and waits, an elected lane issues: from a one-lane branch 512 tokens x 4096 x 4096 took
     // 13.1 us instead of 12.4.
     pdl_wait();
+    const auto tokens = [&](int s, const W8Walk &w) {
+      tma_load_2d(smem + s * C::kStage + C::kStageW, &tm_a, &full[s], w.chunk * kW8Chunk, w.tt * NT);
+    };
     int s = 0, issued = 0;
     uint32_t phase = 1;
-    for (W8Walk w(tile0, a.TT, k0, k1); issued < chunks; ++issued, w.next()) {
+    W8Walk w(tile0, a.TT, k0, k1);
+    for (; issued < ahead; ++issued, ++s, w.next()) {
+      if (elect_one()) tokens(s, w);
+      __syncwarp();
+    }
+    for (; issued < chunks; ++issued, w.next()) {
       if (issued >= C::kStages && !warp_wait(&empty[s], phase, &abort_flag)) break;
       if (elect_one()) {
-        if (issued >= ahead) weights(s, w);
-        tma_load_2d(smem + s * C::kStage + C::kStageW, &tm_a, &full[s], w.chunk * kW8Chunk, w.tt * NT);
+        weights(s, w);
+        tokens(s, w);
       }
       __syncwarp();
       if (++s == C::kStages) s = 0, phase ^= 1;
@@ -494,6 +502,11 @@ struct W8PairCfg {
   static constexpr int kCols = 32, kOutCols = 16, kOut = 8 * kOutCols * 32 * 2;
   static constexpr int kRoom = 224 * 1024 - kOut - 1024 - 2 * NT * 4;
   static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
+  // Chunks of weights ahead of the quantizer's codes: none for tiles of 128 tokens (300 tokens, 4096 -> 6144: 14.5
+  // against 15.0 us with three, 15.4 with all of the ring; 512 tokens, 4096 -> 4096: 15.8, 16.1, 16.3), three for 256
+  // (130 tokens, 4096 -> 28672: 29.8, 29.6, 30.2).
+  static constexpr int kEarly = NT == 128 ? 0 : 3;
+  static_assert(kEarly < kStages, "the early chunks lie in the ring");
   static constexpr int kSmem = kStages * kStage + kOut + 1024;
   static constexpr int kTmem = 2 * NT;
 };
@@ -545,7 +558,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   };
   int ahead = 0;  // chunks whose weights are under way
   if (warp == 0 && a.early) {
-    for (W8Walk w(tile0, a.TT, 0, a.KC); ahead < C::kStages && ahead < chunks; ++ahead, w.next()) {
+    for (W8Walk w(tile0, a.TT, 0, a.KC); ahead < C::kEarly && ahead < chunks; ++ahead, w.next()) {
       if (elect_one()) weights(ahead, w);
       __syncwarp();
     }
@@ -559,15 +572,22 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ loads, each block's own
     pdl_wait();
+    const auto tokens = [&](int s, const W8Walk &w) {
+      tma_load_2d_pair(smem + s * C::kStage + C::kStageW, &tm_a, cluster_map(smem_u32(&full[s]), 0),
+                       w.chunk * kW8Chunk, w.tt * NT + side * (NT / 2));
+    };
     int s = 0;
     uint32_t phase = 1;
     W8Walk w(tile0, a.TT, 0, a.KC);
-    for (int issued = 0; issued < chunks; ++issued, w.next()) {
+    for (; s < ahead; ++s, w.next()) {
+      if (elect_one()) tokens(s, w);
+      __syncwarp();
+    }
+    for (int issued = ahead; issued < chunks; ++issued, w.next()) {
       if (issued >= C::kStages && !warp_wait(&empty[s], phase, &abort_flag)) break;
       if (elect_one()) {
-        if (issued >= ahead) weights(s, w);
-        tma_load_2d_pair(smem + s * C::kStage + C::kStageW, &tm_a, cluster_map(smem_u32(&full[s]), 0),
-                         w.chunk * kW8Chunk, w.tt * NT + side * (NT / 2));
+        weights(s, w);
+        tokens(s, w);
       }
       __syncwarp();
       if (++s == C::kStages) s = 0, phase ^= 1;
