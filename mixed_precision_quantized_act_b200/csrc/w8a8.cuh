@@ -691,12 +691,13 @@ static bool w8a8_plan(int64_t M, int64_t N, int64_t K, W8Plan *plan) {
   const int64_t rows = (N + kW8Rows - 1) / kW8Rows, pairs = (rows + 1) / 2;
   p.KC = static_cast<int>((K + kW8Chunk - 1) / kW8Chunk);
   p.NT = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  // Two blocks on a tile where that still leaves 64 of them (N = 4096: 256 tokens 11.7 against 12.3 us, 128 tokens,
-  // which leave 32, 11.6 against 10.4; N = 28672, 128 tokens: 25 against 33 us).  A chunk of 128 tokens takes
-  // some 250 ns, one of 256 some 350: whichever needs less for its rounds (N = 4096: 512 tokens 12.4 against
-  // 15.1 us, 1024 tokens 19.8 against 15.9).
+  // Two blocks on a tile where there are more tiles of 64 tokens and 128 channels than SMs (one tile an SM
+  // is faster: 256 tokens, N = 4096 12.6 against 13.7 us, 128 tokens, N = 8192 12.9 against 13.9; more
+  // than that: 100 tokens, N = 10240 15.7 against 14.3, 256 tokens, N = 6144 15.4 against 14.2).  A chunk of 128 tokens
+  // takes some 250 ns, one of 256 some 350: whichever needs less for its rounds (N = 4096, the product by itself:
+  // 512 tokens 12.4 against 15.1 us, 1024 tokens 19.8 against 15.9).
   const int64_t narrow = pairs * ((M + 127) / 128), broad = pairs * ((M + 255) / 256), slots = sms / 2;
-  p.pair = M > 64 && narrow >= 32;
+  p.pair = M > 64 && rows * ((M + 63) / 64) > sms;
   if (p.pair) p.NT = M > 128 && (broad + slots - 1) / slots * 7 < (narrow + slots - 1) / slots * 5 ? 256 : 128;
   const int64_t TT = (M + p.NT - 1) / p.NT, tiles = (p.pair ? pairs : rows) * TT;
   if (tiles * p.KC > 0x7FFFFFFF) return false;

@@ -84,6 +84,18 @@ def test_some_tokens_of_few_tiles(dev, M, N, K, with_bias):
     test_linear_is_quantizer_and_product(dev, M, N, K)
 
 
+# two blocks on a tile of 128 tokens, and of 256: the last tile of either side full, ragged, for the first block alone
+PAIRS = [(65, 13000, 48), (70, 9600, 640), (127, 9601, 528), (300, 6144, 272), (500, 4096, 1024), (511, 4097, 400),
+         (1025, 4096, 2064), (129, 20000, 1040), (700, 16300, 528), (1024, 4096, 4096), (1500, 2177, 144)]
+
+
+@pytest.mark.parametrize("M,N,K", PAIRS)
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_many_tokens(dev, M, N, K, with_bias):
+    test_product_of_given_codes(dev, M, N, K, with_bias)
+    test_linear_is_quantizer_and_product(dev, M, N, K)
+
+
 def test_a_first_call_within_a_capture():
     """Nothing that the launch asks the runtime for, once a process, is refused while a stream is captured."""
     code = """
