@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT>::kThreads, 1) kv8_decode_kernel(
 // Prompts: the 4-bit cache's kernel (kv4_prompt.cuh) with these rows.  A block's
 // scales are taken once for 16 columns, the values' as a summand of the exponent.
 // 1024 and 866 new tokens behind contexts of 8192 and 6354, 32 query and 8 key heads
-// of 128: 250 to 258 us, 845 to 820 TFLOP/s (52 to 50 % of the measured bf16 burst rate); 16 and 4 heads
+// of 128: 250 to 270 us, 845 to 785 TFLOP/s (52 to 48 % of the measured bf16 burst rate); 16 and 4 heads
 // of 64: 120 us.  The softmax bounds it: 64 columns take its warps some 2200 clocks, of
 // which the exponentials of both tiles need 1024.
 // ---------------------------------------------------------------------------
