@@ -293,7 +293,9 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT>::kThreads, 1) kv8_decode_kernel(
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         // ---- weights
-        const float rp = __fdividef(1.0f, sv[x] < kKv8LeastScale ? kKv8LeastScale : sv[x]);
+        // A NaN scale counts as the least one here: the weights of the rows that see a key of the block are NaN (ls),
+        // those of a row that sees none are zero and add nothing.
+        const float rp = __fdividef(1.0f, fmaxf(sv[x], kKv8LeastScale));
         const float rr = sv[x] >= 0.125f * S ? rp : 0.0f;
         uint32_t pf[NT][2];
 #pragma unroll
