@@ -764,8 +764,12 @@ MIXLLM_API mixllm_status mixllm_head_norm_rope(const void *q_f16, int64_t q_stri
  * block's scale NaN, and with it all of the block's tokens, until the block's
  * first row is written again.
  *   slots     device int64 [n_slots], distinct; a negative one skips the token
- *             (its q_out row too).  The tokens of one block stand one behind
- *             the other (as mixllm_kv4_assign lists them).
+ *             (its q_out row too).  The tokens of one block follow one another
+ *             (as mixllm_kv4_assign lists them), with nothing between them but
+ *             skipped ones, and within 16 places of the list: the keys and
+ *             values of those farther behind the block's first one are left
+ *             out and recorded (MIXLLM_ERR_BOUNDS).  A block whose tokens
+ *             another block's stand between is left with undefined contents.
  *   k, v      device fp16 [n_slots, kv_heads, head_dim], tokens stride apart
  *   q, q_out  device fp16 [n_slots, q_heads, head_dim] likewise; q_heads = 0:
  *             none.  q_out may be q.

@@ -21,8 +21,9 @@ constexpr int kKv8Block = 16;  // tokens of one scale
 
 // ---------------------------------------------------------------------------
 // Append.  A block of 16 tokens shares a scale, so its tokens are two warps'
-// work: they take a run of new tokens of one block (neighbours in the list of
-// slots) for one head, key or value, keep their rows in registers, and
+// work: they take a run of new tokens of one block (within 16 places of the list
+// of slots, skipped ones among them) for one head, key or value, keep their rows
+// in registers, and
 //   s = max(s before, amax / 127)   (before: 0 where the run holds the block's first row)
 //   code = 128 + rne(x / s), and where s has grown the block's other rows are
 //   re-coded: 128 + rne((code - 128) * (s before / s)).
@@ -60,15 +61,16 @@ struct Kv8Half {
   uint32_t rows;
 };
 
-// One run's rows of one head, key (kv = 0) or value: two warps, eight tokens each.
-// Lane i's `slot` and `pos` are those of token t0 + i (slot -1: none).  What depends
-// on slot and position alone is loaded before anything is used.
+// One run's rows of one head, key (kv = 0) or value: the 16 places of the list from
+// t0 + first on, two warps, eight places each; bit j of `places`: there is a token of
+// the run at the j-th.  Lane i's `slot` and `pos` are those of place t0 + i.  What
+// depends on slot and position alone is loaded before anything is used.
 template <int D, int kNorm>
 __device__ __forceinline__ void kv8_write_run(const Kv8AppendArgs &a, const HeadArgs &heads, int64_t t0, int64_t slot,
-                                              int pos, int first, int count, int kv, int h, Kv8Half *halves) {
+                                              int pos, int first, uint32_t places, int kv, int h, Kv8Half *halves) {
   constexpr int kLanes = D / 8, kTogether = 32 / kLanes, kPasses = kKv8Block / 2 / kTogether;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % kLanes;
-  const int mine = (warp & 1) * (kKv8Block / 2) + lane / kLanes;  // of the run's tokens, this lane's first
+  const int mine = (warp & 1) * (kKv8Block / 2) + lane / kLanes;  // of the run's places, this lane's first
   const int64_t block = __shfl_sync(0xFFFFFFFFu, slot, first) >> 4;
   const int64_t base = kv8_row(a.cache, block << 4, kv, h);
   float *scale = a.cache.scales + (base >> 4);
@@ -82,7 +84,7 @@ __device__ __forceinline__ void kv8_write_run(const Kv8AppendArgs &a, const Head
     const int j = mine + p * kTogether;
     row_of[p] = static_cast<int>(__shfl_sync(0xFFFFFFFFu, slot, (first + j) & 31)) & (kKv8Block - 1);
     x[p] = make_uint4(0, 0, 0, 0);
-    if (j < count) x[p] = *reinterpret_cast<const uint4 *>(src + (first + j) * stride + h * D + sub * 8);
+    if (places >> j & 1u) x[p] = *reinterpret_cast<const uint4 *>(src + (first + j) * stride + h * D + sub * 8);
     else row_of[p] = -1;
   }
   // ---- the rows, normalized and rotated
@@ -90,7 +92,7 @@ __device__ __forceinline__ void kv8_write_run(const Kv8AppendArgs &a, const Head
   float amax = 0.0f;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    if ((warp & 1) * (kKv8Block / 2) + p * kTogether >= count) continue;  // the same for the whole warp
+    if (places >> ((warp & 1) * (kKv8Block / 2) + p * kTogether) == 0) continue;  // the same for the whole warp
     const int at = __shfl_sync(0xFFFFFFFFu, pos, (first + mine + p * kTogether) & 31);
     if (heads.rope && row_of[p] >= 0 && (at < 0 || at >= heads.max_pos)) {
       if (kv == 0 && sub == 0) record_status(kStatusBounds);
@@ -164,6 +166,50 @@ __device__ __forceinline__ void kv8_write_run(const Kv8AppendArgs &a, const Head
   }
 }
 
+// The last slot of a cached token before place `end` of the list, or -1: for lists with long runs of skipped ones.
+// The whole warp.
+__device__ __forceinline__ int64_t kv8_last_before(const int64_t *slots, int64_t end, int64_t limit) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (; end > 0; end -= 128) {
+    int64_t s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = end - 32 * (i + 1) + lane;
+      s[i] = at >= 0 ? slots[at] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t there = __ballot_sync(0xFFFFFFFFu, s[i] >= 0 && s[i] < limit);
+      if (there) return __shfl_sync(0xFFFFFFFFu, s[i], 31 - __clz(there));
+    }
+  }
+  return -1;
+}
+
+// A run is 16 places.  Records tokens of places t0 .. t0 + 15 whose run began before t0 and that lie behind those: the
+// first such token of a block has another of its block in the 16 places before it, whose run began in the 32 before t0
+// then, or it has none.  The whole warp.
+__device__ __forceinline__ void kv8_record_far(const int64_t *slots, int64_t t0, int64_t T, int64_t limit) {
+  const int lane = threadIdx.x & 31;
+  const int64_t slot = lane < kKv8Block && t0 + lane < T ? slots[t0 + lane] : -1;
+  const int64_t back = t0 + lane >= 32 ? slots[t0 + lane - 32] : -1;  // of the 32 places before t0
+  const bool is = slot >= 0 && slot < limit, is_back = back >= 0 && back < limit;
+  const uint32_t there = __ballot_sync(0xFFFFFFFFu, is), there_back = __ballot_sync(0xFFFFFFFFu, is_back);
+  if (!there) return;
+  const int64_t block = __shfl_sync(0xFFFFFFFFu, slot, __ffs(there) - 1) >> 4;
+  const uint32_t another = __ballot_sync(0xFFFFFFFFu, is && slot >> 4 != block);
+  const int far = 31 - __clz(there & (another ? (another & -another) - 1u : ~0u));  // the first block's last token here
+  const uint32_t same = __ballot_sync(0xFFFFFFFFu, is_back && back >> 4 == block), other = there_back & ~same;
+  const uint32_t chain = other ? same & ~((2u << (31 - __clz(other))) - 1u) : same;
+  if (chain) {
+    if (far + 32 - (__ffs(chain) - 1) >= kKv8Block) record_status(kStatusBounds);
+  } else if (!there_back) {
+    const int64_t last = kv8_last_before(slots, t0 - 32, limit);
+    if (last >= 0 && last >> 4 == block) record_status(kStatusBounds);
+  }
+}
+
 struct Kv8Grid {
   unsigned q_blocks, q_groups;  // blocks of queries; groups of `per` heads
   int per;
@@ -205,36 +251,35 @@ __global__ void __launch_bounds__(kHeadThreads, 3) kv8_append_kernel(const Kv8Ap
   __shared__ Kv8Half halves[kHeadThreads / 32];
   const int lane = threadIdx.x & 31, team = threadIdx.x >> 6;
   const int64_t t0 = static_cast<int64_t>(tile) * kKv8Block;
-  int64_t slot = t0 + lane < heads.T ? a.slots[t0 + lane] : -1, prev = lane == 0 && t0 > 0 ? a.slots[t0 - 1] : -1;
+  int64_t slot = t0 + lane < heads.T ? a.slots[t0 + lane] : -1, last = t0 > 0 ? a.slots[t0 - 1] : -1;
   const int pos = heads.rope && t0 + lane < heads.T ? heads.positions[t0 + lane] : 0;
   if (slot >= limit) {
     record_status(kStatusBounds);
     slot = -1;
   }
-  if (prev >= limit) prev = -1;
-  {
-    const int64_t left = __shfl_up_sync(0xFFFFFFFFu, slot, 1);
-    if (lane > 0) prev = left;
-  }
-  const bool begins = slot >= 0 && (prev < 0 || prev >> 4 != slot >> 4);
-  const uint32_t begin = __ballot_sync(0xFFFFFFFFu, begins);
-  const uint32_t ends = begin | __ballot_sync(0xFFFFFFFFu, slot < 0);  // no run goes on here
+  if (last >= limit) last = -1;
+  // A token begins a run unless the last one before it is of the same block, however many skipped ones stand between.
+  const uint32_t there = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+  if (last < 0 && t0 > 0 && (there & 0xFFFFu)) last = kv8_last_before(a.slots, t0 - 1, limit);
+  const uint32_t below = there & ((1u << lane) - 1u);
+  const int64_t left_of = __shfl_sync(0xFFFFFFFFu, slot, below ? 31 - __clz(below) : 0);
+  const int64_t prev = below ? left_of : last;
+  const uint32_t begin = __ballot_sync(0xFFFFFFFFu, slot >= 0 && (prev < 0 || prev >> 4 != slot >> 4));
   const int pair0 = g * grid.pairs, pairs = min(2 * a.cache.H - pair0, grid.pairs);
   int item = 0;
   for (uint32_t left = begin & 0xFFFFu; left; left &= left - 1) {
     const int first = __ffs(left) - 1;
-    const uint32_t behind = ends & ~((2u << first) - 1u);
-    int count = (behind ? __ffs(behind) - 1 : 32) - first;
-    if (count > kKv8Block) {  // a slot that is there twice
-      if (lane == 0) record_status(kStatusBounds);
-      count = kKv8Block;
-    }
+    const uint32_t later = begin & ~((2u << first) - 1u);
+    const uint32_t rest = there & ~((1u << first) - 1u) & (later ? (later & -later) - 1u : ~0u);  // of its block
+    const uint32_t run = rest & (0xFFFFu << first);  // what is farther behind is left out, and recorded
+    if (rest != run) record_status(kStatusBounds);
     for (int p = 0; p < pairs; ++p, ++item) {
       if (item % (grid.split * kTeams) != static_cast<int>(part) * kTeams + team) continue;
       const int pair = pair0 + p, kv = pair >= a.cache.H;
-      kv8_write_run<D, kNorm>(a, heads, t0, slot, pos, first, count, kv, pair - kv * a.cache.H, halves);
+      kv8_write_run<D, kNorm>(a, heads, t0, slot, pos, first, run >> first, kv, pair - kv * a.cache.H, halves);
     }
   }
+  if (g == 0 && part == 0 && threadIdx.x < 32) kv8_record_far(a.slots, t0, heads.T, limit);
   pdl_wait();  // the queries' kernel, where there is one, runs beside this one: who waits for this waits for it
 }
 

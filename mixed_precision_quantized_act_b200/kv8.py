@@ -50,12 +50,13 @@ def kv8_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, dev
 def kv8_append_into(k, v, slots, cache: KV8Cache, q=None, q_out=None, positions=None, rope=None, w_q=None, w_k=None,
                     eps: float = 1e-6, stream=None):
     """Quantizes k and v fp16 [T, kv_heads, head_dim] into their slots int64
-    [T] (negative: skipped; the tokens of a block of 16 one behind the other);
-    with w_k, w_q fp16 [head_dim] every key and query head is normalized first,
-    with rope fp32 [max_pos, rotary] and positions int32 [T] rotated: q fp16
-    [T, q_heads, head_dim] into q_out (which may be q).  A block's scale grows
-    with its tokens, and its older rows are re-coded then (mixllm_kv8_append).
-    Rows may be strided: slices of one qkv output serve."""
+    [T] (negative: skipped; the tokens of a block of 16 follow one another, with
+    only skipped ones between them, within 16 places of the list); with w_k, w_q
+    fp16 [head_dim] every key and query head is normalized first, with rope fp32
+    [max_pos, rotary] and positions int32 [T] rotated: q fp16 [T, q_heads,
+    head_dim] into q_out (which may be q).  A block's scale grows with its tokens,
+    and its older rows are re-coded then (mixllm_kv8_append).  Rows may be strided:
+    slices of one qkv output serve."""
     dev = cache.index
     T = slots.shape[0]
     D = cache.head_dim
