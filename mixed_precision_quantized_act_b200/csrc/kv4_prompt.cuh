@@ -453,7 +453,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typenam
         look_up();
       }
       const bool next_ok = page_ok;
-      if (!mbar_wait(&k_empty[s], phase ^ 1, &abort_flag)) break;
+      // A warp leaves as one: shuffles follow, which would wait for a lane that gave up by itself.  (warp_wait, which
+      // votes once more, takes 261 us instead of 253 for the 8-bit cache's prompts.)
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&k_empty[s], phase ^ 1, &abort_flag))) break;
       const int at = it & (kPmScaleRing - 1);
       {
         const float ks = F::scale(km) * scale2, vs = F::scale(vm);
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typenam
       store(k_s + s * kOperand, kr, km);
       mbar_arrive(&k_full[s]);
       if (left > 1) km = F::load(a.cache, row, kr);
-      if (!mbar_wait(&v_empty[s], phase ^ 1, &abort_flag)) break;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&v_empty[s], phase ^ 1, &abort_flag))) break;
       store(v_s + s * kOperand, vr, vm);
       mbar_arrive(&v_full[s]);
       if (left > 1) vm = F::load(a.cache, row < 0 ? row : row + to_value, vr);
