@@ -241,7 +241,7 @@ __device__ __forceinline__ bool w8_write_tile(const W8Job &a, int64_t ch0, int64
   for (int j = tid - 128; j < NT; j += 256) token_scale[j] = j < tokens ? a.s_a[m0 + j] : 0.0f;
   const float sw = ch < a.N ? a.s_w[ch] : 0.0f;
   const float bias = a.bias && ch < a.N ? __half2float(a.bias[ch]) : 0.0f;
-  if (!named_bar_and(1, 256, mbar_wait(full, parity, abort))) return false;  // also publishes the scales
+  if (!named_bar_and(1, 256, warp_wait(full, parity, abort))) return false;  // also publishes the scales; warps arrive whole
   tc_fence_after();
   const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll 1
