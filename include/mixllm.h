@@ -578,7 +578,10 @@ MIXLLM_API mixllm_status mixllm_kv4_assign(const int32_t *ctx_lens, const int32_
  *               x_i cos_i - x_j sin_i,  x_j cos_i + x_i sin_i  (j = i + rotary/2)
  *             in fp32 (each product and sum rounded) and are rounded to fp16.
  *             rotary = 0: no rotation (both NULL); else a multiple of 16 up to
- *             head_dim.
+ *             head_dim.  A token whose position is negative or not below max_pos
+ *             is skipped like one without a slot, and recorded
+ *             (MIXLLM_ERR_BOUNDS); for heads that have been rotated before,
+ *             positions with rotary = 0 and a positive max_pos are checked alone.
  * k, v, q, q_out, rope 16-byte aligned, strides (in elements) multiples of 8.
  * n_slots = 0 is a no-op.  Asynchronous on `stream`.
  */

@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv4_append_kernel(const App
   if (t >= a.T) return;
   const int64_t slot = a.slots[t];
   if (slot < 0) return;  // padding behind the last token
-  const int64_t pos = a.rope ? a.positions[t] : 0;
-  if (slot >= a.cache.pages << a.cache.page_log2 || pos < 0 || (a.rope && pos >= a.max_pos)) {
+  const int64_t pos = a.positions ? a.positions[t] : 0;
+  if (slot >= a.cache.pages << a.cache.page_log2 || pos < 0 || (a.positions && pos >= a.max_pos)) {
     if (sub == 0) record_status(kStatusBounds);
     return;
   }

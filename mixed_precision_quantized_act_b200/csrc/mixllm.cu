@@ -813,7 +813,7 @@ mixllm_status mixllm_kv4_append(uint8_t *codes, uint32_t *meta, int64_t pages, i
                        q_heads,
                        static_cast<__half *>(q_out_f16),
                        q_out_stride,
-                       positions,
+                       max_pos > 0 ? positions : nullptr,  // (a rotation has them)
                        rotary > 0 ? rope : nullptr,
                        max_pos,
                        rotary};

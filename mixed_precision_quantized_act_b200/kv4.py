@@ -80,11 +80,14 @@ def kv4_assign_into(ctx_lens, new_lens, block_table, free_pages, free_count, pag
          ptr(cu_new), ptr(slots), ptr(positions), T, ptr(free_left), ptr(status))
 
 
-def kv4_append_into(k, v, slots, cache: KV4Cache, q=None, q_out=None, positions=None, rope=None, stream=None):
+def kv4_append_into(k, v, slots, cache: KV4Cache, q=None, q_out=None, positions=None, rope=None, stream=None,
+                    max_pos: int = 0):
     """Quantizes k and v fp16 [T, kv_heads, head_dim] into their slots int64
     [T] (negative: skipped); with rope fp32 [max_pos, rotary] and positions
     int32 [T], rotates the keys and q fp16 [T, q_heads, head_dim] (into q_out,
-    which may be q) first.  Rows may be strided: slices of one qkv output serve."""
+    which may be q) first.  Without rope, max_pos > 0 says how far the positions
+    of heads that were rotated before may go: tokens out of that range are skipped
+    as they are with it.  Rows may be strided: slices of one qkv output serve."""
     dev = cache.index
     T = slots.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
@@ -92,7 +95,7 @@ def kv4_append_into(k, v, slots, cache: KV4Cache, q=None, q_out=None, positions=
         raise ValueError("q needs q_out, and rope positions")
     need(slots, "slots", _I64, (T,), dev)
     k_stride, v_stride = rows(k, "k", _F16, shape, dev), rows(v, "v", _F16, shape, dev)
-    q_heads = q_stride = out_stride = max_pos = rotary = 0
+    q_heads = q_stride = out_stride = rotary = 0
     if q is not None:
         q_heads = q.shape[1]
         q_stride = rows(q, "q", _F16, (T, q_heads, cache.head_dim), dev)
@@ -100,6 +103,9 @@ def kv4_append_into(k, v, slots, cache: KV4Cache, q=None, q_out=None, positions=
     if rope is not None:
         max_pos, rotary = rope.shape
         need(rope, "rope", _F32, rope.shape, dev)
+    elif max_pos > 0 and positions is None:
+        raise ValueError("max_pos needs positions")
+    if max_pos > 0:
         need(positions, "positions", _I32, (T,), dev)
     call("mixllm_kv4_append", dev, stream, *cache._args(), ptr(slots), T, ptr(k), k_stride, ptr(v), v_stride, ptr(q),
          q_stride, q_heads, ptr(q_out), out_stride, ptr(positions), ptr(rope), max_pos, rotary)

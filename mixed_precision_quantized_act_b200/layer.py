@@ -193,7 +193,9 @@ class AttentionBlock:
                                 eps=self.head_eps, **turn)
         elif self.k is not None:
             norm.head_norm_rope_into(q, self.q, self.w_q, k=k, k_out=self.k, w_k=self.w_k, eps=self.head_eps, **turn)
-            kv4.kv4_append_into(self.k, v, slots, self.cache, stream=stream)
+            # the norms' kernel left the keys of positions beyond the table as they were: skip those here, too
+            checked = dict(positions=positions, max_pos=self.rope.shape[0]) if self.rope is not None else {}
+            kv4.kv4_append_into(self.k, v, slots, self.cache, stream=stream, **checked)
         else:
             kv4.kv4_append_into(k, v, slots, self.cache, q=q, q_out=self.q, **turn)
 
