@@ -706,16 +706,21 @@ static bool w8a8_plan(int64_t M, int64_t N, int64_t K, W8Plan *plan) {
   if (p.pair) {
     p.grid = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2) * 2;
   } else {
-    // One block an SM.  17 to 64 tokens: where that gives two thirds of the SMs a block and every cluster a place
-    // (4096 -> 4096, 64 tokens: 9.8 against 10.8 us, 32 tokens: 8.7 against 9.1; 14336 -> 4096, 64 tokens: 18.1
-    // against 20.2; 4096 -> 12288, 32 tokens: 13.0 against 15.4).  Up to 16: where K then is not cut, but would be for
-    // two blocks an SM (4096 -> 14336, 1 token: 13.7 against 14.8); with K cut both ways two blocks an SM are
-    // better (4096 -> 6144: 9.0 against 9.4), and with neither (4096 -> 18432: 15.7 against 16.4).
+    // One block an SM.  17 to 64 tokens: where that gives five eighths of the SMs a block and every cluster a place
+    // (4096 -> 4096, 64 tokens: 9.6 against 10.5 us, 32 tokens: 8.7 against 9.1; 14336 -> 4096, 64 tokens: 18.1
+    // against 20.2; 4096 -> 12288, 32 tokens: 12.4 against 14.9, 4096 -> 11904, 93 blocks: 12.3 against 14.8; with fewer,
+    // 14336 -> 5888, 32 tokens, 92 blocks: 20.7 against 20.2).  Up to 16: where K then is not cut, but would be for
+    // two blocks an SM (4096 -> 14336, 1 token: 13.8 against 14.4); with K cut both ways two blocks an SM are
+    // better (4096 -> 6144: 9.0 against 9.4), and with neither (4096 -> 18432: 15.7 against 16.5).
+    // K is cut while the shares leave an eighth of the places (two an SM) free, which clusters cannot all take, in
+    // whole clusters of four (1 token, 4096 -> 16384, 256 shares: 16.4 us, not cut 15.0, of one block an SM 15.2;
+    // 4096 -> 8192, 256 shares: 9.9; 4096 -> 8320, 130 shares: 10.7).
+    const int64_t most = sms * 7 / 4 / 4 * 4;
     for (int S = 4; S >= 1 && !p.alone; --S)
-      if ((p.NT > 16 || (S == 1 && tiles <= 128)) && tiles * S <= sms && tiles * S * 3 >= sms * 2 - 8 &&
+      if ((p.NT > 16 || (S == 1 && tiles * 2 <= most)) && tiles * S <= sms && tiles * S * 8 >= sms * 5 &&
           S * 2 <= p.KC && (S == 1 || tiles <= w8a8_clusters(S)))
         p.alone = true, p.S = S;
-    while (!p.alone && p.S < 4 && tiles * p.S * 2 <= 256 && p.S * 2 <= p.KC) p.S *= 2;
+    while (!p.alone && p.S < 4 && tiles * p.S * 2 <= most && p.S * 2 <= p.KC) p.S *= 2;
     p.grid = static_cast<int>(p.S > 1 ? tiles * p.S : tiles < 2 * sms ? tiles : 2 * sms);
   }
   *plan = p;
