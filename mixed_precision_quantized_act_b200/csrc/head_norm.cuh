@@ -5,7 +5,8 @@
 #include <cuda_fp16.h>
 #include <cstdint>
 
-#include "kv4_ptx.cuh"  // pairs of floats
+#include "gemm_w4w8a8.cuh"  // device_sm_count
+#include "kv4_ptx.cuh"      // pairs of floats
 #include "launch.h"
 #include "norm.cuh"
 #include "ptx_sm100.cuh"
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kHeadThreads, 4) head_norm_rope_kernel(const H
 
 // Heads of one lane: sixteen where the call fills the GPU all the same, one where it is latency that counts.
 static int turn_heads_per_lane(int64_t T, int heads, int D) {
-    int per = T * heads * (D / 8) >= 8ll * 148 * 2048 ? 16 : 1;
+  int per = T * heads * (D / 8) >= 8ll * device_sm_count() * 2048 ? 16 : 1;
   while ((heads + per - 1) / per > 65535 / 2) ++per;
   return per;
 }
