@@ -755,8 +755,9 @@ MIXLLM_API mixllm_status mixllm_head_norm_rope(const void *q_f16, int64_t q_stri
 
 /*
  * Writes the keys and values of n_slots tokens into their slots and, on the way,
- * normalizes and rotates keys and queries like mixllm_head_norm_rope (one
- * kernel).  For every block of 16 tokens, head and kind that gets new rows:
+ * normalizes and rotates keys and queries like mixllm_head_norm_rope (one kernel
+ * up to 512 tokens; above, the queries take one of their own that runs beside the
+ * other).  For every block of 16 tokens, head and kind that gets new rows:
  *   s     = max(s before, amax / 127) over the new rows, where s before is 0 if
  *           the block's first row is among them, else the block's scale
  *   code  = 128 + clamp(rne(x / s), -127, 127)   (128 where s = 0)

@@ -547,8 +547,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) kv4_prompt_kernel(const typenam
           return (b == 0 ? there.x : there.y) &
                  (n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u));
         };
-        // the logarithm of the row's largest weight; a value scale of zero counts as 2^-24, so that the sum of
-        // p stays finite, too
+        // the logarithm of the row's largest weight; a value scale of zero counts as the format's least (a token's own
+        // as 2^-24, a block's as 2^-40), so that the sum of p stays finite, too
         const auto maximum = [&] {
           float top = -INFINITY;
 #pragma unroll

@@ -54,7 +54,7 @@ namespace mixllm {
 // 8 key heads of 128: 102 us, 5.3 TB/s (81 % of the measured copy rate; the loops take
 // 82 us of it, at that rate, the rest is the first loads, SMs that end 10 us apart, and
 // the joins); 4 requests of 100000 to 131071 tokens, 64 and 8 heads: 164 us, 5.9 TB/s
-// (90 %); one request of 1003 tokens: 9.6 us.
+// (90 %); one request of 1003 tokens: 9.4 us.
 // ---------------------------------------------------------------------------
 constexpr float kKv8LeastScale = 0x1p-40f;
 

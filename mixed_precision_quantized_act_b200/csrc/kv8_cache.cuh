@@ -32,10 +32,12 @@ constexpr int kKv8Block = 16;  // tokens of one scale
 // tokens in a kernel of their own that runs beside this one.
 //
 // HBM-bound by its bytes, in fact by latency: slots, then rows, table and scale
-// together, then the write.  4101 tokens of 64 + 8 heads of 128: 39.6 us (queries 27,
-// keys and values 17.4, overlapping) and 8.5 us to read back, for 28.6 us of traffic;
+// together, then the write.  4101 tokens of 64 + 16 heads of 128: 40.5 us (queries 25,
+// keys and values 18.1, overlapping) and 8.7 us to read back, for 28.6 us of traffic;
 // one warp a run took 24 us for keys and values (128 registers, 16 warps an SM; now 24),
-// queries in this kernel 37.  32 tokens: 8.8 us.
+// queries in this kernel 37.  32 tokens: 8.7 us.  Which places of a run hold a token is
+// one mask for the warp: a row number for every lane spills (51.2 us with the read-back
+// instead of 49.5).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int64_t kv8_row(const Kv8Cache &c, int64_t slot, int kv, int h) {
   const int64_t page = slot >> c.page_log2;

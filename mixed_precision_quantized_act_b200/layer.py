@@ -124,7 +124,7 @@ class AttentionBlock:
     before a W4.4A8 qkv the residual update and its norm are one kernel with the
     quantization.  w_q and w_k, fp16 [head_dim], are the weights of the query and
     key heads' norms (None: none); with a KV8Cache these, the rotation and the
-    write are one kernel.  Buffers are allocated once, and ready for any stream when
+    write are one call (one kernel up to 512 tokens).  Buffers are allocated once, and ready for any stream when
     the constructor returns; `run` allocates nothing and can be captured into a graph,
     lengths and slots being device tensors (kv4_assign_into).
     """
